@@ -1,4 +1,4 @@
-"""Python binding of libmoe's C ABI (include/moe.h), by ctypes.
+"""Python binding of libmoe's C ABI (include/moe.h, include/moe_serve.h), by ctypes.
 
 Argument marshalling only: every function here has the name of a C entry
 point, checks nothing the library does not check itself, passes torch CUDA
@@ -8,7 +8,8 @@ library's HIP kernels; there is no other code path. Importing this module on a
 machine without the built library raises ImportError.
 
 ``MoEStage`` chains the calls of one forward and one backward pass, holding
-the buffers (torch is used for device memory only).
+the buffers (torch is used for device memory only); ``ServingStage`` holds
+those of the inference forward and picks the call for a batch's size.
 """
 from __future__ import annotations
 
@@ -101,6 +102,15 @@ _SIGS = {
     "moe_lora_gemm_down_dgrad_dy": ([moe_shape, ctypes.c_int32] + [_P] * 10 + [ctypes.c_size_t, _P], ctypes.c_int),
     "moe_lora_grads_unmerged_gathered": ([moe_shape, ctypes.c_int32] + [_P] * 14 + [ctypes.c_size_t, _P],
                                          ctypes.c_int),
+    "moe_quantize_fp8_block_rows": ([ctypes.c_int32, ctypes.c_int32] + [_P] * 4, ctypes.c_int),
+    "moe_quantize_fp8_block_weights": ([ctypes.c_int32] * 3 + [_P] * 4, ctypes.c_int),
+    "moe_gemm_fp8_block": ([ctypes.c_int32] * 4 + [_P] * 8, ctypes.c_int),
+    "moe_gemm_gate_up_fp8_block": ([moe_shape] + [_P] * 11, ctypes.c_int),
+    "moe_experts_fp8_block": ([moe_shape] + [_P] * 22 + [ctypes.c_size_t, _P], ctypes.c_int),
+    "moe_forward_fused_fp8_block": ([moe_shape] + [_P] * 25 + [ctypes.c_size_t, _P], ctypes.c_int),
+    "moe_few_workspace_bytes": ([moe_shape], ctypes.c_size_t),
+    "moe_forward_few": ([moe_shape] + [_P] * 11 + [ctypes.c_size_t, _P], ctypes.c_int),
+    "moe_forward_few_fp8_block": ([moe_shape] + [_P] * 14 + [ctypes.c_size_t, _P], ctypes.c_int),
 }
 for _name, (_args, _ret) in _SIGS.items():
     _fn = getattr(lib, _name)
@@ -722,6 +732,144 @@ class MoEStage:
         moe_unpermute_sum(s, b["dx_perm"], b["flat_to_sorted"], b["dx"], stream)
         moe_route_bwd(s, b["d_topk_w"], b["topk_w"], b["topk_idx"], b["d_logits"], stream)
         return b["dx"]
+
+
+# ---- Serving (include/moe_serve.h) -------------------------------------------
+
+
+def moe_quantize_fp8_block_rows(rows, K, x, q, scale, stream=None):
+    _check("moe_quantize_fp8_block_rows", lib.moe_quantize_fp8_block_rows(
+        int(rows), int(K), _ptr(x), _ptr(q), _ptr(scale), _stream(stream)))
+
+
+def moe_quantize_fp8_block_weights(E, N, K, w, q, scale, stream=None):
+    _check("moe_quantize_fp8_block_weights", lib.moe_quantize_fp8_block_weights(
+        int(E), int(N), int(K), _ptr(w), _ptr(q), _ptr(scale), _stream(stream)))
+
+
+def moe_gemm_fp8_block(M, E, N, K, aq, a_scale, offsets, wq, w_scale, row_weight, out, stream=None):
+    """offsets None: one expert (E == 1), every row; row_weight None: 1."""
+    _check("moe_gemm_fp8_block", lib.moe_gemm_fp8_block(
+        int(M), int(E), int(N), int(K), _ptr(aq), _ptr(a_scale), _ptr(offsets), _ptr(wq), _ptr(w_scale),
+        _ptr(row_weight), _ptr(out), _stream(stream)))
+
+
+def moe_gemm_gate_up_fp8_block(s, xq, x_scale, row_token, offsets, wq_gate, w_gate_scale, wq_up, w_up_scale, aq,
+                               a_scale, stream=None):
+    args = (xq, x_scale, row_token, offsets, wq_gate, w_gate_scale, wq_up, w_up_scale, aq, a_scale)
+    _check("moe_gemm_gate_up_fp8_block", lib.moe_gemm_gate_up_fp8_block(s, *[_ptr(t) for t in args], _stream(stream)))
+
+
+def moe_experts_fp8_block(s, x, topk_idx, topk_w, wq_gate, w_gate_scale, wq_up, w_up_scale, wq_down, w_down_scale,
+                          counts, offsets, sorted_to_flat, flat_to_sorted, row_token, row_weight, xq, x_scale, aq,
+                          a_scale, o_perm, y, ws, ws_bytes=None, stream=None):
+    args = (x, topk_idx, topk_w, wq_gate, w_gate_scale, wq_up, w_up_scale, wq_down, w_down_scale, counts, offsets,
+            sorted_to_flat, flat_to_sorted, row_token, row_weight, xq, x_scale, aq, a_scale, o_perm, y, ws)
+    _check("moe_experts_fp8_block", lib.moe_experts_fp8_block(s, *[_ptr(t) for t in args], _nbytes(ws, ws_bytes),
+                                                              _stream(stream)))
+
+
+def moe_forward_fused_fp8_block(s, x, w_router, logit_bias, wq_gate, w_gate_scale, wq_up, w_up_scale, wq_down,
+                                w_down_scale, logits, topk_idx, topk_w, counts, offsets, sorted_to_flat,
+                                flat_to_sorted, row_token, row_weight, xq, x_scale, aq, a_scale, o_perm, y, ws,
+                                ws_bytes=None, stream=None):
+    args = (x, w_router, logit_bias, wq_gate, w_gate_scale, wq_up, w_up_scale, wq_down, w_down_scale, logits, topk_idx,
+            topk_w, counts, offsets, sorted_to_flat, flat_to_sorted, row_token, row_weight, xq, x_scale, aq, a_scale,
+            o_perm, y, ws)
+    _check("moe_forward_fused_fp8_block", lib.moe_forward_fused_fp8_block(
+        s, *[_ptr(t) for t in args], _nbytes(ws, ws_bytes), _stream(stream)))
+
+
+def moe_few_workspace_bytes(s: moe_shape) -> int:
+    return int(lib.moe_few_workspace_bytes(s))
+
+
+def moe_forward_few(s, x, w_router, logit_bias, w_gate, w_up, w_down, logits, topk_idx, topk_w, y, ws, ws_bytes=None,
+                    stream=None):
+    args = (x, w_router, logit_bias, w_gate, w_up, w_down, logits, topk_idx, topk_w, y, ws)
+    _check("moe_forward_few", lib.moe_forward_few(s, *[_ptr(t) for t in args], _nbytes(ws, ws_bytes), _stream(stream)))
+
+
+def moe_forward_few_fp8_block(s, x, w_router, logit_bias, wq_gate, w_gate_scale, wq_up, w_up_scale, wq_down,
+                              w_down_scale, logits, topk_idx, topk_w, y, ws, ws_bytes=None, stream=None):
+    args = (x, w_router, logit_bias, wq_gate, w_gate_scale, wq_up, w_up_scale, wq_down, w_down_scale, logits, topk_idx,
+            topk_w, y, ws)
+    _check("moe_forward_few_fp8_block", lib.moe_forward_few_fp8_block(
+        s, *[_ptr(t) for t in args], _nbytes(ws, ws_bytes), _stream(stream)))
+
+
+class FP8BlockWeights:
+    """Expert weights in E4M3 with a float32 scale per 128 x 128 block: codes
+    gate/up [E,I,H], down [E,H,I] (uint8) and their scales. From bf16 weights
+    (moe_quantize_fp8_block_weights), or, with ``stored``, a checkpoint's own
+    (codes, scales) pairs as they are."""
+
+    def __init__(self, w_gate=None, w_up=None, w_down=None, stream=None, stored=None):
+        def quant(w):
+            E, N, K = w.shape
+            q = torch.empty(E, N, K, dtype=torch.uint8, device=w.device)
+            scale = torch.empty(E, -(-N // 128), -(-K // 128), dtype=torch.float32, device=w.device)
+            moe_quantize_fp8_block_weights(E, N, K, w, q, scale, stream=stream)
+            return q, scale
+
+        self.gate, self.up, self.down = stored if stored is not None else (quant(w_gate), quant(w_up), quant(w_down))
+
+
+class ServingStage:
+    """Buffers and call choice of one MoE layer's inference forward.
+
+    ``weights``: (w_gate, w_up, w_down) in bf16, or FP8BlockWeights. Holds the
+    buffers for up to ``max_T`` tokens on the weights' device. ``forward(x)``
+    runs the few-token layer (moe_forward_few, moe_forward_few_fp8_block) for
+    batches it takes (at most 64 tokens, k <= 16), and moe_forward_fused or
+    moe_forward_fused_fp8_block for the others; it returns y [T,H], a view of
+    a held buffer (overwritten by the next call), and leaves topk_idx and
+    topk_w in ``buf``. Calls of one stage share its workspaces: enqueue them
+    on one stream, or order the streams.
+    """
+
+    def __init__(self, max_T: int, k: int, w_router, weights, logit_bias=None):
+        self.w_router, self.logit_bias, self.k, self.max_T = w_router, logit_bias, k, max_T
+        self.block = isinstance(weights, FP8BlockWeights)
+        self.w = (*weights.gate, *weights.up, *weights.down) if self.block else tuple(weights)
+        self.E, self.I, self.H = self.w[0].shape
+        E, I, H, T, M, dev = self.E, self.I, self.H, max_T, max_T * k, self.w[0].device
+        i32, u8, bf16 = torch.int32, torch.uint8, torch.bfloat16
+        e = lambda *sz, dt=torch.float32: torch.empty(*sz, dtype=dt, device=dev)  # noqa: E731
+        self.buf: Dict[str, torch.Tensor] = {"logits": e(T, E), "topk_idx": e(T, k, dt=i32), "topk_w": e(T, k),
+                                             "y": e(T, H, dt=bf16)}
+        few = moe_few_workspace_bytes(shape(min(T, 64), H, E, k, I, bf16))
+        self.few_T = min(T, 64) if few else 0
+        self.few_ws = e(few, dt=u8) if few else None
+        if self.few_T < T:
+            ws = moe_workspace_bytes(shape(T, H, E, k, I, bf16))
+            if ws == 0:
+                raise MoEError("moe_workspace_bytes", 1, "shape rejected")
+            self.ws = e(ws, dt=u8)
+            self.buf.update({"counts": e(E, dt=i32), "offsets": e(E + 1, dt=i32), "sorted_to_flat": e(M, dt=i32),
+                             "flat_to_sorted": e(M, dt=i32), "row_token": e(M, dt=i32), "row_weight": e(M)})
+            if self.block:
+                self.buf.update({"xq": e(T, H, dt=u8), "x_scale": e(T, -(-H // 128)), "aq": e(M, I, dt=u8),
+                                 "a_scale": e(M, -(-I // 128))})
+            else:
+                self.buf["a"] = e(M, I, dt=bf16)
+            self.buf["o_perm"] = e(M, H, dt=bf16)
+
+    def forward(self, x, stream=None):
+        T, b = x.shape[0], self.buf
+        if T > self.max_T:
+            raise ValueError(f"{T} tokens; the stage holds buffers for {self.max_T}")
+        s = shape(T, self.H, self.E, self.k, self.I, torch.bfloat16)
+        y = b["y"][:T]
+        if T <= self.few_T:
+            fn = moe_forward_few_fp8_block if self.block else moe_forward_few
+            fn(s, x, self.w_router, self.logit_bias, *self.w, b["logits"], b["topk_idx"], b["topk_w"], y, self.few_ws,
+               stream=stream)
+        else:
+            fn = moe_forward_fused_fp8_block if self.block else moe_forward_fused
+            fn(s, x, self.w_router, self.logit_bias, *self.w, *[t for n, t in b.items() if n != "y"], y, self.ws,
+               stream=stream)
+        return y
 
 
 LORA_NAMES = ("a_gate", "b_gate", "a_up", "b_up", "a_down", "b_down")

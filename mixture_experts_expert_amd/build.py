@@ -21,7 +21,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmoe.so")
 
 SOURCES = ["api.hip", "route.hip", "permute.hip", "combine.hip", "fp8.hip", "mxfp4.hip", "lora.hip", "gemm_f32.hip",
-           "gemm_bf16.hip"]
+           "gemm_bf16.hip", "fp8_block.hip", "gemm_fp8_block.hip", "few.hip", "api_serve.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 CFLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",

@@ -1,0 +1,590 @@
+// Grouped products of E4M3 operands with one fp32 scale per block of 128:
+// activations 1 x 128, weights 128 x 128.
+//
+//   out[p,n] = sum over blocks b of sa[p,b] sw[n/128,b] (sum_{k in b} a[p,k] w[n,k])
+//
+// The scales are not powers of two, so the matrix core cannot apply them: one
+// v_mfma_f32_16x16x128_f8f6f4 covers exactly one block of k, and its partial
+// product goes into the fp32 accumulators with one fma per element. With the
+// weights as the A operand a lane's four results belong to one row of a, so
+// the block's factor sa * sw is one register per 16 rows, and the fmas take
+// half the matrix core's time on the vector units beside it.
+//
+// Two kernels:
+//
+// block_tile_kernel, for experts with many rows: a persistent workgroup of 8
+// wavefronts (two per SIMD, so that one's fmas run under the other's
+// products) on BM x 256 tiles, 2 x 4 wavefronts of BM/2 x 64. Operands go
+// from memory straight into LDS (two stages of one 128-wide k-step; the next
+// step, or the next tile's first one, loads while this one is multiplied).
+// A row's 128 bytes are eight 16-byte chunks, XOR-swizzled by row so that a
+// 16-lane read touches every bank once. Which weight row sits at which LDS row
+// is chosen so that a lane ends with consecutive output columns: 16 of the
+// plain product, 8 each of gate and up.
+//
+// block_stream_kernel, for experts with few rows: bound by the weights' bytes.
+// Weights go from memory into registers several steps ahead, up to 64 rows of
+// a per pass; with few workgroups of work the reduction is split over the
+// wavefronts of one, and the parts meet in LDS in a fixed order.
+//
+// The gate/up forms end with a = silu(g) u quantised: a workgroup holds whole
+// 1 x 128 blocks of a, whose maxima meet in LDS.
+#include <type_traits>
+
+#include "moe_internal.h"
+
+namespace moe {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+
+constexpr int kThreads = 512;
+constexpr int kWaves = kThreads / kWave;
+constexpr int KS = 128;                     // k per step: one scale block
+constexpr uint32_t kOutside = 0x80000000u;  // past every buffer's range: loads read zeros
+
+struct Params {
+  int M, E, N, K, KB, NB;   // KB, NB: blocks of the reduction and of the weight rows
+  int arows;                // rows of a behind row_token
+  const int32_t* offsets;
+  const int32_t* row_token;
+  const uint8_t *a, *w0, *w1;
+  const float *sa, *sw0, *sw1;
+  const float* row_weight;
+  bf16_t* out;
+  uint8_t* aq;
+  float* sout;
+};
+
+__device__ __forceinline__ rsrc_t make_rsrc(const void* base, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), static_cast<short>(0), static_cast<int>(bytes),
+                                           0x00020000);
+}
+
+__device__ __forceinline__ i32x8 join(const u32x4& lo, const u32x4& hi) {
+  return i32x8{static_cast<int>(lo.x), static_cast<int>(lo.y), static_cast<int>(lo.z), static_cast<int>(lo.w),
+               static_cast<int>(hi.x), static_cast<int>(hi.y), static_cast<int>(hi.z), static_cast<int>(hi.w)};
+}
+
+// The unscaled E4M3 x E4M3 product of one block.
+__device__ __forceinline__ f32x4 block_product(const i32x8& w, const i32x8& a) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, f32x4{}, 0, 0, 0, 0, 0, 0);
+}
+
+__device__ __forceinline__ float lane_value(float v, int src) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), src));
+}
+
+// silu(g) u with the hardware exponential and reciprocal (about 1 ulp each;
+// the result is rounded to 8 bits).
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.4426950408889634f)) * u;
+}
+
+// 448 / amax (0 for amax = 0), and the power of two that keeps it finite for
+// blocks below 2^-64.
+__device__ __forceinline__ float code_factor(float amax, float& up) {
+  up = amax < 0x1p-64f ? 0x1p64f : 1.0f;
+  return amax > 0.0f ? 448.0f / (amax * up) : 0.0f;
+}
+
+// The largest magnitude rounds to at most one ulp past 448: clamped, because
+// the conversion turns values past the range into NaN. NaN stays NaN.
+__device__ __forceinline__ float to_code_range(float v, float up, float r) {
+  const float t = v * up * r;
+  return t == t ? __builtin_amdgcn_fmed3f(t, -448.0f, 448.0f) : t;
+}
+
+__device__ __forceinline__ uint32_t codes4(const float (&v)[4], float up, float r) {
+  float t[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) t[i] = to_code_range(v[i], up, r);
+  int q = 0;
+  q = __builtin_amdgcn_cvt_pk_fp8_f32(t[0], t[1], q, false);
+  q = __builtin_amdgcn_cvt_pk_fp8_f32(t[2], t[3], q, true);
+  return static_cast<uint32_t>(q);
+}
+
+// ---- many rows per expert ---------------------------------------------------
+
+constexpr int BN = 256;
+
+// GU: N columns of each of w0 and w1 (128 per tile), else N of w0 (256 per tile).
+template <bool GU, int BM>
+__global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P) {
+  constexpr int FM = BM / 32;            // 16-row tiles of a per wavefront
+  constexpr int NA = BM / 64;            // load instructions of a per wavefront and step
+  constexpr int OB = BM * KS, OS = OB + BN * KS;
+  constexpr int TN = GU ? BN / 2 : BN;
+  __shared__ __attribute__((aligned(1024))) uint8_t st0[OS + BM * 4];
+  __shared__ __attribute__((aligned(1024))) uint8_t st1[OS + BM * 4];
+  __shared__ int tstart[1025];
+  __shared__ int eoff[1025];
+  __shared__ int wsum[kWaves];
+  __shared__ float amax[GU ? BM : 1][4];
+
+  const int tid = threadIdx.x;
+  const int lane_id = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 2, wn = wave & 3;
+  const int E = P.E, K = P.K, KB = P.KB;
+
+  // tstart[e]: row tiles of the experts before e (two experts per thread).
+  {
+    int c[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int e = 2 * tid + i;
+      const int b = e < E && P.offsets ? P.offsets[e] : 0;
+      const int t = e < E ? (P.offsets ? P.offsets[e + 1] : P.M) : 0;
+      c[i] = e < E ? (t - b + BM - 1) / BM : 0;
+      if (e < E) eoff[e] = b;
+      if (e == E - 1) eoff[E] = t;
+    }
+    const int mine = c[0] + c[1];
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+      const int v = __shfl_up(incl, o, kWave);
+      if (lane_id >= o) incl += v;
+    }
+    if (lane_id == kWave - 1) wsum[wave] = incl;
+    __syncthreads();
+    int at = incl - mine;
+    for (int w = 0; w < wave; ++w) at += wsum[w];
+    if (2 * tid < E) tstart[2 * tid] = at;
+    if (2 * tid + 1 < E) tstart[2 * tid + 1] = at + c[0];
+    if (tid == kThreads - 1) tstart[E] = at + mine;
+    __syncthreads();
+  }
+  const int ntn = (P.N + TN - 1) / TN;
+  const int total = tstart[E] * ntn;
+  // Eighths of the tile list per XCD, neighbouring tiles on one XCD.
+  const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3, nslots = gridDim.x >> 3;
+  const int lo = static_cast<int>(static_cast<int64_t>(total) * xcd / 8);
+  const int hi = static_cast<int>(static_cast<int64_t>(total) * (xcd + 1) / 8);
+  const int steps = KB, padded = (steps + 1) & ~1;
+  const int tail = K - (steps - 1) * KS;  // k of the last step
+
+  // Load state of the tile whose steps are being loaded, and the copy that
+  // the multiplications and the epilogue use.
+  int e = 0, row0 = 0, mvalid = 0, n0 = 0;
+  uint32_t aoff[NA], boff[4], soff = kOutside;
+  float swg = 0.0f, swu = 0.0f;          // lane l: the weight scales of step l (of the current 64)
+  auto set_tile = [&](int L) __attribute__((always_inline)) {
+    int l = 0, h = E - 1;
+    while (l < h) {
+      const int mid = (l + h + 1) >> 1;
+      if (tstart[mid] * ntn <= L) l = mid; else h = mid - 1;
+    }
+    const int rem = L - tstart[l] * ntn, mte = tstart[l + 1] - tstart[l];
+    const int nt = rem / mte, mt = rem - nt * mte;
+    const int64_t cnt = eoff[l + 1] - eoff[l];  // the expert's rows, evenly over its tiles
+    const int r0 = static_cast<int>(mt * cnt / mte);
+    e = __builtin_amdgcn_readfirstlane(l);
+    row0 = __builtin_amdgcn_readfirstlane(eoff[l] + r0);
+    mvalid = __builtin_amdgcn_readfirstlane(static_cast<int>((mt + 1) * cnt / mte) - r0);
+    n0 = __builtin_amdgcn_readfirstlane(nt * TN);
+    int lane = lane_id;  // opaque: the lane terms are recomputed here, not kept alive
+    asm volatile("" : "+v"(lane));
+#pragma unroll
+    for (int t = 0; t < NA; ++t) {
+      const int r = (wave * NA + t) * 8 + (lane >> 3);
+      const int c = (lane & 7) ^ ((r >> 1) & 7);
+      const int row = GU ? (r < mvalid ? P.row_token[row0 + r] : 0) : r;
+      aoff[t] = r < mvalid ? static_cast<uint32_t>(row) * K + c * 16 : kOutside;
+    }
+    if (wave < BM / 64) {
+      const int r = wave * 64 + lane;
+      const int row = GU ? (r < mvalid ? P.row_token[row0 + r] : 0) : r;
+      soff = r < mvalid ? static_cast<uint32_t>(row) * KB * 4 : kOutside;
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const int r = (wave * 4 + t) * 8 + (lane >> 3);
+      const int c = (lane & 7) ^ ((r >> 1) & 7);
+      const int j = (r >> 4) & 3, q = r & 15;
+      const int n = GU ? n0 + (r >> 6) * 32 + 8 * (q >> 2) + 4 * (j & 1) + (q & 3)
+                       : n0 + (r >> 6) * 64 + 16 * (q >> 2) + 4 * j + (q & 3);
+      boff[t] = n < P.N ? static_cast<uint32_t>(n) * K + c * 16 : kOutside;
+    }
+  };
+  // Load instruction v of step s into stage S: a rows, weight rows, scales.
+  constexpr int LOADS = NA + 5;
+  rsrc_t ra, rb, rs;
+  auto set_step = [&](int s) __attribute__((always_inline)) {
+    const int64_t k0 = static_cast<int64_t>(s) * KS;
+    if constexpr (GU) {
+      ra = make_rsrc(P.a + k0, static_cast<int64_t>(P.arows) * K - k0);
+      rs = make_rsrc(P.sa + s, (static_cast<int64_t>(P.arows) * KB - s) * 4);
+      rb = make_rsrc(((wave & 1) ? P.w1 : P.w0) + static_cast<int64_t>(e) * P.N * K + k0,
+                     static_cast<int64_t>(P.N) * K - k0);
+    } else {
+      ra = make_rsrc(P.a + static_cast<int64_t>(row0) * K + k0, static_cast<int64_t>(mvalid) * K - k0);
+      rs = make_rsrc(P.sa + static_cast<int64_t>(row0) * KB + s, (static_cast<int64_t>(mvalid) * KB - s) * 4);
+      rb = make_rsrc(P.w0 + static_cast<int64_t>(e) * P.N * K + k0, static_cast<int64_t>(P.N) * K - k0);
+    }
+  };
+  auto load = [&](int v, int s, uint8_t* S) __attribute__((always_inline)) {
+    typedef __attribute__((address_space(3))) void* lds_ptr;
+    if (v == LOADS - 1) {
+      if (wave < BM / 64) __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)(S + OS + wave * 256), 4, soff, 0, 0, 0);
+      return;
+    }
+    const bool is_a = v < NA;
+    const int blk = is_a ? wave * NA + v : wave * 4 + (v - NA);
+    uint32_t off = is_a ? aoff[v < NA ? v : 0] : boff[v < NA ? 0 : v - NA];
+    if (s == steps - 1 && tail != KS) {  // chunks past the row's end read zeros
+      const int r = blk * 8 + (lane_id >> 3);
+      if (((lane_id & 7) ^ ((r >> 1) & 7)) * 16 >= tail) off = kOutside;
+    }
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(is_a ? ra : rb, (lds_ptr)(S + (is_a ? 0 : OB) + blk * 1024), 16, off, 0, 0,
+                                             0);
+  };
+
+  f32x4 acc[FM][4];
+  int nv = 0;  // this wavefront's 16-row tiles that hold rows
+  // One step on stage C; the loads of step sn (of the load state's tile) into
+  // stage D meanwhile.
+  auto step = [&](auto fullc, const uint8_t* C, uint8_t* D, bool live, bool loads, int s, int sn)
+                  __attribute__((always_inline)) {
+    constexpr bool FULL = decltype(fullc)::value;
+    if (loads) set_step(sn);
+    int lane = lane_id;
+    asm volatile("" : "+v"(lane));
+    const int g2 = 2 * (lane >> 4), q = lane & 15;
+    i32x8 wf[4];
+    if (live) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = wn * 64 + j * 16 + q;
+        const uint8_t* p = C + OB + r * KS;
+        const int o = (g2 ^ ((r >> 1) & 7)) << 4;
+        wf[j] = join(*reinterpret_cast<const u32x4*>(p + o), *reinterpret_cast<const u32x4*>(p + (o ^ 16)));
+      }
+    }
+    const float fg = lane_value(swg, s & 63), fu = GU ? lane_value(swu, s & 63) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      if (live && (FULL || i < nv)) {
+        const int r = wm * (BM / 2) + i * 16 + q;
+        const uint8_t* p = C + r * KS;
+        const int o = (g2 ^ ((r >> 1) & 7)) << 4;
+        const i32x8 af = join(*reinterpret_cast<const u32x4*>(p + o), *reinterpret_cast<const u32x4*>(p + (o ^ 16)));
+        const float sr = *reinterpret_cast<const float*>(C + OS + r * 4);
+        const float s0 = sr * fg, s1 = GU ? sr * fu : s0;
+        f32x4 pr[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) pr[j] = block_product(wf[j], af);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) acc[i][j][x] = fmaf(j < 2 ? s0 : s1, pr[j][x], acc[i][j][x]);
+      }
+      if (loads) {
+        load(i, sn, D);
+        if (i == FM - 1)
+#pragma unroll
+          for (int v = FM; v < LOADS; ++v) load(v, sn, D);
+      }
+    }
+  };
+  auto landed = [&]() __attribute__((always_inline)) {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  auto weight_scales = [&](int we, int wn0, int s) __attribute__((always_inline)) {
+    const int b = min(s + lane_id, KB - 1);
+    const int nb = GU ? wn0 / 128 : min(wn0 + (wn >> 1) * 128, P.N - 1) / 128;
+    const int64_t at = (static_cast<int64_t>(we) * P.NB + nb) * KB + b;
+    swg = P.sw0[at];
+    if constexpr (GU) swu = P.sw1[at];
+  };
+
+  int L = lo + slot;
+  if (L >= hi) return;
+  set_tile(L);
+  set_step(0);
+#pragma unroll
+  for (int v = 0; v < LOADS; ++v) load(v, 0, st0);
+  landed();
+  while (L < hi) {
+    const int ce = e, crow0 = row0, cvalid = mvalid, cn0 = n0;
+    const int next = L + nslots;
+    nv = min(max((cvalid - wm * (BM / 2) + 15) / 16, 0), FM);
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
+    for (int s = 0; s < padded; s += 2) {
+      if ((s & 63) == 0) weight_scales(ce, cn0, s);
+      const bool odd = s + 1 < steps;  // the second step exists
+      const bool last = s + 2 >= padded;
+      if (nv == FM) step(std::true_type{}, st0, st1, true, odd, s, s + 1);
+      else step(std::false_type{}, st0, st1, true, odd, s, s + 1);
+      landed();
+      if (last && next < hi) set_tile(next);
+      const bool more = !last || next < hi;
+      if (nv == FM) step(std::true_type{}, st1, st0, odd, more, s + 1, last ? 0 : s + 2);
+      else step(std::false_type{}, st1, st0, odd, more, s + 1, last ? 0 : s + 2);
+      if (!last) landed();
+    }
+    // ---- epilogue
+    const int lane = lane_id, g = lane >> 4, q = lane & 15;
+    if constexpr (GU) {
+      const int NBo = (P.N + 127) / 128;
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        float m = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float v = silu_mul(acc[i][j][x], acc[i][j + 2][x]);
+            acc[i][j][x] = v;
+            m = fmaxf(m, fabsf(v));
+          }
+        m = fmaxf(m, __shfl_xor(m, 16, kWave));
+        m = fmaxf(m, __shfl_xor(m, 32, kWave));
+        if (g == 0) amax[wm * (BM / 2) + i * 16 + q][wn] = m;
+      }
+      landed();
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const int r = wm * (BM / 2) + i * 16 + q;
+        if (r >= cvalid) continue;
+        const float m = fmaxf(fmaxf(amax[r][0], amax[r][1]), fmaxf(amax[r][2], amax[r][3]));
+        float up;
+        const float f = code_factor(m, up);
+        const int n = cn0 + wn * 32 + 8 * g;
+        const int64_t p = crow0 + r;
+        if (n < P.N) {
+          const float v0[4] = {acc[i][0][0], acc[i][0][1], acc[i][0][2], acc[i][0][3]};
+          const float v1[4] = {acc[i][1][0], acc[i][1][1], acc[i][1][2], acc[i][1][3]};
+          *reinterpret_cast<uint2*>(P.aq + p * P.N + n) = make_uint2(codes4(v0, up, f), codes4(v1, up, f));
+        }
+        if (wn == 0 && g == 0) P.sout[p * NBo + cn0 / 128] = m / 448.0f;
+      }
+    } else {
+      landed();
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const int r = wm * (BM / 2) + i * 16 + q;
+        if (r >= cvalid) continue;
+        const int64_t p = crow0 + r;
+        const float w = P.row_weight ? P.row_weight[p] : 1.0f;
+        const int n = cn0 + wn * 64 + 16 * g;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (n + 8 * h >= P.N) continue;
+          const f32x4 u = acc[i][2 * h], v = acc[i][2 * h + 1];
+          *reinterpret_cast<uint4*>(P.out + p * P.N + n + 8 * h) =
+              make_uint4(pack_bf16x2(w * u[0], w * u[1]), pack_bf16x2(w * u[2], w * u[3]),
+                         pack_bf16x2(w * v[0], w * v[1]), pack_bf16x2(w * v[2], w * v[3]));
+        }
+      }
+    }
+    L = next;
+  }
+}
+
+// ---- few rows per expert ----------------------------------------------------
+
+constexpr int kTiles = 4;  // 16-row tiles of a per pass over the weights
+
+// One workgroup: expert e, and 16 columns per wavefront of w0 and w1 (GU), or
+// (kWaves / ks) * 16 columns of w0, each split over ks wavefronts along k.
+template <bool GU, int AHEAD>
+__global__ __launch_bounds__(kThreads, 2) void block_stream_kernel(const Params P, int ks, int groups) {
+  __shared__ __attribute__((aligned(16))) float red[kWaves][16][20];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int q = lane & 15, g = lane >> 4;
+  const int e = blockIdx.x / groups, grp = blockIdx.x - e * groups;
+  const int first = P.offsets ? P.offsets[e] : 0;
+  const int rows = (P.offsets ? P.offsets[e + 1] : P.M) - first;
+  if (rows <= 0) return;
+  const int K = P.K, KB = P.KB, N = P.N;
+  const int cw = GU ? wave : wave / ks, kp = GU ? 0 : wave - cw * ks;
+  const int n0 = (grp * (GU ? kWaves : kWaves / ks) + cw) * 16;
+  const int s0 = kp * KB / ks, s1 = (kp + 1) * KB / ks;
+  const int64_t wbytes = static_cast<int64_t>(N) * K;
+  const rsrc_t r0 = make_rsrc(P.w0 + e * wbytes, wbytes);
+  const rsrc_t r1 = make_rsrc((GU ? P.w1 : P.w0) + e * wbytes, wbytes);
+  const uint32_t woff = n0 + q < N ? static_cast<uint32_t>(n0 + q) * K : kOutside;
+  const int64_t srow = (static_cast<int64_t>(e) * P.NB + min(n0, N - 1) / 128) * KB;
+  auto chunk = [&](const rsrc_t& r, uint32_t row, int s) -> i32x8 {
+    const int k = s * KS + 32 * g;
+    const u32x4 lo = __builtin_amdgcn_raw_buffer_load_b128(r, row != kOutside && k < K ? row + k : kOutside, 0, 0);
+    const u32x4 hi =
+        __builtin_amdgcn_raw_buffer_load_b128(r, row != kOutside && k + 16 < K ? row + k + 16 : kOutside, 0, 0);
+    return join(lo, hi);
+  };
+  for (int p0 = 0; p0 < rows; p0 += 16 * kTiles) {
+    i32x8 w0[AHEAD], w1[AHEAD];
+#pragma unroll
+    for (int d = 0; d < AHEAD; ++d)
+      if (s0 + d < s1) {
+        w0[d] = chunk(r0, woff, s0 + d);
+        if constexpr (GU) w1[d] = chunk(r1, woff, s0 + d);
+      }
+    const int tiles = min(kTiles, (rows - p0 + 15) / 16);
+    const int64_t base = GU ? 0 : first + p0;
+    const int64_t left = GU ? P.arows : rows - p0;
+    const rsrc_t ra = make_rsrc(P.a + base * K, min(left, static_cast<int64_t>(GU ? P.arows : 16 * kTiles)) * K);
+    const float* sa = P.sa + base * KB;
+    uint32_t aoff[kTiles];
+    int arow[kTiles];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      const int r = p0 + 16 * t + q;
+      const bool in = r < rows;
+      arow[t] = in ? (GU ? P.row_token[first + r] : r - p0) : 0;
+      aoff[t] = in ? static_cast<uint32_t>(arow[t]) * K : kOutside;
+    }
+    float sw0 = 0.0f, sw1 = 0.0f;
+    f32x4 a0[kTiles], a1[kTiles];
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) a0[t] = a1[t] = f32x4{};
+    for (int s = s0; s < s1; s += AHEAD) {
+      if ((s - s0) % 64 == 0) {
+        const int b = min(s + lane, KB - 1);
+        sw0 = P.sw0[srow + b];
+        if constexpr (GU) sw1 = P.sw1[srow + b];
+      }
+      i32x8 af[AHEAD];
+      float sf[AHEAD];
+#pragma unroll
+      for (int d = 0; d < AHEAD; ++d)
+        if (s + d < s1) {
+          af[d] = chunk(ra, aoff[0], s + d);
+          sf[d] = sa[static_cast<int64_t>(arow[0]) * KB + s + d];
+        }
+#pragma unroll
+      for (int d = 0; d < AHEAD; ++d) {
+        if (s + d >= s1) break;
+        const float f0 = lane_value(sw0, (s + d - s0) % 64), f1 = GU ? lane_value(sw1, (s + d - s0) % 64) : 0.0f;
+#pragma unroll
+        for (int t = 0; t < kTiles; ++t) {
+          if (t >= tiles) break;
+          const i32x8 x = t == 0 ? af[d] : chunk(ra, aoff[t], s + d);
+          const float sr = t == 0 ? sf[d] : sa[static_cast<int64_t>(arow[t]) * KB + s + d];
+          const f32x4 m0 = block_product(w0[d], x);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a0[t][i] = fmaf(sr * f0, m0[i], a0[t][i]);
+          if constexpr (GU) {
+            const f32x4 m1 = block_product(w1[d], x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) a1[t][i] = fmaf(sr * f1, m1[i], a1[t][i]);
+          }
+        }
+        if (s + d + AHEAD < s1) {
+          w0[d] = chunk(r0, woff, s + d + AHEAD);
+          if constexpr (GU) w1[d] = chunk(r1, woff, s + d + AHEAD);
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t) {
+      if (t >= tiles) break;
+      const int r = p0 + 16 * t + q;
+      const int n = n0 + 4 * g;
+      const int64_t p = first + r;
+      if constexpr (GU) {
+        float v[4], m = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[i] = silu_mul(a0[t][i], a1[t][i]);
+          m = fmaxf(m, fabsf(v[i]));
+        }
+        m = fmaxf(m, __shfl_xor(m, 16, kWave));
+        m = fmaxf(m, __shfl_xor(m, 32, kWave));
+        __syncthreads();  // the previous tile's maxima are read
+        if (g == 0) red[wave][q][0] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) m = fmaxf(m, red[w][q][0]);
+        float up;
+        const float f = code_factor(m, up);
+        if (r < rows) {
+          if (n < N) *reinterpret_cast<uint32_t*>(P.aq + p * N + n) = codes4(v, up, f);
+          if (wave == 0 && g == 0) P.sout[p * ((N + 127) / 128) + grp] = m / 448.0f;
+        }
+      } else {
+        f32x4 v = a0[t];
+        if (ks > 1) {  // the parts along k, in order
+          __syncthreads();
+          *reinterpret_cast<f32x4*>(&red[wave][q][4 * g]) = v;
+          __syncthreads();
+          if (kp != 0) continue;
+          for (int w = 1; w < ks; ++w) {
+            const f32x4 o = *reinterpret_cast<const f32x4*>(&red[wave + w][q][4 * g]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += o[i];
+          }
+        }
+        if (r < rows && n < N) {
+          const float w = P.row_weight ? P.row_weight[p] : 1.0f;
+          *reinterpret_cast<uint2*>(P.out + p * N + n) =
+              make_uint2(pack_bf16x2(w * v[0], w * v[1]), pack_bf16x2(w * v[2], w * v[3]));
+        }
+      }
+    }
+  }
+}
+
+template <bool GU>
+hipError_t launch(const BlockGemmArgs& a, hipStream_t st) {
+  Params P{};
+  P.M = a.M;
+  P.E = a.E;
+  P.N = a.N;
+  P.K = a.K;
+  P.KB = ceil_div(a.K, 128);
+  P.NB = ceil_div(a.N, 128);
+  P.arows = a.arows;
+  P.offsets = a.offsets;
+  P.row_token = a.row_token;
+  P.a = a.a;
+  P.w0 = a.w0;
+  P.w1 = a.w1;
+  P.sa = a.a_scale;
+  P.sw0 = a.w0_scale;
+  P.sw1 = a.w1_scale;
+  P.row_weight = a.row_weight;
+  P.out = static_cast<bf16_t*>(a.out);
+  P.aq = a.aq;
+  P.sout = a.a_out_scale;
+  const unsigned grid = static_cast<unsigned>(gemm_grid());
+  // Rows per expert, on average: up to 32 the weights' bytes bound the
+  // product; beyond 96, 256-row tiles waste less than they save.
+  const int64_t avg = (a.M + a.E - 1) / a.E;
+  if (avg <= 32) {
+    // Enough workgroups to fill the device: split the reduction when there
+    // are too few columns.
+    int ks = 1;
+    if (!GU)
+      while (ks < kWaves && static_cast<int64_t>(a.E) * ceil_div(a.N, 16 * kWaves / ks) < 2 * grid && ks < P.KB) ks *= 2;
+    const int groups = ceil_div(a.N, 16 * kWaves / ks);
+    block_stream_kernel<GU, 4><<<static_cast<unsigned>(a.E) * groups, kThreads, 0, st>>>(P, ks, groups);
+  } else if (avg <= 96) {
+    block_tile_kernel<GU, 128><<<grid, kThreads, 0, st>>>(P);
+  } else {
+    block_tile_kernel<GU, 256><<<grid, kThreads, 0, st>>>(P);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gemm_fp8_block(const BlockGemmArgs& a, hipStream_t st) {
+  if (a.M == 0) return hipSuccess;
+  return a.w1 != nullptr ? launch<true>(a, st) : launch<false>(a, st);
+}
+
+}  // namespace moe

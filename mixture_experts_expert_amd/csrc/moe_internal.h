@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "moe.h"
+#include "moe_serve.h"
 
 namespace moe {
 
@@ -251,5 +252,52 @@ hipError_t launch_lora_prepare(const moe_shape& s, int r, float scale, const Lor
 hipError_t launch_lora_project(const moe_shape& s, int r, int which, const void* in, const int32_t* offsets,
                                void* ws, hipStream_t st, const int32_t* tok = nullptr, const float* rw = nullptr);
 hipError_t launch_lora_outer(const moe_shape& s, int r, const LoraArgs& g, void* ws, hipStream_t st);
+
+// ---- Serving operators (moe_serve.h) ----------------------------------------
+
+// Block-scaled quantisers (fp8_block.hip): E4M3 codes and fp32 scales amax /
+// 448 per 1 x 128 (rows) or 128 x 128 (stacked weights) block.
+hipError_t launch_quantize_fp8_block_rows(int rows, int K, const void* in, uint8_t* q, float* scale, hipStream_t st);
+hipError_t launch_quantize_fp8_block_weights(int E, int N, int K, const void* w, uint8_t* q, float* scale,
+                                             hipStream_t st);
+
+// Grouped products of block-scaled operands (gemm_fp8_block.hip). Plain:
+// out [M][N] = bf16(row_weight (a w0^T)). Gate/up (w1 set): N columns of each
+// of w0 and w1, rows of a through row_token, and silu(g) u quantised to aq
+// [M][N] with scales a_out_scale [M][ceil(N/128)].
+struct BlockGemmArgs {
+  int M, E, N, K;
+  int arows;               // rows of a (M, or those behind row_token)
+  const uint8_t* a;
+  const float* a_scale;
+  const int32_t* row_token;
+  const int32_t* offsets;  // NULL: one expert, every row
+  const uint8_t *w0, *w1;
+  const float *w0_scale, *w1_scale;
+  const float* row_weight;
+  void* out;
+  uint8_t* aq;
+  float* a_out_scale;
+};
+hipError_t launch_gemm_fp8_block(const BlockGemmArgs& a, hipStream_t st);
+
+// The whole layer for a few tokens (few.hip).
+constexpr int kFewMaxT = 64, kFewMaxK = 16;
+struct FewLayout {  // byte offsets in the workspace; the counters come first
+  int counters, groups;
+  size_t act, part, total;
+};
+FewLayout few_layout(const moe_shape& s);
+struct FewArgs {
+  const void *x, *w_router;
+  const float* bias;
+  const void *w_gate, *w_up, *w_down;  // bf16, or E4M3 codes with the scales
+  const float *gate_scale, *up_scale, *down_scale;
+  float* logits;
+  int32_t* topk_idx;
+  float* topk_w;
+  void* y;
+};
+hipError_t launch_few(const moe_shape& s, const FewArgs& a, void* ws, hipStream_t st);
 
 }  // namespace moe

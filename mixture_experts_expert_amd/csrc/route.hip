@@ -17,6 +17,7 @@
 // A block covers 64 tokens x 32 experts (four wavefronts of eight experts);
 // at T = 8192, E = 128 the grid gives every SIMD two wavefronts.
 #include "moe_internal.h"
+#include "select.h"
 
 namespace moe {
 namespace {
@@ -279,51 +280,10 @@ __global__ __launch_bounds__(kWave* kTokPerBlock) void router_topk_kernel(int Tn
 
 // The top-k for E <= 256 and k <= 16: one token per 16-lane DPP row (four
 // per wavefront), NC logits per lane (e = n + 16 c), every cross-lane step a
-// DPP move. A selection key orders (logit, index) as `before` does: the
-// logit's order bits (NaN lowest; -0 counted as +0, so equal logits tie on the
-// index) above the complement of the index. Taken and absent slots hold 0,
-// below every key, so one unsigned max per round picks the next expert.
+// DPP move (select.h). Taken and absent slots hold key 0, below every key, so
+// one unsigned max per round picks the next expert.
 constexpr int kRowTopkThreads = 256;
 constexpr int kRowTok = kRowTopkThreads / 16;  // tokens per block
-
-__device__ __forceinline__ uint64_t sel_key(float v, int e) {
-  const float c = v + 0.0f;  // -0 -> +0
-  const uint32_t b = __float_as_uint(c);
-  const uint32_t o = (c != c) ? 0u : ((b & 0x80000000u) ? ~b : (b | 0x80000000u));
-  return (static_cast<uint64_t>(o) << 32) | static_cast<uint32_t>(~e);
-}
-
-__device__ __forceinline__ float key_value(uint64_t key) {
-  const uint32_t o = static_cast<uint32_t>(key >> 32);
-  return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);  // o = 0: a NaN
-}
-
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp32(uint32_t v) {
-  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(0, static_cast<int>(v), CTRL, 0xF, 0xF, false));
-}
-
-// Quad swaps (quad_perm [1,0,3,2] and [2,3,0,1]), then half-row and row
-// mirrors: every lane of a 16-lane row ends with the row's maximum (or sum).
-__device__ __forceinline__ uint64_t row_max_key(uint64_t k) {
-#define RM_STEP(CTRL)                                                                                      \
-  {                                                                                                        \
-    const uint64_t o = (static_cast<uint64_t>(dpp32<CTRL>(static_cast<uint32_t>(k >> 32))) << 32) |       \
-                       dpp32<CTRL>(static_cast<uint32_t>(k));                                              \
-    k = o > k ? o : k;                                                                                     \
-  }
-  RM_STEP(0xB1) RM_STEP(0x4E) RM_STEP(0x141) RM_STEP(0x140)
-#undef RM_STEP
-  return k;
-}
-
-__device__ __forceinline__ float row_sum(float v) {
-  v += __uint_as_float(dpp32<0xB1>(__float_as_uint(v)));
-  v += __uint_as_float(dpp32<0x4E>(__float_as_uint(v)));
-  v += __uint_as_float(dpp32<0x141>(__float_as_uint(v)));
-  v += __uint_as_float(dpp32<0x140>(__float_as_uint(v)));
-  return v;
-}
 
 template <int NC>
 __global__ __launch_bounds__(kRowTopkThreads) void router_topk_row_kernel(int Tn, int E, int k,
