@@ -17,39 +17,48 @@
 //   few_kernel: one persistent workgroup of 8 wavefronts per CU. Each selects
 //     the experts of all tokens for itself (no third launch), then takes
 //     units by ticket:
-//     - gate/up unit: one expert, 8 F columns of gate and of up. The reduction
-//       is split over the 8 wavefronts; the partial sums meet in LDS, and
-//       a = bf16(w silu(g) u) goes to the workspace per (token, slot).
-//     - down unit: one group of experts, 16 F columns of y. The (expert, k)
+//     - gate/up unit: one expert, 8 columns (8 rows of W_gate and 8 of W_up).
+//       The reduction is split over the 8 wavefronts, so each token row's part
+//       is loaded by one of them (wavefronts that work side by side on one
+//       expert's columns wait for each other's pending lines in the vector
+//       cache: 300 instead of 165 us for 64 tokens' gate and up). The partial
+//       sums meet in LDS; a = bf16(w silu(g) u) goes to the workspace.
+//     - down unit: one group of experts, 16 columns of y. The (expert, k)
 //       steps are split over the wavefronts, each adding its experts' products
 //       into its own y tile in LDS; the eight tiles are then summed in order.
 //       With one group (up to 8 experts) that is y; otherwise the groups'
 //       fp32 partial sums go to the workspace and the last workgroup to
 //       finish a column block adds them in group order.
+//     A wavefront's loads run two batches of steps ahead of its products and
+//     on into the next units; nothing in that stream is conditional (a step
+//     that does not exist reads out of range, which costs nothing), since only
+//     then do the compiler's waits leave the newer loads running.
 //
-// Order and progress: tickets come from 16 counters, 8 for gate/up and 8 for
-// down (one counter would serialise the first 256 tickets, about 10 ns each).
-// A workgroup starts at its own XCD's counter, and takes a down ticket only
-// once all 8 gate/up counters have run out. A down unit waits for its group's
-// gate/up units; by then running workgroups hold all of those, and gate/up
-// units wait for nothing: the wait ends whatever else occupies the device.
-// (If another call overwrites the workspace, against the interface, the wait
-// gives up after two seconds.)
+// Order and progress: the gate/up units come in as many shares as there are
+// workgroups; a workgroup claims one at its start, and another whenever it is
+// done, as long as one is left (eight counters, one per XCD, each first asked
+// by its own workgroups). It goes on to the down units only once all shares
+// are claimed. A down unit waits for its group's gate/up units; by then
+// running workgroups hold all of those, and gate/up units wait for nothing:
+// the wait ends whatever else occupies the device. (If another call
+// overwrites the workspace, against the interface, the wait gives up after
+// two seconds.) Claiming unit by unit instead stalls the loads: an atomic's
+// answer comes back behind all loads issued before it.
 //
-// Tile: v_mfma_f32_16x16x32_bf16 with the weights as A (16 rows; a gate/up
-// fragment with F = 1 is 8 rows of gate and 8 of up) and up to 16 token rows
-// as B, so a lane's four results are four consecutive columns of one row. A
-// step is 64 k: lane group g = lane / 16 takes k 16 g .. 16 g + 15 of it (the
-// first 8 in one product, the others in the next; any assignment of k to
-// lanes serves as long as both operands share it), so a row's 128 bytes are
-// read together. E4M3 weights are widened to bf16 (exact) in registers and
-// each step's partial product is multiplied by its block's scale in fp32.
-//
-// In flight: 64 to 128 KB per CU. Twice that is slower (measured with two
-// workgroups per CU: 64 instead of 43 us for one token at the 30B shape), as
-// the units' stores and counters then queue behind everyone's weights.
+// Tile: v_mfma_f32_16x16x32_bf16 with the weights as A (16 rows) and up to 16
+// token rows as B, so a lane's four results are four consecutive columns of
+// one row. A step is 128 bytes of each weight row: 64 bf16 or 128 E4M3 codes
+// (one scale block; a last half block reads zeros). Loads take a row's 128
+// bytes with eight neighbouring lanes (a load in the product's own layout,
+// neighbouring lanes in different rows, costs the address unit 64 cycles
+// instead of 16), and the steps change layout through LDS of the wavefront's
+// own, weights and token rows alike: no barrier, and the registers stay the
+// prefetch buffer. E4M3 weights are widened to bf16 (exact) and each step's
+// product is multiplied by its block's scale in fp32.
 #include "moe_internal.h"
 #include "select.h"
+
+#include <type_traits>
 
 namespace moe {
 namespace {
@@ -57,19 +66,21 @@ namespace {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kBf16 = 0, kFp8 = 1;  // weight formats
 constexpr int kNW = 8;              // wavefronts per workgroup
 constexpr int kThreads = kNW * kWave;
-constexpr int kStep = 64;           // k per step
-constexpr int kLists = 8;           // ticket counters per phase, one per XCD
+constexpr int kGC = 8, kDC = 16;   // columns per gate/up and per down unit
+constexpr int kLists = 8;           // counters of claimed shares, one per XCD
 constexpr int kLine = 32;           // counters that workgroups add to lie 128 bytes apart
 constexpr int kMaxPairs = kFewMaxT * kFewMaxK;
+constexpr uint32_t kNoRow = 0x80000000u;  // an offset past every row, whatever is added to it
 constexpr uint64_t kSpinTicks = 200000000;  // two seconds of the 100 MHz clock
 
-// The workspace's counters (uint32, in lines): [0, 8) gate/up tickets, [8, 16)
-// down tickets, then gate/up tiles done per group; after the lines, down units
-// done per column block.
+// The workspace's counters (uint32, in lines): [0, 8) gate/up shares claimed,
+// then gate/up tiles done per group; after the lines, down units done per
+// column block.
 struct FewParams {
   int T, H, E, k, I;
   const bf16_t* x;
@@ -149,57 +160,70 @@ __global__ __launch_bounds__(kWave) void few_router_kernel(int T, int H, int E, 
 
 // ---- the layer --------------------------------------------------------------
 
-// 16 weight rows' share of one step, in the lane that multiplies it.
-template <int FMT> struct Frag;
-template <> struct Frag<kBf16> {
-  uint4 v[2];
-  // p: this lane's row, at k = 16 g of step 0
-  __device__ __forceinline__ void load(const void* p, int s) {
-    const uint4* q = reinterpret_cast<const uint4*>(static_cast<const bf16_t*>(p) + s * kStep);
-    v[0] = q[0];
-    v[1] = q[1];
-  }
-  __device__ __forceinline__ bf16x8 half(int h) const { return __builtin_bit_cast(bf16x8, v[h]); }
-};
-template <> struct Frag<kFp8> {
-  uint4 v;
-  __device__ __forceinline__ void load(const void* p, int s) {
-    v = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p) + s * kStep);
-  }
-  __device__ __forceinline__ bf16x8 half(int h) const {
-    const uint32_t a = h ? v.z : v.x, b = h ? v.w : v.y;
-    const bf16x2 r0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false);
-    const bf16x2 r1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true);
-    const bf16x2 r2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false);
-    const bf16x2 r3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true);
-    return bf16x8{r0.x, r0.y, r1.x, r1.y, r2.x, r2.y, r3.x, r3.y};
-  }
-};
-
-struct Rows {  // a token row's share of one step
-  uint4 v[2];
-  __device__ __forceinline__ void load(const bf16_t* p, int s) {
-    const uint4* q = reinterpret_cast<const uint4*>(p + s * kStep);
-    v[0] = q[0];
-    v[1] = q[1];
-  }
-  __device__ __forceinline__ void load(const rsrc_t& r, uint32_t off, int s) {  // another workgroup's row
-    const uint32_t o = off + static_cast<uint32_t>(s) * (kStep * 2);
-    v[0] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, o, 0, kDeviceScope));
-    v[1] = __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(r, o + 16, 0, kDeviceScope));
-  }
-  __device__ __forceinline__ bf16x8 half(int h) const { return __builtin_bit_cast(bf16x8, v[h]); }
-};
-
-// acc += (scale) W rows x token rows over one step.
+// One step in registers as loaded: 16 weight rows x 128 bytes, lane l the
+// 16-byte chunk l % 8 of rows l / 8 and 8 + l / 8; and up to 16 token rows x
+// the same k (kXL lanes per row, kXN loads).
+template <int FMT> constexpr int kStep = FMT == kBf16 ? 64 : 128;   // k per step
+template <int FMT> constexpr int kXL = FMT == kBf16 ? 8 : 16;
+template <int FMT> constexpr int kXN = kXL<FMT> / 4;
 template <int FMT>
-__device__ __forceinline__ void multiply(f32x4& acc, const Frag<FMT>& w, const Rows& r, float scale) {
+struct Step {
+  u32x4 w[2];
+  u32x4 x[kXN<FMT>];
+};
+
+// The wavefront's LDS for one step: weight rows, then token rows, chunks
+// swizzled by row so that both sides touch every bank once.
+template <int FMT> constexpr int kStepBytes = 2048 + kXL<FMT> * 256;
+__device__ __forceinline__ int w_slot(int row, int chunk) { return row * 128 + ((chunk ^ ((row >> 1) & 7)) << 4); }
+template <int FMT>
+__device__ __forceinline__ int x_slot(int row, int chunk) {
+  return 2048 + row * (kXL<FMT> * 16) + ((chunk ^ (FMT == kBf16 ? (row >> 1) & 7 : row)) << 4);
+}
+
+__device__ __forceinline__ bf16x8 widen8(uint32_t a, uint32_t b) {  // eight E4M3 codes
+  const bf16x2 r0 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, false);
+  const bf16x2 r1 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 1.0f, true);
+  const bf16x2 r2 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, false);
+  const bf16x2 r3 = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 1.0f, true);
+  return bf16x8{r0.x, r0.y, r1.x, r1.y, r2.x, r2.y, r3.x, r3.y};
+}
+
+template <int FMT>
+__device__ __forceinline__ void put_w(char* lds, const Step<FMT>& s) {
+  const int lane = threadIdx.x % kWave, row = lane / 8, chunk = lane % 8;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4*>(lds + w_slot(row + 8 * i, chunk)) = s.w[i];
+}
+template <int FMT>
+__device__ __forceinline__ void put_x(char* lds, const u32x4 (&x)[kXN<FMT>]) {
+  constexpr int RPI = kWave / kXL<FMT>;  // rows per load
+  const int lane = threadIdx.x % kWave, row = lane / kXL<FMT>, chunk = lane % kXL<FMT>;
+#pragma unroll
+  for (int i = 0; i < kXN<FMT>; ++i) *reinterpret_cast<u32x4*>(lds + x_slot<FMT>(row + RPI * i, chunk)) = x[i];
+}
+
+// acc += (scale) weight rows x token rows over the step in LDS.
+template <int FMT>
+__device__ __forceinline__ void multiply(f32x4& acc, const char* lds, float scale) {
+  const int lane = threadIdx.x % kWave, row = lane % 16, g = lane / 16;
+  auto at = [&](int o) { return *reinterpret_cast<const u32x4*>(lds + o); };
   if constexpr (FMT == kBf16) {
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.half(0), r.half(0), acc, 0, 0, 0);
-    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.half(1), r.half(1), acc, 0, 0, 0);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const u32x4 w = at(w_slot(row, 4 * h + g)), x = at(x_slot<FMT>(row, 4 * h + g));
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, x), acc,
+                                                    0, 0, 0);
+    }
   } else {
-    f32x4 p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.half(0), r.half(0), f32x4{}, 0, 0, 0);
-    p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.half(1), r.half(1), p, 0, 0, 0);
+    f32x4 p = f32x4{};
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const u32x4 w = at(w_slot(row, 4 * h + g));
+      const u32x4 x0 = at(x_slot<FMT>(row, 2 * (4 * h + g))), x1 = at(x_slot<FMT>(row, 2 * (4 * h + g) + 1));
+      p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(w.x, w.y), __builtin_bit_cast(bf16x8, x0), p, 0, 0, 0);
+      p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(widen8(w.z, w.w), __builtin_bit_cast(bf16x8, x1), p, 0, 0, 0);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[i] = fmaf(scale, p[i], acc[i]);
   }
@@ -211,24 +235,25 @@ __device__ __forceinline__ float lane_value(float v, int src) {
 
 struct FewLists {  // in LDS: the pairs (token, slot) sorted by expert
   int na;                          // experts that some token selected
-  int unit;                        // the next unit
+  int share;                       // the next share of gate/up units
   int last;
   uint16_t expert[1024];           // active expert a -> expert
   uint16_t start[1025];            // its pairs: list[start[a] .. start[a + 1])
   uint16_t list[kMaxPairs];        // pair t * k + j
+  uint16_t token[kMaxPairs];       // t, by place in the list
   float weight[kMaxPairs];         // by pair
 };
 
-// Scratch, reused by the phases of a unit.
-template <int TILES, int F>
+// Scratch: the selection's, then the units'.
+template <int TILES>
 union FewScratch {
   struct {
     uint16_t sel[kMaxPairs];       // expert of each pair
     int count[1024];               // pairs per expert, then a cursor
     int wave_sum[kNW];
   } lists;
-  float red[TILES][kNW][16][16 * F + 4];      // gate/up: [tile][wave][row][gate columns, up columns]
-  float tile[kNW][16 * TILES][16 * F + 4];    // down: [wave][token][column]
+  float red[2][TILES][kNW][16][20];      // gate/up, by turns: [row tile][wave][row][8 gate, 8 up columns]
+  float tile[kNW][16 * TILES][kDC + 4];  // down: [wave][token][column]
 };
 
 // Barrier for LDS traffic: unlike __syncthreads it leaves loads in flight.
@@ -390,8 +415,8 @@ __device__ __forceinline__ void few_select_waves(const FewParams& P, FewLists& L
 // The experts of all tokens, and the lists of the pairs by expert. A row's
 // place in its expert's list changes no result: every row is summed on its
 // own, a token's experts in expert order.
-template <int TILES, int F, int NC>
-__device__ __forceinline__ void few_select(const FewParams& P, FewLists& L, FewScratch<TILES, F>& S) {
+template <int TILES, int NC>
+__device__ __forceinline__ void few_select(const FewParams& P, FewLists& L, FewScratch<TILES>& S) {
   const int tid = threadIdx.x, lane = tid % kWave;
   const int E = P.E, pairs = P.T * P.k;
   if constexpr (TILES == 1) few_select_waves<(NC + 3) / 4>(P, L, S);
@@ -411,6 +436,7 @@ __device__ __forceinline__ void few_select(const FewParams& P, FewLists& L, FewS
       for (int i = 0; i < pairs; ++i) a += __builtin_amdgcn_readlane(mine, i) < mine && (firsts >> i & 1);
       if (lane < pairs) {
         L.list[at] = static_cast<uint16_t>(lane);
+        L.token[at] = static_cast<uint16_t>(lane / P.k);
         if (!repeat) {
           L.expert[a] = static_cast<uint16_t>(mine);
           L.start[a] = static_cast<uint16_t>(at);
@@ -461,8 +487,11 @@ __device__ __forceinline__ void few_select(const FewParams& P, FewLists& L, FewS
     L.start[a] = static_cast<uint16_t>(p);
   }
   __syncthreads();
-  for (int q = tid; q < pairs; q += kThreads)
-    L.list[atomicAdd(&S.lists.count[S.lists.sel[q]], 1)] = static_cast<uint16_t>(q);
+  for (int q = tid; q < pairs; q += kThreads) {
+    const int at = atomicAdd(&S.lists.count[S.lists.sel[q]], 1);
+    L.list[at] = static_cast<uint16_t>(q);
+    L.token[at] = static_cast<uint16_t>(q / P.k);
+  }
   __syncthreads();
 }
 
@@ -470,157 +499,367 @@ __device__ __forceinline__ void few_select(const FewParams& P, FewLists& L, FewS
 // and no partial sums; beyond 64, groups of 16 halve the partial sums.
 __host__ __device__ __forceinline__ int few_group(int na) { return na > 64 ? 16 : 8; }
 
-// Tickets (thread 0). list_size: units u = list, list + 8, ... below n.
-__device__ __forceinline__ int list_size(int n, int list) { return (n - list + kLists - 1) / kLists; }
+// Claims of gate/up shares, handled by wavefront 0 (lane 0 claims, lanes 0 to
+// 7 look at the counters). Counter l hands out shares l, l + 8, ..., n of them
+// in all.
+struct Claims {
+  int list;          // the counter that is asked
+  uint32_t ticket;   // lane 0: its answer
+  uint32_t seen;     // lane l: counter l at that time
 
-struct Tickets {
-  int gu, down;    // units of each phase
-  int phase, list;
-  uint32_t ticket; // requested of the current list
-  __device__ __forceinline__ uint32_t* counter(const FewParams& P, int l) const {
-    return P.cnt + (phase * kLists + l) * kLine;
+  static __device__ __forceinline__ uint32_t add(uint32_t* c) {
+    uint32_t v = 0;
+    if (threadIdx.x % kWave == 0) v = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return v;
   }
+  static __device__ __forceinline__ int size(int n, int list) { return (n - list + kLists - 1) / kLists; }
   __device__ __forceinline__ void request(const FewParams& P) {
-    ticket = __hip_atomic_fetch_add(counter(P, list), 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    ticket = add(P.cnt + list * kLine);
+    const int l = threadIdx.x % kWave;
+    if (l < kLists) seen = __hip_atomic_load(P.cnt + l * kLine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
-  // The unit of the requested ticket: a gate/up unit, gu + a down unit, or -1.
-  // A list that has run out is left for one that still has units.
-  __device__ __forceinline__ int take(const FewParams& P) {
+  // The requested share, or -1 once all are claimed. A counter that has run
+  // out is left for one that had not at the last look.
+  __device__ __forceinline__ int take(const FewParams& P, int n) {
     for (;;) {
-      const int n = phase == 0 ? gu : down;
-      if (ticket < static_cast<uint32_t>(list_size(n, list))) return phase * gu + static_cast<int>(ticket) * kLists + list;
-      uint32_t c[kLists];
-#pragma unroll
-      for (int l = 0; l < kLists; ++l)
-        c[l] = __hip_atomic_load(counter(P, l), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      int next = -1;
-#pragma unroll
-      for (int l = kLists - 1; l >= 0; --l)
-        if (c[l] < static_cast<uint32_t>(list_size(n, l))) next = l;
-      if (next >= 0) {
-        list = next;
-      } else if (phase == 0) {
-        phase = 1;
-        list = blockIdx.x % kLists;
-      } else {
-        return -1;
-      }
+      const int t = __builtin_amdgcn_readfirstlane(min(ticket, 0x7fffffffu));
+      if (t < size(n, list)) return t * kLists + list;
+      const int l = threadIdx.x % kWave;
+      const uint64_t open = __ballot(l < kLists && l != list && seen < static_cast<uint32_t>(size(n, l)));
+      if (open == 0) return -1;
+      list = __builtin_ctzll(open);
       request(P);
     }
   }
 };
 
-// Waits until *p reaches `want` (one thread; the caller's barrier follows).
+// Waits until *p reaches `want`.
 __device__ __forceinline__ void wait_count(const uint32_t* p, uint32_t want) {
   const uint64_t t0 = __builtin_amdgcn_s_memrealtime();
   while (__hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < want) {
     if (__builtin_amdgcn_s_memrealtime() - t0 > kSpinTicks) break;
     __builtin_amdgcn_s_sleep(1);
   }
+  asm volatile("" ::: "memory");  // what follows is read after it
 }
 
-// TILES: 16-row tiles of one expert's tokens (one for T <= 16, else four); F:
-// weight fragments per step; AHEAD: steps of weights in flight per wavefront;
-// NC: logits per lane of a 16-lane row (E <= 16 NC).
-template <int FMT, int TILES, int F, int AHEAD, int NC>
+// TILES: 16-row tiles of one expert's tokens (one for T <= 16, else four); NB:
+// steps per batch (two batches are in flight per wavefront); NC: logits per
+// lane of a 16-lane row (E <= 16 NC).
+template <int FMT, int TILES, int NB, int NC>
 __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
-  constexpr int GC = 8 * F, DC = 16 * F;  // columns per gate/up and per down unit
   constexpr int ESZ = FMT == kBf16 ? 2 : 1;
+  constexpr int RPI = kWave / kXL<FMT>, XN = kXN<FMT>;
+  constexpr int kBatchLoads = NB * (2 + XN);
   __shared__ FewLists L;
-  __shared__ __attribute__((aligned(16))) FewScratch<TILES, F> S;
+  __shared__ __attribute__((aligned(16))) FewScratch<TILES> S;
+  __shared__ __attribute__((aligned(16))) char step_lds[kNW][kStepBytes<FMT>];
   const int tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int col = lane % 16, g = lane / 16;
+  const int wr = lane / 8, wc = lane % 8, xrow = lane / kXL<FMT>, xc = lane % kXL<FMT>;
   const int T = P.T, H = P.H, I = P.I, k = P.k;
+  char* lds = step_lds[wave];
 
-  Tickets tk{};
-  tk.list = blockIdx.x % kLists;
-  if (tid == 0) tk.request(P);
-  few_select<TILES, F, NC>(P, L, S);
+  const int shares = gridDim.x;
+  Claims claims{static_cast<int>(blockIdx.x % kLists), 0, 0};
+  if (wave == 0) claims.request(P);
+  few_select<TILES, NC>(P, L, S);
   const int na = L.na, size = few_group(na), ngrp = (na + size - 1) / size;
-  tk.gu = na * (I / GC);
-  tk.down = ngrp * (H / DC);
-  if (tid == 0) L.unit = tk.take(P);
-  __syncthreads();
+  const int gpe = I / kGC, dpg = H / kDC;  // gate/up units per expert, down units per group
+  const int hsteps = (H + kStep<FMT> - 1) / kStep<FMT>, spe = (I + kStep<FMT> - 1) / kStep<FMT>;
+  const bool hhalf = H % kStep<FMT> != 0, ihalf = I % kStep<FMT> != 0;
+  const int down = ngrp * dpg;
+  // The next share (barriers for all).
+  auto claim = [&]() {
+    if (wave == 0) {
+      const int share = claims.take(P, shares);
+      if (lane == 0) L.share = share;
+      if (share >= 0) claims.request(P);  // the one after, answered long before it is asked for
+    }
+    __syncthreads();
+    const int share = __builtin_amdgcn_readfirstlane(L.share);
+    lds_barrier();  // everyone has read it
+    return share;
+  };
 
-  // The stream of a unit's steps: this wavefront's steps q of [q0, q1), its
-  // weights in w and the first 16 rows' values in r, AHEAD steps deep. The
-  // load cursors (p, left, la for weights; pr for x) are ahead of the
-  // multiplications.
-  Frag<FMT> w[AHEAD][F];
-  Rows r[AHEAD];
-  const char* p[F];
-  const bf16_t* pr = nullptr;
-  int q0 = 0, q1 = 0, left = 0, la = 0;
-  float sa = 1.0f, sb = 1.0f;            // E4M3: lane l holds the scales of step l (of the current 64)
-  const int spe = I / kStep;             // down: steps per expert
-  const int gpe = I / GC, dpg = H / DC;  // gate/up units per expert, down units per group
-  const rsrc_t act = make_rsrc(P.act, static_cast<int64_t>(T) * k * I * 2);
-
-  auto load_w = [&](int d) __attribute__((always_inline)) {
+  const rsrc_t xs = make_rsrc(P.x, static_cast<int64_t>(T) * H * 2);
+  Step<FMT> st[2][NB];
+  float sa[2] = {1.0f, 1.0f}, sb[2] = {1.0f, 1.0f};  // E4M3: lane d, the scales of the batch's step d
+  f32x4 acc[TILES];
+  auto clear = [&]() __attribute__((always_inline)) {
 #pragma unroll
-    for (int f = 0; f < F; ++f) {
-      w[d][f].load(p[f], 0);
-      p[f] += kStep * ESZ;
+    for (int t = 0; t < TILES; ++t) acc[t] = f32x4{};
+  };
+  auto load_b128 = [&](auto scope, const rsrc_t& r, uint32_t off) __attribute__((always_inline)) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, decltype(scope)::value));
+  };
+  typedef std::integral_constant<int, 0> Cached;
+  typedef std::integral_constant<int, kDeviceScope> Fresh;
+
+  // ---- gate/up units: the steps [q0, q1) of each are this wavefront's
+  const int q0 = wave * hsteps / kNW, q1 = (wave + 1) * hsteps / kNW;
+  const int batches = ((hsteps + kNW - 1) / kNW + NB - 1) / NB;  // the same for all wavefronts
+  // Batch j of unit u into set B (u < 0: reads nothing).
+  auto fetch = [&](auto setc, int u, int j) __attribute__((always_inline)) {
+    constexpr int B = decltype(setc)::value;
+    const int v = max(u, 0), a = v / gpe, c = v - a * gpe, e = L.expert[a], first = L.start[a];
+    const int rows = u < 0 ? 0 : L.start[a + 1] - first;
+    const int64_t at = (static_cast<int64_t>(e) * I + c * kGC) * H * ESZ;
+    const rsrc_t r0 = make_rsrc(static_cast<const char*>(P.w0) + at, u < 0 ? 0 : kGC * H * ESZ);
+    const rsrc_t r1 = make_rsrc(static_cast<const char*>(P.w1) + at, u < 0 ? 0 : kGC * H * ESZ);
+    const uint32_t wo = static_cast<uint32_t>(wr) * H * ESZ + 16 * wc;
+    uint32_t xo[XN];
+#pragma unroll
+    for (int i = 0; i < XN; ++i) {
+      const int row = xrow + RPI * i;
+      xo[i] = row < rows ? static_cast<uint32_t>(L.token[first + row]) * H * 2 + 16 * xc : kNoRow;
+    }
+    const int qb = q0 + j * NB;
+#pragma unroll
+    for (int d = 0; d < NB; ++d) {
+      const int q = qb + d;
+      const bool half = hhalf && q == hsteps - 1;
+      const uint32_t wd = q >= q1 || (half && wc >= 4) ? kNoRow : wo + q * 128;
+      st[B][d].w[0] = load_b128(Cached{}, r0, wd);
+      st[B][d].w[1] = load_b128(Cached{}, r1, wd);
+      const uint32_t xd = q >= q1 || (half && xc >= kXL<FMT> / 2) ? kNoRow : static_cast<uint32_t>(q) * (2 * kStep<FMT>);
+#pragma unroll
+      for (int i = 0; i < XN; ++i) st[B][d].x[i] = load_b128(Cached{}, xs, (xd & kNoRow) | (xo[i] + xd));
+    }
+    if constexpr (FMT == kFp8) {
+      const int64_t sc = (static_cast<int64_t>(e) * ((I + 127) / 128) + c * kGC / 128) * hsteps +
+                         min(qb + lane % NB, hsteps - 1);
+      sa[B] = P.s0[sc];
+      sb[B] = P.s1[sc];
     }
   };
-  auto down_rows = [&](int c, int a) __attribute__((always_inline)) {  // weight rows of active expert a
+  // The products of batch j of unit u, in set B.
+  auto use = [&](auto setc, int u, int j) __attribute__((always_inline)) {
+    constexpr int B = decltype(setc)::value;
+    const int a = u / gpe, first = L.start[a], rows = L.start[a + 1] - first, tiles = (rows + 15) / 16;
 #pragma unroll
-    for (int f = 0; f < F; ++f)
-      p[f] = static_cast<const char*>(P.w2) +
-             ((static_cast<int64_t>(L.expert[a]) * H + c * DC + 16 * f + col) * I + 16 * g) * ESZ;
+    for (int d = 0; d < NB; ++d) {
+      float f = 1.0f;
+      if constexpr (FMT == kFp8) {
+        const float fg = lane_value(sa[B], d), fu = lane_value(sb[B], d);
+        f = lane < 32 ? fg : fu;  // result rows 8 .. 15 are up's
+      }
+      put_w<FMT>(lds, st[B][d]);
+      put_x<FMT>(lds, st[B][d].x);
+      multiply<FMT>(acc[0], lds, f);
+      if constexpr (TILES > 1) {
+        const int q = q0 + j * NB + d;
+        if (q < q1)
+          for (int t = 1; t < tiles; ++t) {
+            u32x4 x[XN];
+#pragma unroll
+            for (int i = 0; i < XN; ++i) {
+              const int row = 16 * t + xrow + RPI * i;
+              const bool dead = row >= rows || (hhalf && q == hsteps - 1 && xc >= kXL<FMT> / 2);
+              x[i] = load_b128(Cached{}, xs,
+                               dead ? kNoRow
+                                    : static_cast<uint32_t>(L.token[first + row]) * H * 2 + 16 * xc + q * (2 * kStep<FMT>));
+            }
+            put_x<FMT>(lds, x);
+            if (t == 1) multiply<FMT>(acc[1], lds, f);
+            else if (t == 2) multiply<FMT>(acc[2], lds, f);
+            else multiply<FMT>(acc[3], lds, f);
+          }
+      }
+    }
   };
-  // The finished unit: its partial results are in the scratch.
-  int fin = -1;
-  uint32_t* pending = nullptr;  // counter of a gate/up tile whose stores may still be under way
-  auto signal = [&]() __attribute__((always_inline)) {
-    if (pending != nullptr) {
-      stores_done();
-      if (lane == 0) __hip_atomic_fetch_add(pending, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  // A unit's end: the partial sums to LDS; wavefront t then sums row tile t,
+  // in wavefront order, two columns of a row per lane.
+  uint32_t* pending = nullptr;  // counter of a tile whose stores may still be under way
+  int turn = 0;
+  auto finish = [&](int u) __attribute__((always_inline)) {
+    const int a = u / gpe, c = u - a * gpe, first = L.start[a], rows = L.start[a + 1] - first, tiles = (rows + 15) / 16;
+    if (pending != nullptr) {  // older than the last batch's loads
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0x0F70 | (kBatchLoads & 15) | (kBatchLoads >> 4) << 14);  // vmcnt(kBatchLoads)
+      asm volatile("" ::: "memory");
+      Claims::add(pending);
       pending = nullptr;
     }
-  };
-  // A gate/up unit: wavefront t sums the partial products of row tile t, in
-  // wavefront order: 2 F columns of one row per lane.
-  auto finish_gate_up = [&](int v) __attribute__((always_inline)) {
-    const int a = v / gpe, c = v - a * gpe;
-    const int first = L.start[a], rows = L.start[a + 1] - first;
-    if (16 * wave >= rows) return;
-    const int row = lane / 4, c0 = 2 * F * (lane % 4);
-    float vg[2 * F], vu[2 * F];
 #pragma unroll
-    for (int i = 0; i < 2 * F; ++i) vg[i] = vu[i] = 0.0f;
+    for (int t = 0; t < TILES; ++t)
+      if (t < tiles) *reinterpret_cast<f32x4*>(&S.red[turn][t][wave][col][4 * g]) = acc[t];
+    lds_barrier();
+    if (wave < tiles) {
+      const int t = wave < TILES ? wave : 0, row = lane / 4, c0 = 2 * (lane % 4);
+      float2 vg = make_float2(0.0f, 0.0f), vu = vg;
 #pragma unroll
-    for (int x = 0; x < kNW; ++x)
-#pragma unroll
-      for (int i = 0; i < 2 * F; ++i) {
-        vg[i] += S.red[wave < TILES ? wave : 0][x][row][c0 + i];
-        vu[i] += S.red[wave < TILES ? wave : 0][x][row][GC + c0 + i];
+      for (int v = 0; v < kNW; ++v) {
+        const float2 x = *reinterpret_cast<const float2*>(&S.red[turn][t][v][row][c0]);
+        const float2 y = *reinterpret_cast<const float2*>(&S.red[turn][t][v][row][8 + c0]);
+        vg.x += x.x;
+        vg.y += x.y;
+        vu.x += y.x;
+        vu.y += y.y;
       }
-    if (16 * wave + row < rows) {
-      const int pair = L.list[first + 16 * wave + row];
-      const float pw = L.weight[pair];
-#pragma unroll
-      for (int i = 0; i < 2 * F; ++i) vg[i] = pw * (vg[i] * sigmoidf_dev(vg[i]) * vu[i]);
-      const int64_t at = static_cast<int64_t>(pair) * I + c * GC + c0;
-#pragma unroll
-      for (int i = 0; i < F; ++i)
-        __hip_atomic_store(reinterpret_cast<uint32_t*>(P.act + at + 2 * i), pack_bf16x2(vg[2 * i], vg[2 * i + 1]),
+      if (16 * t + row < rows) {
+        const int pair = L.list[first + 16 * t + row];
+        const float pw = L.weight[pair];
+        __hip_atomic_store(reinterpret_cast<uint32_t*>(P.act + static_cast<int64_t>(pair) * I + c * kGC + c0),
+                           pack_bf16x2(pw * (vg.x * sigmoidf_dev(vg.x) * vu.x), pw * (vg.y * sigmoidf_dev(vg.y) * vu.y)),
                            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      pending = P.cnt + (kLists + a / size) * kLine;
     }
-    pending = P.cnt + (2 * kLists + a / size) * kLine;
+    turn ^= 1;
   };
-  // A down unit: the wavefronts' tiles, in order.
-  auto finish_down = [&](int v) __attribute__((always_inline)) {
-    const int grp = (v - tk.gu) / dpg, c = v - tk.gu - grp * dpg;
-    for (int i = tid; i < T * DC / 2; i += kThreads) {
-      const int t = i / (DC / 2), h = 2 * (i % (DC / 2));
+  {
+    typedef std::integral_constant<int, 0> Set0;
+    typedef std::integral_constant<int, 1> Set1;
+    const int units = na * gpe;
+    for (int share = claim(); share >= 0; share = claim()) {
+      int u = share < units ? share : -1;
+      auto after = [&](int v) { return v >= 0 && v + shares < units ? v + shares : -1; };
+      int un = after(u);
+      fetch(Set0{}, u, 0);
+      if (batches > 1) fetch(Set1{}, u, 1);
+      else fetch(Set1{}, un, 0);
+      clear();
+      int j = 0;
+      auto turn_over = [&](auto setc) __attribute__((always_inline)) {
+        use(setc, u, j);
+        if (++j == batches) {
+          finish(u);
+          u = un;
+          un = after(u);
+          j = 0;
+          clear();
+        }
+        // The set just used takes the batch after the next: batch j + 1 of u,
+        // or the first of its successor.
+        const int f = j + 1;
+        fetch(setc, f < batches ? u : un, f < batches ? f : 0);
+      };
+      while (u >= 0) {
+        turn_over(Set0{});
+        if (u < 0) break;
+        turn_over(Set1{});
+      }
+    }
+    if (pending != nullptr) {  // before this workgroup waits for others
+      stores_done();
+      Claims::add(pending);
+    }
+  }
+
+  // ---- down units
+  __syncthreads();
+  const rsrc_t act = make_rsrc(P.act, static_cast<int64_t>(T) * k * I * 2);
+  for (int u = blockIdx.x; u < down; u += gridDim.x) {
+    const int grp = u / dpg, c = u - grp * dpg, a0 = grp * size, a_end = a0 + min(size, na - a0);
+    const int total = (a_end - a0) * spe, d0 = wave * total / kNW, d1 = (wave + 1) * total / kNW;
+    const int nb = (d1 - d0 + NB - 1) / NB;
+    const uint32_t wo = static_cast<uint32_t>(wr) * I * ESZ + 16 * wc;
+    // Weights of batch j into set B.
+    auto fetch_w = [&](auto setc, int j) __attribute__((always_inline)) {
+      constexpr int B = decltype(setc)::value;
+#pragma unroll
+      for (int d = 0; d < NB; ++d) {
+        const int q = min(d0 + j * NB + d, total - 1), a = q / spe, s = q - a * spe;
+        const rsrc_t r = make_rsrc(static_cast<const char*>(P.w2) +
+                                       (static_cast<int64_t>(L.expert[a0 + a]) * H + c * kDC) * I * ESZ,
+                                   d0 + j * NB + d < d1 ? kDC * I * ESZ : 0);
+        const uint32_t o = ihalf && s == spe - 1 && wc >= 4 ? kNoRow : wo + s * 128;
+        st[B][d].w[0] = load_b128(Cached{}, r, o);
+        st[B][d].w[1] = load_b128(Cached{}, r, o + 8 * I * ESZ);
+      }
+      if constexpr (FMT == kFp8) {
+        const int q = min(d0 + j * NB + lane % NB, total - 1);
+        sa[B] = P.s2[(static_cast<int64_t>(L.expert[a0 + q / spe]) * ((H + 127) / 128) + c * kDC / 128) * spe + q % spe];
+      }
+    };
+    // Activations of batch j, rows 16 t on, step d.
+    auto row_loads = [&](int j, int d, int t, u32x4(&x)[XN]) __attribute__((always_inline)) {
+      const int q = min(d0 + j * NB + d, total - 1), a = a0 + q / spe, s = q % spe;
+      const int f0 = L.start[a], n = d0 + j * NB + d < d1 ? L.start[a + 1] - f0 : 0;
+#pragma unroll
+      for (int i = 0; i < XN; ++i) {
+        const int row = 16 * t + xrow + RPI * i;
+        const bool dead = row >= n || (ihalf && s == spe - 1 && xc >= kXL<FMT> / 2);
+        x[i] = load_b128(Fresh{}, act,
+                         dead ? kNoRow : static_cast<uint32_t>(L.list[f0 + row]) * I * 2 + 16 * xc + s * (2 * kStep<FMT>));
+      }
+    };
+    auto fetch_x = [&](auto setc, int j) __attribute__((always_inline)) {
+      constexpr int B = decltype(setc)::value;
+#pragma unroll
+      for (int d = 0; d < NB; ++d) row_loads(j, d, 0, st[B][d].x);
+    };
+    float* tile = &S.tile[wave][0][0];
+    constexpr int TS = kDC + 4;
+    auto use_down = [&](auto setc, int j) __attribute__((always_inline)) {
+      constexpr int B = decltype(setc)::value;
+#pragma unroll
+      for (int d = 0; d < NB; ++d) {
+        const int q = d0 + j * NB + d;
+        if (q < d1) {
+          const int a = q / spe, s = q - a * spe, first = L.start[a0 + a], rows = L.start[a0 + a + 1] - first;
+          const int tiles = (rows + 15) / 16;
+          const float f = FMT == kFp8 ? lane_value(sa[B], d) : 1.0f;
+          put_w<FMT>(lds, st[B][d]);
+          put_x<FMT>(lds, st[B][d].x);
+          multiply<FMT>(acc[0], lds, f);
+          if constexpr (TILES > 1) {
+            for (int t = 1; t < tiles; ++t) {
+              u32x4 x[XN];
+              row_loads(j, d, t, x);
+              put_x<FMT>(lds, x);
+              if (t == 1) multiply<FMT>(acc[1], lds, f);
+              else if (t == 2) multiply<FMT>(acc[2], lds, f);
+              else multiply<FMT>(acc[3], lds, f);
+            }
+          }
+          if (s == spe - 1 || q + 1 == d1) {  // this expert's products into the tile, row by row
+#pragma unroll
+            for (int t = 0; t < TILES; ++t) {
+              if (t < tiles && 16 * t + col < rows) {
+                f32x4* to = reinterpret_cast<f32x4*>(tile + L.token[first + 16 * t + col] * TS + 4 * g);
+                f32x4 v = *to;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] += acc[t][i];
+                *to = v;
+              }
+            }
+            clear();
+          }
+        }
+      }
+    };
+    typedef std::integral_constant<int, 0> Set0;
+    typedef std::integral_constant<int, 1> Set1;
+    fetch_w(Set0{}, 0);
+    fetch_w(Set1{}, 1);
+    for (int i = lane; i < T * kDC; i += kWave) tile[i / kDC * TS + i % kDC] = 0.0f;
+    // The group's activations are there once all its tiles are counted.
+    uint32_t want = 0;
+    for (int a = a0; a < a_end; ++a) want += (L.start[a + 1] - L.start[a] + 15) / 16 * gpe;
+    wait_count(P.cnt + (kLists + grp) * kLine, want);
+    fetch_x(Set0{}, 0);
+    fetch_x(Set1{}, 1);
+    clear();
+    for (int j = 0; j < nb; j += 2) {
+      use_down(Set0{}, j);
+      fetch_w(Set0{}, j + 2);
+      fetch_x(Set0{}, j + 2);
+      use_down(Set1{}, j + 1);
+      fetch_w(Set1{}, j + 3);
+      fetch_x(Set1{}, j + 3);
+    }
+    lds_barrier();
+    for (int i = tid; i < T * kDC / 2; i += kThreads) {
+      const int t = i / (kDC / 2), h = 2 * (i % (kDC / 2));
       float v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
-      for (int x = 0; x < kNW; ++x) {
-        v0 += S.tile[x][t][h];
-        v1 += S.tile[x][t][h + 1];
+      for (int v = 0; v < kNW; ++v) {
+        v0 += S.tile[v][t][h];
+        v1 += S.tile[v][t][h + 1];
       }
-      const int64_t at = static_cast<int64_t>(t) * H + c * DC + h;
+      const int64_t at = static_cast<int64_t>(t) * H + c * kDC + h;
       if (ngrp == 1) {
         *reinterpret_cast<uint32_t*>(P.y + at) = pack_bf16x2(v0, v1);
       } else {
@@ -629,243 +868,37 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
                            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
     }
-    if (ngrp == 1) return;
-    stores_done();
-    lds_barrier();
-    if (tid == 0)
-      L.last = __hip_atomic_fetch_add(P.cnt_down + c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
-               static_cast<uint32_t>(ngrp) - 1;
-    lds_barrier();
-    if (!L.last) return;
-    for (int i = tid; i < T * DC / 2; i += kThreads) {
-      const int64_t at = static_cast<int64_t>(i / (DC / 2)) * H + c * DC + 2 * (i % (DC / 2));
-      float v0 = 0.0f, v1 = 0.0f;
-      for (int x = 0; x < ngrp; ++x) {
-        const uint64_t b =
-            __hip_atomic_load(reinterpret_cast<uint64_t*>(P.part + static_cast<int64_t>(x) * T * H + at),
-                              __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        v0 += __uint_as_float(static_cast<uint32_t>(b));
-        v1 += __uint_as_float(static_cast<uint32_t>(b >> 32));
-      }
-      *reinterpret_cast<uint32_t*>(P.y + at) = pack_bf16x2(v0, v1);
-    }
-  };
-
-  int u = __builtin_amdgcn_readfirstlane(L.unit);
-  for (;;) {
-    // First loads of unit u, then the finished unit's results.
-    const bool down = u >= tk.gu;
-    int first = 0, rows = 0, tiles = 0;  // the expert whose steps are multiplied
-    int grp = 0, c = 0, a0 = 0, a_end = 0;
-    auto scales = [&](int q) __attribute__((always_inline)) {
-      if constexpr (FMT == kFp8) {
-        if (!down) {
-          const int kb = (H + 127) / 128;
-          const int64_t at = (static_cast<int64_t>(L.expert[a0]) * ((I + 127) / 128) + c * GC / 128) * kb;
-          const int b = min((q + lane) / 2, kb - 1);
-          sa = P.s0[at + b];
-          sb = P.s1[at + b];
-        } else {
-          const int kb = (I + 127) / 128, s = min(q + lane, (a_end - a0) * spe - 1);
-          sa = P.s2[(static_cast<int64_t>(L.expert[a0 + s / spe]) * ((H + 127) / 128) + c * DC / 128) * kb +
-                    s % spe / 2];
-        }
-      }
-    };
-    // The next step's weights into slot d; a down unit's cursor moves on to
-    // the group's next expert.
-    auto load_down = [&](int d) __attribute__((always_inline)) {
-      load_w(d);
-      if (--left == 0) {
-        left = spe;
-        if (++la < a_end) down_rows(c, la);
-      }
-    };
-    auto load_gate_up = [&](int d) __attribute__((always_inline)) {
-      load_w(d);
-      r[d].load(pr, 0);
-      pr += kStep;
-    };
-    if (u >= 0 && !down) {
-      a0 = u / gpe;
-      c = u - a0 * gpe;
-      const int e = L.expert[a0], steps = H / kStep;
-      first = L.start[a0];
-      rows = L.start[a0 + 1] - first;
-      tiles = (rows + 15) / 16;
-      q0 = wave * steps / kNW;
-      q1 = (wave + 1) * steps / kNW;
-#pragma unroll
-      for (int f = 0; f < F; ++f) {  // F = 1: 8 rows of gate, 8 of up; F = 2: 16 of each
-        const bool up = F == 1 ? col >= 8 : f == 1;
-        const int n = c * GC + (F == 1 ? col % 8 : col);
-        p[f] = static_cast<const char*>(up ? P.w1 : P.w0) +
-               ((static_cast<int64_t>(e) * I + n) * H + q0 * kStep + 16 * g) * ESZ;
-      }
-      pr = P.x + static_cast<int64_t>(L.list[first + min(col, rows - 1)] / k) * H + q0 * kStep + 16 * g;
-#pragma unroll
-      for (int d = 0; d < AHEAD; ++d)
-        if (q0 + d < q1) load_gate_up(d);
-      scales(q0);
-    } else if (u >= 0) {
-      grp = (u - tk.gu) / dpg;
-      c = u - tk.gu - grp * dpg;
-      a0 = grp * size;
-      a_end = a0 + min(size, na - a0);
-      const int total = (a_end - a0) * spe;
-      q0 = wave * total / kNW;
-      q1 = (wave + 1) * total / kNW;
-      la = a0 + q0 / spe;
-      left = spe - q0 % spe;
-      if (q0 < q1) {
-        down_rows(c, la);
-#pragma unroll
-        for (int f = 0; f < F; ++f) p[f] += (q0 % spe) * kStep * ESZ;
-      }
-#pragma unroll
-      for (int d = 0; d < AHEAD; ++d)
-        if (q0 + d < q1) load_down(d);
-      scales(q0);
-    }
-    if (fin >= tk.gu) finish_down(fin);
-    else if (fin >= 0) finish_gate_up(fin);
-    if (u < 0) break;
-    if (tid == 0) tk.request(P);  // the next ticket travels while this unit is computed
-
-    f32x4 acc[TILES][F];
-#pragma unroll
-    for (int t = 0; t < TILES; ++t)
-#pragma unroll
-      for (int f = 0; f < F; ++f) acc[t][f] = f32x4{};
-    if (!down) {
-      for (int q = q0; q < q1; q += AHEAD) {
-        if (FMT == kFp8 && q > q0 && (q - q0) % 64 == 0) scales(q);
-#pragma unroll
-        for (int d = 0; d < AHEAD; ++d) {
-          if (q + d < q1) {
-            float fa = 1.0f, fb = 1.0f;
-            if constexpr (FMT == kFp8) {
-              fa = lane_value(sa, (q + d - q0) % 64);
-              fb = lane_value(sb, (q + d - q0) % 64);
-              if constexpr (F == 1) fa = g < 2 ? fa : fb;  // result rows 8 .. 15 are up's
-            }
-#pragma unroll
-            for (int t = 0; t < TILES; ++t) {
-              if (t < tiles) {
-                Rows x = r[d];
-                if (t > 0)
-                  x.load(P.x + static_cast<int64_t>(L.list[first + min(16 * t + col, rows - 1)] / k) * H + 16 * g,
-                         q + d);
-#pragma unroll
-                for (int f = 0; f < F; ++f) multiply<FMT>(acc[t][f], w[d][f], x, f == 0 ? fa : fb);
-              }
-            }
-            if (q + d + AHEAD < q1) load_gate_up(d);
-          }
-        }
-      }
-      signal();  // the previous unit's tile: its stores are older than the loads used above
-      lds_barrier();  // everyone is done with the scratch
-#pragma unroll
-      for (int t = 0; t < TILES; ++t)
-        if (t < tiles)
-#pragma unroll
-          for (int f = 0; f < F; ++f) *reinterpret_cast<f32x4*>(&S.red[t][wave][col][16 * f + 4 * g]) = acc[t][f];
-    } else {
-      float* tile = &S.tile[wave][0][0];
-      constexpr int TS = DC + 4;
-      signal();  // before this workgroup waits for others
-      lds_barrier();  // everyone is done with the scratch
-      for (int i = lane; i < T * DC; i += kWave) tile[i / DC * TS + i % DC] = 0.0f;
-      // The group's activations are there once all its tiles are counted.
-      if (tid == 0) {
-        uint32_t want = 0;
-        for (int a = a0; a < a_end; ++a) want += (L.start[a + 1] - L.start[a] + 15) / 16 * gpe;
-        wait_count(P.cnt + (2 * kLists + grp) * kLine, want);
-      }
+    if (ngrp > 1) {
+      stores_done();
       lds_barrier();
-      int ca = a0 + q0 / spe, cs = q0 % spe;
-      int ra = ca, rs = cs;  // row load cursor
-      uint32_t rr = 0;
-      auto row_at = [&](int a, int t) __attribute__((always_inline)) {
-        const int f0 = L.start[a], n = L.start[a + 1] - f0;
-        return (static_cast<uint32_t>(L.list[f0 + min(16 * t + col, n - 1)]) * I + 16 * g) * 2;
-      };
-      auto load_rows = [&](int d) __attribute__((always_inline)) {
-        r[d].load(act, rr, rs);
-        if (++rs == spe) {
-          rs = 0;
-          if (++ra < a_end) rr = row_at(ra, 0);
-        }
-      };
-      if (q0 < q1) rr = row_at(ra, 0);
-#pragma unroll
-      for (int d = 0; d < AHEAD; ++d)
-        if (q0 + d < q1) load_rows(d);
-      if (q0 < q1) {
-        first = L.start[ca];
-        rows = L.start[ca + 1] - first;
-        tiles = (rows + 15) / 16;
-      }
-      for (int q = q0; q < q1; q += AHEAD) {
-        if (FMT == kFp8 && q > q0 && (q - q0) % 64 == 0) scales(q);
-#pragma unroll
-        for (int d = 0; d < AHEAD; ++d) {
-          if (q + d < q1) {
-            const float fa = FMT == kFp8 ? lane_value(sa, (q + d - q0) % 64) : 1.0f;
-#pragma unroll
-            for (int t = 0; t < TILES; ++t) {
-              if (t < tiles) {
-                Rows x = r[d];
-                if (t > 0) x.load(act, row_at(ca, t), cs);
-#pragma unroll
-                for (int f = 0; f < F; ++f) multiply<FMT>(acc[t][f], w[d][f], x, fa);
-              }
-            }
-            if (++cs == spe || q + d + 1 == q1) {  // this expert's products into the tile, row by row
-#pragma unroll
-              for (int t = 0; t < TILES; ++t) {
-                if (t < tiles && 16 * t + col < rows) {
-                  float* to = tile + L.list[first + 16 * t + col] / k * TS + 4 * g;
-#pragma unroll
-                  for (int f = 0; f < F; ++f) {
-                    f32x4 v = *reinterpret_cast<f32x4*>(to + 16 * f);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] += acc[t][f][i];
-                    *reinterpret_cast<f32x4*>(to + 16 * f) = v;
-                  }
-                }
-#pragma unroll
-                for (int f = 0; f < F; ++f) acc[t][f] = f32x4{};
-              }
-              cs = 0;
-              if (++ca < a_end) {
-                first = L.start[ca];
-                rows = L.start[ca + 1] - first;
-                tiles = (rows + 15) / 16;
-              }
-            }
-            if (q + d + AHEAD < q1) {
-              load_down(d);
-              load_rows(d);
-            }
+      if (tid == 0)
+        L.last = __hip_atomic_fetch_add(P.cnt_down + c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                 static_cast<uint32_t>(ngrp) - 1;
+      lds_barrier();
+      if (L.last) {
+        for (int i = tid; i < T * kDC / 2; i += kThreads) {
+          const int64_t at = static_cast<int64_t>(i / (kDC / 2)) * H + c * kDC + 2 * (i % (kDC / 2));
+          float v0 = 0.0f, v1 = 0.0f;
+          for (int v = 0; v < ngrp; ++v) {
+            const uint64_t b =
+                __hip_atomic_load(reinterpret_cast<uint64_t*>(P.part + static_cast<int64_t>(v) * T * H + at),
+                                  __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            v0 += __uint_as_float(static_cast<uint32_t>(b));
+            v1 += __uint_as_float(static_cast<uint32_t>(b >> 32));
           }
+          *reinterpret_cast<uint32_t*>(P.y + at) = pack_bf16x2(v0, v1);
         }
       }
     }
-    fin = u;
-    if (tid == 0) L.unit = tk.take(P);
-    lds_barrier();
-    u = __builtin_amdgcn_readfirstlane(L.unit);
+    lds_barrier();  // the tiles are free
   }
-  signal();
 }
 
 template <int FMT, int NC>
 void launch_layer(const FewParams& P, unsigned grid, hipStream_t st) {
-  constexpr int A = FMT == kBf16 ? 4 : 8;
-  if (P.T <= 16) few_kernel<FMT, 1, 1, A, NC><<<grid, kThreads, 0, st>>>(P);
-  else few_kernel<FMT, 4, 2, A / 2, NC><<<grid, kThreads, 0, st>>>(P);
+  constexpr int NB = FMT == kBf16 ? 4 : 2;
+  if (P.T <= 16) few_kernel<FMT, 1, NB, NC><<<grid, kThreads, 0, st>>>(P);
+  else few_kernel<FMT, 4, NB, NC><<<grid, kThreads, 0, st>>>(P);
 }
 
 int few_max_active(const moe_shape& s) { return s.T * s.k < s.E ? s.T * s.k : s.E; }
@@ -880,7 +913,7 @@ FewLayout few_layout(const moe_shape& s) {
   FewLayout l{};
   auto up = [](size_t v) { return (v + 255) & ~static_cast<size_t>(255); };
   l.groups = few_max_groups(s);
-  l.counters = (2 * kLists + l.groups) * kLine + s.H / 16;
+  l.counters = (kLists + l.groups) * kLine + s.H / 16;
   l.act = up(static_cast<size_t>(l.counters) * 4);
   l.part = up(l.act + static_cast<size_t>(s.T) * s.k * s.I * 2);
   l.total = up(l.part + static_cast<size_t>(l.groups) * s.T * s.H * 4);
@@ -910,7 +943,7 @@ hipError_t launch_few(const moe_shape& s, const FewArgs& a, void* ws, hipStream_
   P.cnt = reinterpret_cast<uint32_t*>(base);
   P.act = reinterpret_cast<bf16_t*>(base + l.act);
   P.part = reinterpret_cast<float*>(base + l.part);
-  P.cnt_down = P.cnt + (2 * kLists + l.groups) * kLine;
+  P.cnt_down = P.cnt + (kLists + l.groups) * kLine;
   const dim3 rg(static_cast<unsigned>(s.E), static_cast<unsigned>(ceil_div(s.T, kRouterTokens)));
   few_router_kernel<<<rg, kWave, 0, st>>>(s.T, s.H, s.E, P.x, static_cast<const bf16_t*>(a.w_router), a.bias, a.logits,
                                           P.cnt, l.counters);
