@@ -10,7 +10,7 @@
 // units finish; no activation row but the selected experts' (T k I bf16) is
 // ever written.
 //
-//   few_router_kernel: logits, one wavefront per expert and 8 tokens. x and
+//   few_router_kernel: logits, one workgroup per expert and 8 tokens. x and
 //     w_router products are exact in fp32 (bf16 factors) and summed in fp64,
 //     so the logit is the exact sum rounded once, whatever the split. It also
 //     clears the second kernel's counters.
@@ -118,43 +118,54 @@ __device__ __forceinline__ void stores_done() {
 // ---- router -----------------------------------------------------------------
 
 constexpr int kRouterTokens = 8;
+constexpr int kRouterWaves = 4;  // one expert's reduction is split over them: one load's latency at H = 2048
 
-__global__ __launch_bounds__(kWave) void few_router_kernel(int T, int H, int E, const bf16_t* __restrict__ x,
-                                                           const bf16_t* __restrict__ wr,
-                                                           const float* __restrict__ bias, float* __restrict__ logits,
-                                                           uint32_t* __restrict__ cnt, int ncnt) {
+__global__ __launch_bounds__(kRouterWaves* kWave) void few_router_kernel(int T, int H, int E,
+                                                                         const bf16_t* __restrict__ x,
+                                                                         const bf16_t* __restrict__ wr,
+                                                                         const float* __restrict__ bias,
+                                                                         float* __restrict__ logits,
+                                                                         uint32_t* __restrict__ cnt, int ncnt) {
+  constexpr int N = kRouterWaves * kWave;
+  __shared__ double part[kRouterWaves][kRouterTokens];
   const int e = blockIdx.x, t0 = blockIdx.y * kRouterTokens;
-  const int lane = threadIdx.x;
-  const int stride = gridDim.x * gridDim.y * kWave;
-  for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * kWave + lane; i < ncnt; i += stride) cnt[i] = 0;
+  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  const int stride = gridDim.x * gridDim.y * N;
+  for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * N + tid; i < ncnt; i += stride) cnt[i] = 0;
   double acc[kRouterTokens];
 #pragma unroll
   for (int i = 0; i < kRouterTokens; ++i) acc[i] = 0.0;
-  const uint4* w4 = reinterpret_cast<const uint4*>(wr + static_cast<int64_t>(e) * H);
-  const int nt = min(kRouterTokens, T - t0);
-#pragma unroll 2
-  for (int c = lane; c < H / 8; c += kWave) {
-    const uint4 wv = w4[c];
-    const uint32_t wu[4] = {wv.x, wv.y, wv.z, wv.w};
+  const u32x4* w4 = reinterpret_cast<const u32x4*>(wr + static_cast<int64_t>(e) * H);
+  const u32x4* x4 = reinterpret_cast<const u32x4*>(x + static_cast<int64_t>(t0) * H);
+  const int nt = min(kRouterTokens, T - t0), chunks = H / 8;
+  for (int c = tid; c < chunks; c += N) {
+    const u32x4 wv = w4[c];
+    u32x4 xv[kRouterTokens];
+#pragma unroll
+    for (int i = 0; i < kRouterTokens; ++i) xv[i] = i < nt ? x4[static_cast<int64_t>(i) * chunks + c] : wv;
 #pragma unroll
     for (int i = 0; i < kRouterTokens; ++i) {
       if (i >= nt) break;
-      const uint4 xv = reinterpret_cast<const uint4*>(x + static_cast<int64_t>(t0 + i) * H)[c];
-      const uint32_t xu[4] = {xv.x, xv.y, xv.z, xv.w};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        acc[i] += static_cast<double>(__uint_as_float(xu[q] << 16) * __uint_as_float(wu[q] << 16));
-        acc[i] += static_cast<double>(__uint_as_float(xu[q] & 0xffff0000u) * __uint_as_float(wu[q] & 0xffff0000u));
+        acc[i] += static_cast<double>(__uint_as_float(xv[i][q] << 16) * __uint_as_float(wv[q] << 16));
+        acc[i] += static_cast<double>(__uint_as_float(xv[i][q] & 0xffff0000u) * __uint_as_float(wv[q] & 0xffff0000u));
       }
     }
   }
-  const double b = bias ? static_cast<double>(bias[e]) : 0.0;
 #pragma unroll
   for (int i = 0; i < kRouterTokens; ++i) {
     if (i >= nt) break;
 #pragma unroll
     for (int o = kWave / 2; o > 0; o >>= 1) acc[i] += __shfl_xor(acc[i], o, kWave);
-    if (lane == 0) logits[static_cast<int64_t>(t0 + i) * E + e] = static_cast<float>(acc[i] + b);
+    if (lane == 0) part[wave][i] = acc[i];
+  }
+  __syncthreads();
+  if (tid < nt) {
+    double v = part[0][tid];
+#pragma unroll
+    for (int w = 1; w < kRouterWaves; ++w) v += part[w][tid];
+    logits[static_cast<int64_t>(t0 + tid) * E + e] = static_cast<float>(v + (bias ? static_cast<double>(bias[e]) : 0.0));
   }
 }
 
@@ -162,14 +173,14 @@ __global__ __launch_bounds__(kWave) void few_router_kernel(int T, int H, int E, 
 
 // One step in registers as loaded: 16 weight rows x 128 bytes, lane l the
 // 16-byte chunk l % 8 of rows l / 8 and 8 + l / 8; and up to 16 token rows x
-// the same k (kXL lanes per row, kXN loads).
+// the same k (kXL lanes per row, XR rows).
 template <int FMT> constexpr int kStep = FMT == kBf16 ? 64 : 128;   // k per step
 template <int FMT> constexpr int kXL = FMT == kBf16 ? 8 : 16;
-template <int FMT> constexpr int kXN = kXL<FMT> / 4;
-template <int FMT>
+template <int FMT> constexpr int kRPI = kWave / kXL<FMT>;           // token rows per load
+template <int FMT, int XR>
 struct Step {
   u32x4 w[2];
-  u32x4 x[kXN<FMT>];
+  u32x4 x[XR / kRPI<FMT>];
 };
 
 // The wavefront's LDS for one step: weight rows, then token rows, chunks
@@ -189,18 +200,16 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t a, uint32_t b) {  // eight E4M
   return bf16x8{r0.x, r0.y, r1.x, r1.y, r2.x, r2.y, r3.x, r3.y};
 }
 
-template <int FMT>
-__device__ __forceinline__ void put_w(char* lds, const Step<FMT>& s) {
+__device__ __forceinline__ void put_w(char* lds, const u32x4 (&w)[2]) {
   const int lane = threadIdx.x % kWave, row = lane / 8, chunk = lane % 8;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4*>(lds + w_slot(row + 8 * i, chunk)) = s.w[i];
+  for (int i = 0; i < 2; ++i) *reinterpret_cast<u32x4*>(lds + w_slot(row + 8 * i, chunk)) = w[i];
 }
-template <int FMT>
-__device__ __forceinline__ void put_x(char* lds, const u32x4 (&x)[kXN<FMT>]) {
-  constexpr int RPI = kWave / kXL<FMT>;  // rows per load
-  const int lane = threadIdx.x % kWave, row = lane / kXL<FMT>, chunk = lane % kXL<FMT>;
+template <int FMT, int XN>
+__device__ __forceinline__ void put_x(char* lds, const u32x4 (&x)[XN], int row0) {
+  const int lane = threadIdx.x % kWave, row = row0 + lane / kXL<FMT>, chunk = lane % kXL<FMT>;
 #pragma unroll
-  for (int i = 0; i < kXN<FMT>; ++i) *reinterpret_cast<u32x4*>(lds + x_slot<FMT>(row + RPI * i, chunk)) = x[i];
+  for (int i = 0; i < XN; ++i) *reinterpret_cast<u32x4*>(lds + x_slot<FMT>(row + kRPI<FMT> * i, chunk)) = x[i];
 }
 
 // acc += (scale) weight rows x token rows over the step in LDS.
@@ -241,6 +250,7 @@ struct FewLists {  // in LDS: the pairs (token, slot) sorted by expert
   uint16_t start[1025];            // its pairs: list[start[a] .. start[a + 1])
   uint16_t list[kMaxPairs];        // pair t * k + j
   uint16_t token[kMaxPairs];       // t, by place in the list
+  uint16_t sel[kMaxPairs];         // expert of each pair
   float weight[kMaxPairs];         // by pair
 };
 
@@ -248,7 +258,6 @@ struct FewLists {  // in LDS: the pairs (token, slot) sorted by expert
 template <int TILES>
 union FewScratch {
   struct {
-    uint16_t sel[kMaxPairs];       // expert of each pair
     int count[1024];               // pairs per expert, then a cursor
     int wave_sum[kNW];
   } lists;
@@ -277,7 +286,8 @@ __device__ __forceinline__ uint32_t row_extreme(uint32_t v) {
 // Selection for more than 16 tokens: one token per 16-lane row (wavefronts
 // past the last token skip it). A lane holds the order bits
 // of logits n + 16 c (sel_key's upper word; 0 for a NaN). A round takes the
-// largest, then the lowest index that has it, and marks that one as taken.
+// largest, then the lowest index that has it, and marks that one as taken. The
+// weights follow at once: softmax and renormalisation as moe_route.
 template <int NC, class S_t>
 __device__ __forceinline__ void few_select_rows(const FewParams& P, FewLists& L, S_t& S) {
   const int tid = threadIdx.x, n = tid % 16;
@@ -332,13 +342,8 @@ __device__ __forceinline__ void few_select_rows(const FewParams& P, FewLists& L,
     const float p = top / z;
     const float den = row_sum(p) + 1e-20f;
     if (active && n < k) {
-      const int pair = t * k + n;
-      S.lists.sel[pair] = static_cast<uint16_t>(sel_i);
-      L.weight[pair] = p / den;
-      if (blockIdx.x == 0) {
-        P.topk_idx[pair] = sel_i;
-        P.topk_w[pair] = p / den;
-      }
+      L.sel[t * k + n] = static_cast<uint16_t>(sel_i);
+      L.weight[t * k + n] = p / den;
     }
   }
 }
@@ -360,7 +365,6 @@ __device__ __forceinline__ void few_select_waves(const FewParams& P, FewLists& L
       if (e < E) o[c] = static_cast<uint32_t>(sel_key(l[e], 0) >> 32);
       if (e < E) left |= 1u << c;
     }
-    float sel_v = 0.0f, vmax = 0.0f;
     int sel_i = 0;
     for (int j = 0; j < k; ++j) {
       uint32_t m = 0;
@@ -385,29 +389,31 @@ __device__ __forceinline__ void few_select_waves(const FewParams& P, FewLists& L
           }
         }
       }
-      const float bv = key_value(static_cast<uint64_t>(m) << 32);
-      if (j == 0) vmax = bv;
-      if (lane == j) {
-        sel_v = bv;
-        sel_i = at;
-      }
+      if (lane == j) sel_i = at;
     }
-    const float top = lane < k ? expf(sel_v - vmax) : 0.0f;
-    float z = top;
-#pragma unroll
-    for (int c = 0; c < NC; ++c)
-      if (left >> c & 1) z += expf(key_value(static_cast<uint64_t>(o[c]) << 32) - vmax);
+    if (lane < k) L.sel[t * k + lane] = static_cast<uint16_t>(sel_i);
+  }
+}
+
+// The weights of up to 16 tokens' experts: one token per wavefront. Off the way of the first weight loads;
+// the values are needed at the end of the first unit.
+__device__ __forceinline__ void few_weights(const FewParams& P, FewLists& L) {
+  const int lane = threadIdx.x % kWave;
+  const int E = P.E, k = P.k;
+  for (int t = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave); t < P.T; t += kNW) {
+    const float* l = P.logits + static_cast<int64_t>(t) * E;
+    const float v0 = lane < E ? l[lane] : 0.0f, v1 = kWave + lane < E ? l[kWave + lane] : 0.0f;
+    const int mine = lane < k ? L.sel[t * k + lane] : 0;
+    const float sel = l[mine];
+    const float vmax = lane_value(sel, 0);  // the first is the largest
+    float z = (lane < E ? expf(v0 - vmax) : 0.0f) + (kWave + lane < E ? expf(v1 - vmax) : 0.0f);
+    for (int e = 2 * kWave + lane; e < E; e += kWave) z += expf(l[e] - vmax);
     z = wave_sum(z);
-    const float p = top / z;
+    const float p = lane < k ? expf(sel - vmax) / z : 0.0f;
     const float den = row_sum(p) + 1e-20f;  // k <= 16: all of p lies in the first row
     if (lane < k) {
       const int pair = t * k + lane;
-      S.lists.sel[pair] = static_cast<uint16_t>(sel_i);
       L.weight[pair] = p / den;
-      if (blockIdx.x == 0) {
-        P.topk_idx[pair] = sel_i;
-        P.topk_w[pair] = p / den;
-      }
     }
   }
 }
@@ -424,7 +430,7 @@ __device__ __forceinline__ void few_select(const FewParams& P, FewLists& L, FewS
   __syncthreads();
   if (pairs <= kWave) {  // one wavefront, a pair per lane
     if (tid < kWave) {
-      const int mine = lane < pairs ? S.lists.sel[lane] : 0xffff;
+      const int mine = lane < pairs ? L.sel[lane] : 0xffff;
       int at = 0, a = 0;
       bool repeat = false;
       for (int i = 0; i < pairs; ++i) {
@@ -452,7 +458,7 @@ __device__ __forceinline__ void few_select(const FewParams& P, FewLists& L, FewS
   }
   for (int e = tid; e < E; e += kThreads) S.lists.count[e] = 0;
   __syncthreads();
-  for (int q = tid; q < pairs; q += kThreads) atomicAdd(&S.lists.count[S.lists.sel[q]], 1);
+  for (int q = tid; q < pairs; q += kThreads) atomicAdd(&S.lists.count[L.sel[q]], 1);
   __syncthreads();
   // Active experts in order, with their list starts: a scan over the experts,
   // two per thread, of (active, pairs) packed into one word.
@@ -488,7 +494,7 @@ __device__ __forceinline__ void few_select(const FewParams& P, FewLists& L, FewS
   }
   __syncthreads();
   for (int q = tid; q < pairs; q += kThreads) {
-    const int at = atomicAdd(&S.lists.count[S.lists.sel[q]], 1);
+    const int at = atomicAdd(&S.lists.count[L.sel[q]], 1);
     L.list[at] = static_cast<uint16_t>(q);
     L.token[at] = static_cast<uint16_t>(q / P.k);
   }
@@ -543,13 +549,15 @@ __device__ __forceinline__ void wait_count(const uint32_t* p, uint32_t want) {
   asm volatile("" ::: "memory");  // what follows is read after it
 }
 
-// TILES: 16-row tiles of one expert's tokens (one for T <= 16, else four); NB:
-// steps per batch (two batches are in flight per wavefront); NC: logits per
-// lane of a 16-lane row (E <= 16 NC).
-template <int FMT, int TILES, int NB, int NC>
+// TILES: 16-row tiles of one expert's tokens (one for T <= 16, else four); XR:
+// the token rows whose values travel with the weights (an expert's further
+// rows are loaded when their step is multiplied); NB: steps per batch (two
+// batches are in flight per wavefront); NC: logits per lane of a 16-lane row
+// (E <= 16 NC).
+template <int FMT, int TILES, int XR, int NB, int NC>
 __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
   constexpr int ESZ = FMT == kBf16 ? 2 : 1;
-  constexpr int RPI = kWave / kXL<FMT>, XN = kXN<FMT>;
+  constexpr int RPI = kRPI<FMT>, XN = XR / RPI;
   constexpr int kBatchLoads = NB * (2 + XN);
   __shared__ FewLists L;
   __shared__ __attribute__((aligned(16))) FewScratch<TILES> S;
@@ -583,7 +591,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
   };
 
   const rsrc_t xs = make_rsrc(P.x, static_cast<int64_t>(T) * H * 2);
-  Step<FMT> st[2][NB];
+  Step<FMT, XR> st[2][NB];
   float sa[2] = {1.0f, 1.0f}, sb[2] = {1.0f, 1.0f};  // E4M3: lane d, the scales of the batch's step d
   f32x4 acc[TILES];
   auto clear = [&]() __attribute__((always_inline)) {
@@ -593,9 +601,17 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
   auto load_b128 = [&](auto scope, const rsrc_t& r, uint32_t off) __attribute__((always_inline)) {
     return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, decltype(scope)::value));
   };
+  bool weighed = false;
   typedef std::integral_constant<int, 0> Cached;
   typedef std::integral_constant<int, kDeviceScope> Fresh;
 
+  // The product of the step in LDS with row tile t.
+  auto multiply_tile = [&](int t, float f) __attribute__((always_inline)) {
+    if (TILES == 1 || t == 0) multiply<FMT>(acc[0], lds, f);
+    else if (t == 1) multiply<FMT>(acc[TILES > 1 ? 1 : 0], lds, f);
+    else if (t == 2) multiply<FMT>(acc[TILES > 1 ? 2 : 0], lds, f);
+    else multiply<FMT>(acc[TILES > 1 ? 3 : 0], lds, f);
+  };
   // ---- gate/up units: the steps [q0, q1) of each are this wavefront's
   const int q0 = wave * hsteps / kNW, q1 = (wave + 1) * hsteps / kNW;
   const int batches = ((hsteps + kNW - 1) / kNW + NB - 1) / NB;  // the same for all wavefronts
@@ -636,7 +652,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
   // The products of batch j of unit u, in set B.
   auto use = [&](auto setc, int u, int j) __attribute__((always_inline)) {
     constexpr int B = decltype(setc)::value;
-    const int a = u / gpe, first = L.start[a], rows = L.start[a + 1] - first, tiles = (rows + 15) / 16;
+    const int a = u / gpe, first = L.start[a], rows = L.start[a + 1] - first;
 #pragma unroll
     for (int d = 0; d < NB; ++d) {
       float f = 1.0f;
@@ -644,28 +660,25 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
         const float fg = lane_value(sa[B], d), fu = lane_value(sb[B], d);
         f = lane < 32 ? fg : fu;  // result rows 8 .. 15 are up's
       }
-      put_w<FMT>(lds, st[B][d]);
-      put_x<FMT>(lds, st[B][d].x);
-      multiply<FMT>(acc[0], lds, f);
-      if constexpr (TILES > 1) {
-        const int q = q0 + j * NB + d;
-        if (q < q1)
-          for (int t = 1; t < tiles; ++t) {
-            u32x4 x[XN];
+      put_w(lds, st[B][d].w);
+      put_x<FMT>(lds, st[B][d].x, 0);
+      const int q = q0 + j * NB + d;
+      int t = 0;
+      if (q < q1)
+        for (int r0 = XR; r0 < rows; r0 += XR) {
+          if (r0 % 16 == 0) multiply_tile(t++, f);
+          u32x4 x[XN];
 #pragma unroll
-            for (int i = 0; i < XN; ++i) {
-              const int row = 16 * t + xrow + RPI * i;
-              const bool dead = row >= rows || (hhalf && q == hsteps - 1 && xc >= kXL<FMT> / 2);
-              x[i] = load_b128(Cached{}, xs,
-                               dead ? kNoRow
-                                    : static_cast<uint32_t>(L.token[first + row]) * H * 2 + 16 * xc + q * (2 * kStep<FMT>));
-            }
-            put_x<FMT>(lds, x);
-            if (t == 1) multiply<FMT>(acc[1], lds, f);
-            else if (t == 2) multiply<FMT>(acc[2], lds, f);
-            else multiply<FMT>(acc[3], lds, f);
+          for (int i = 0; i < XN; ++i) {
+            const int row = r0 + xrow + RPI * i;
+            const bool dead = row >= rows || (hhalf && q == hsteps - 1 && xc >= kXL<FMT> / 2);
+            x[i] = load_b128(Cached{}, xs,
+                             dead ? kNoRow
+                                  : static_cast<uint32_t>(L.token[first + row]) * H * 2 + 16 * xc + q * (2 * kStep<FMT>));
           }
-      }
+          put_x<FMT>(lds, x, r0 % 16);
+        }
+      multiply_tile(t, f);
     }
   };
   // A unit's end: the partial sums to LDS; wavefront t then sums row tile t,
@@ -720,6 +733,15 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
       if (batches > 1) fetch(Set1{}, u, 1);
       else fetch(Set1{}, un, 0);
       clear();
+      if (TILES == 1 && !weighed) few_weights(P, L);
+      weighed = true;
+      if (share == 0) {  // the routing's outputs
+        __syncthreads();
+        for (int i = tid; i < T * k; i += kThreads) {
+          P.topk_idx[i] = L.sel[i];
+          P.topk_w[i] = L.weight[i];
+        }
+      }
       int j = 0;
       auto turn_over = [&](auto setc) __attribute__((always_inline)) {
         use(setc, u, j);
@@ -753,71 +775,96 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
   for (int u = blockIdx.x; u < down; u += gridDim.x) {
     const int grp = u / dpg, c = u - grp * dpg, a0 = grp * size, a_end = a0 + min(size, na - a0);
     const int total = (a_end - a0) * spe, d0 = wave * total / kNW, d1 = (wave + 1) * total / kNW;
-    const int nb = (d1 - d0 + NB - 1) / NB;
+    // Cursors over the group's steps, expert by expert: of the weights'
+    // loads, the activations' and the products.
+    struct Cursor {
+      int q, a, s;
+    };
+    Cursor cw{d0, a0 + d0 / spe, d0 % spe}, cx = cw, cu = cw;
     const uint32_t wo = static_cast<uint32_t>(wr) * I * ESZ + 16 * wc;
-    // Weights of batch j into set B.
-    auto fetch_w = [&](auto setc, int j) __attribute__((always_inline)) {
+    auto weights_of = [&](int a) {
+      return make_rsrc(static_cast<const char*>(P.w2) + (static_cast<int64_t>(L.expert[a]) * H + c * kDC) * I * ESZ,
+                       kDC * I * ESZ);
+    };
+    rsrc_t rw = cw.q < d1 ? weights_of(cw.a) : make_rsrc(P.w2, 0);
+    float sc[2][NB];  // E4M3: the steps' scales
+    auto fetch_w = [&](auto setc) __attribute__((always_inline)) {
       constexpr int B = decltype(setc)::value;
 #pragma unroll
       for (int d = 0; d < NB; ++d) {
-        const int q = min(d0 + j * NB + d, total - 1), a = q / spe, s = q - a * spe;
-        const rsrc_t r = make_rsrc(static_cast<const char*>(P.w2) +
-                                       (static_cast<int64_t>(L.expert[a0 + a]) * H + c * kDC) * I * ESZ,
-                                   d0 + j * NB + d < d1 ? kDC * I * ESZ : 0);
-        const uint32_t o = ihalf && s == spe - 1 && wc >= 4 ? kNoRow : wo + s * 128;
-        st[B][d].w[0] = load_b128(Cached{}, r, o);
-        st[B][d].w[1] = load_b128(Cached{}, r, o + 8 * I * ESZ);
-      }
-      if constexpr (FMT == kFp8) {
-        const int q = min(d0 + j * NB + lane % NB, total - 1);
-        sa[B] = P.s2[(static_cast<int64_t>(L.expert[a0 + q / spe]) * ((H + 127) / 128) + c * kDC / 128) * spe + q % spe];
+        const uint32_t o = ihalf && cw.s == spe - 1 && wc >= 4 ? kNoRow : wo + cw.s * 128;
+        st[B][d].w[0] = load_b128(Cached{}, rw, o);
+        st[B][d].w[1] = load_b128(Cached{}, rw, o + 8 * I * ESZ);
+        if constexpr (FMT == kFp8)
+          sc[B][d] = P.s2[(static_cast<int64_t>(L.expert[min(cw.a, a_end - 1)]) * ((H + 127) / 128) + c * kDC / 128) * spe +
+                          cw.s];
+        if (++cw.s == spe) {
+          cw.s = 0;
+          if (++cw.a < a_end) rw = weights_of(cw.a);
+        }
+        if (++cw.q >= d1) rw = make_rsrc(P.w2, 0);
       }
     };
-    // Activations of batch j, rows 16 t on, step d.
-    auto row_loads = [&](int j, int d, int t, u32x4(&x)[XN]) __attribute__((always_inline)) {
-      const int q = min(d0 + j * NB + d, total - 1), a = a0 + q / spe, s = q % spe;
-      const int f0 = L.start[a], n = d0 + j * NB + d < d1 ? L.start[a + 1] - f0 : 0;
+    // The activations' offsets of rows r0 on of active expert a.
+    auto row_offsets = [&](int a, int r0, uint32_t(&o)[XN]) __attribute__((always_inline)) {
+      const int f0 = L.start[a], n = L.start[a + 1] - f0;
 #pragma unroll
       for (int i = 0; i < XN; ++i) {
-        const int row = 16 * t + xrow + RPI * i;
-        const bool dead = row >= n || (ihalf && s == spe - 1 && xc >= kXL<FMT> / 2);
-        x[i] = load_b128(Fresh{}, act,
-                         dead ? kNoRow : static_cast<uint32_t>(L.list[f0 + row]) * I * 2 + 16 * xc + s * (2 * kStep<FMT>));
+        const int row = r0 + xrow + RPI * i;
+        o[i] = row < n ? static_cast<uint32_t>(L.list[f0 + row]) * I * 2 + 16 * xc : kNoRow;
       }
     };
-    auto fetch_x = [&](auto setc, int j) __attribute__((always_inline)) {
+    auto row_loads = [&](const uint32_t(&o)[XN], int s, u32x4(&x)[XN]) __attribute__((always_inline)) {
+      const uint32_t dead = ihalf && s == spe - 1 && xc >= kXL<FMT> / 2 ? kNoRow : 0;
+#pragma unroll
+      for (int i = 0; i < XN; ++i) x[i] = load_b128(Fresh{}, act, (o[i] | dead) + s * (2 * kStep<FMT>));
+    };
+    uint32_t xo[XN];
+    auto fetch_x = [&](auto setc) __attribute__((always_inline)) {
       constexpr int B = decltype(setc)::value;
 #pragma unroll
-      for (int d = 0; d < NB; ++d) row_loads(j, d, 0, st[B][d].x);
+      for (int d = 0; d < NB; ++d) {
+        row_loads(xo, cx.s, st[B][d].x);
+        if (++cx.s == spe) {
+          cx.s = 0;
+          if (++cx.a < a_end) row_offsets(cx.a, 0, xo);
+        }
+        if (++cx.q >= d1) {
+#pragma unroll
+          for (int i = 0; i < XN; ++i) xo[i] = kNoRow;
+        }
+      }
     };
     float* tile = &S.tile[wave][0][0];
     constexpr int TS = kDC + 4;
-    auto use_down = [&](auto setc, int j) __attribute__((always_inline)) {
+    int first = 0, rows = 0;
+    auto open = [&](int a) __attribute__((always_inline)) {
+      first = L.start[a];
+      rows = L.start[a + 1] - first;
+    };
+    auto use_down = [&](auto setc) __attribute__((always_inline)) {
       constexpr int B = decltype(setc)::value;
 #pragma unroll
       for (int d = 0; d < NB; ++d) {
-        const int q = d0 + j * NB + d;
-        if (q < d1) {
-          const int a = q / spe, s = q - a * spe, first = L.start[a0 + a], rows = L.start[a0 + a + 1] - first;
-          const int tiles = (rows + 15) / 16;
-          const float f = FMT == kFp8 ? lane_value(sa[B], d) : 1.0f;
-          put_w<FMT>(lds, st[B][d]);
-          put_x<FMT>(lds, st[B][d].x);
-          multiply<FMT>(acc[0], lds, f);
-          if constexpr (TILES > 1) {
-            for (int t = 1; t < tiles; ++t) {
-              u32x4 x[XN];
-              row_loads(j, d, t, x);
-              put_x<FMT>(lds, x);
-              if (t == 1) multiply<FMT>(acc[1], lds, f);
-              else if (t == 2) multiply<FMT>(acc[2], lds, f);
-              else multiply<FMT>(acc[3], lds, f);
-            }
+        if (cu.q < d1) {
+          const float f = FMT == kFp8 ? sc[B][d] : 1.0f;
+          put_w(lds, st[B][d].w);
+          put_x<FMT>(lds, st[B][d].x, 0);
+          int t = 0;
+          for (int r0 = XR; r0 < rows; r0 += XR) {
+            if (r0 % 16 == 0) multiply_tile(t++, f);
+            uint32_t o[XN];
+            u32x4 x[XN];
+            row_offsets(cu.a, r0, o);
+            row_loads(o, cu.s, x);
+            put_x<FMT>(lds, x, r0 % 16);
           }
-          if (s == spe - 1 || q + 1 == d1) {  // this expert's products into the tile, row by row
+          multiply_tile(t, f);
+          ++cu.q;
+          if (++cu.s == spe || cu.q == d1) {  // this expert's products into the tile, row by row
 #pragma unroll
             for (int t = 0; t < TILES; ++t) {
-              if (t < tiles && 16 * t + col < rows) {
+              if (16 * t + col < rows) {
                 f32x4* to = reinterpret_cast<f32x4*>(tile + L.token[first + 16 * t + col] * TS + 4 * g);
                 f32x4 v = *to;
 #pragma unroll
@@ -826,29 +873,38 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
               }
             }
             clear();
+            cu.s = 0;
+            if (cu.q < d1) open(++cu.a);
           }
         }
       }
     };
     typedef std::integral_constant<int, 0> Set0;
     typedef std::integral_constant<int, 1> Set1;
-    fetch_w(Set0{}, 0);
-    fetch_w(Set1{}, 1);
+    fetch_w(Set0{});
+    fetch_w(Set1{});
     for (int i = lane; i < T * kDC; i += kWave) tile[i / kDC * TS + i % kDC] = 0.0f;
     // The group's activations are there once all its tiles are counted.
     uint32_t want = 0;
     for (int a = a0; a < a_end; ++a) want += (L.start[a + 1] - L.start[a] + 15) / 16 * gpe;
     wait_count(P.cnt + (kLists + grp) * kLine, want);
-    fetch_x(Set0{}, 0);
-    fetch_x(Set1{}, 1);
+    if (cx.q < d1) {
+      row_offsets(cx.a, 0, xo);
+      open(cu.a);
+    } else {
+#pragma unroll
+      for (int i = 0; i < XN; ++i) xo[i] = kNoRow;
+    }
+    fetch_x(Set0{});
+    fetch_x(Set1{});
     clear();
-    for (int j = 0; j < nb; j += 2) {
-      use_down(Set0{}, j);
-      fetch_w(Set0{}, j + 2);
-      fetch_x(Set0{}, j + 2);
-      use_down(Set1{}, j + 1);
-      fetch_w(Set1{}, j + 3);
-      fetch_x(Set1{}, j + 3);
+    while (cu.q < d1) {
+      use_down(Set0{});
+      fetch_w(Set0{});
+      fetch_x(Set0{});
+      use_down(Set1{});
+      fetch_w(Set1{});
+      fetch_x(Set1{});
     }
     lds_barrier();
     for (int i = tid; i < T * kDC / 2; i += kThreads) {
@@ -896,9 +952,17 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
 
 template <int FMT, int NC>
 void launch_layer(const FewParams& P, unsigned grid, hipStream_t st) {
+  // An expert has at most T rows, and T k / E on average: up to 4 on average,
+  // few have more than 8.
   constexpr int NB = FMT == kBf16 ? 4 : 2;
-  if (P.T <= 16) few_kernel<FMT, 1, NB, NC><<<grid, kThreads, 0, st>>>(P);
-  else few_kernel<FMT, 4, NB, NC><<<grid, kThreads, 0, st>>>(P);
+  const bool thin = P.T <= 8 || P.T * P.k <= 4 * P.E;
+  if (P.T <= 16) {
+    if (thin) few_kernel<FMT, 1, 8, NB, NC><<<grid, kThreads, 0, st>>>(P);
+    else few_kernel<FMT, 1, 16, NB, NC><<<grid, kThreads, 0, st>>>(P);
+  } else {
+    if (thin) few_kernel<FMT, 4, 8, NB, NC><<<grid, kThreads, 0, st>>>(P);
+    else few_kernel<FMT, 4, 16, NB, NC><<<grid, kThreads, 0, st>>>(P);
+  }
 }
 
 int few_max_active(const moe_shape& s) { return s.T * s.k < s.E ? s.T * s.k : s.E; }
@@ -945,7 +1009,7 @@ hipError_t launch_few(const moe_shape& s, const FewArgs& a, void* ws, hipStream_
   P.part = reinterpret_cast<float*>(base + l.part);
   P.cnt_down = P.cnt + (kLists + l.groups) * kLine;
   const dim3 rg(static_cast<unsigned>(s.E), static_cast<unsigned>(ceil_div(s.T, kRouterTokens)));
-  few_router_kernel<<<rg, kWave, 0, st>>>(s.T, s.H, s.E, P.x, static_cast<const bf16_t*>(a.w_router), a.bias, a.logits,
+  few_router_kernel<<<rg, kRouterWaves * kWave, 0, st>>>(s.T, s.H, s.E, P.x, static_cast<const bf16_t*>(a.w_router), a.bias, a.logits,
                                           P.cnt, l.counters);
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
