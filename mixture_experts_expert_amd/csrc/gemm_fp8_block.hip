@@ -29,8 +29,6 @@
 //
 // The gate/up forms end with a = silu(g) u quantised: a workgroup holds whole
 // 1 x 128 blocks of a, whose maxima meet in LDS.
-#include <type_traits>
-
 #include "moe_internal.h"
 
 namespace moe {
@@ -248,47 +246,52 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
   f32x4 acc[FM][4];
   int nv = 0;  // this wavefront's 16-row tiles that hold rows
   // One step on stage C; the loads of step sn (of the load state's tile) into
-  // stage D meanwhile.
-  auto step = [&](auto fullc, const uint8_t* C, uint8_t* D, bool live, bool loads, int s, int sn)
-                  __attribute__((always_inline)) {
-    constexpr bool FULL = decltype(fullc)::value;
+  // stage D meanwhile. Half of the wavefront's rows at a time, so that a tile
+  // with few rows skips what holds none; a's fragments one 16-row tile ahead.
+  auto step = [&](const uint8_t* C, uint8_t* D, bool live, bool loads, int s, int sn) __attribute__((always_inline)) {
+    constexpr int HM = FM / 2, HL = LOADS / 2;
     if (loads) set_step(sn);
     int lane = lane_id;
     asm volatile("" : "+v"(lane));
-    const int g2 = 2 * (lane >> 4), q = lane & 15;
+    const int q = lane & 15, o = ((2 * (lane >> 4)) ^ ((q >> 1) & 7)) << 4;  // rows 16 apart: the same swizzle
+    auto chunk = [&](const uint8_t* p) __attribute__((always_inline)) {
+      return join(*reinterpret_cast<const u32x4*>(p + o), *reinterpret_cast<const u32x4*>(p + (o ^ 16)));
+    };
+    const uint8_t* wrow = C + OB + (wn * 64 + q) * KS;
+    const uint8_t* arow = C + (wm * (BM / 2) + q) * KS;
+    const uint8_t* srow = C + OS + (wm * (BM / 2) + q) * 4;
     i32x8 wf[4];
-    if (live) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int r = wn * 64 + j * 16 + q;
-        const uint8_t* p = C + OB + r * KS;
-        const int o = (g2 ^ ((r >> 1) & 7)) << 4;
-        wf[j] = join(*reinterpret_cast<const u32x4*>(p + o), *reinterpret_cast<const u32x4*>(p + (o ^ 16)));
-      }
-    }
     const float fg = lane_value(swg, s & 63), fu = GU ? lane_value(swu, s & 63) : 0.0f;
+    if (live && nv > 0)
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      if (live && (FULL || i < nv)) {
-        const int r = wm * (BM / 2) + i * 16 + q;
-        const uint8_t* p = C + r * KS;
-        const int o = (g2 ^ ((r >> 1) & 7)) << 4;
-        const i32x8 af = join(*reinterpret_cast<const u32x4*>(p + o), *reinterpret_cast<const u32x4*>(p + (o ^ 16)));
-        const float sr = *reinterpret_cast<const float*>(C + OS + r * 4);
-        const float s0 = sr * fg, s1 = GU ? sr * fu : s0;
-        f32x4 pr[4];
+      for (int j = 0; j < 4; ++j) wf[j] = chunk(wrow + j * 16 * KS);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) pr[j] = block_product(wf[j], af);
+    for (int h = 0; h < 2; ++h) {
+      if (loads)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int v = h * HL; v < (h ? LOADS : HL); ++v) load(v, sn, D);
+      if (live && nv > h * HM) {
+        i32x8 af[2];
+        float sr[2];
+        af[0] = chunk(arow + h * HM * 16 * KS);
+        sr[0] = *reinterpret_cast<const float*>(srow + h * HM * 64);
 #pragma unroll
-          for (int x = 0; x < 4; ++x) acc[i][j][x] = fmaf(j < 2 ? s0 : s1, pr[j][x], acc[i][j][x]);
-      }
-      if (loads) {
-        load(i, sn, D);
-        if (i == FM - 1)
+        for (int i = 0; i < HM; ++i) {
+          if (i + 1 < HM) {
+            af[(i + 1) & 1] = chunk(arow + (h * HM + i + 1) * 16 * KS);
+            sr[(i + 1) & 1] = *reinterpret_cast<const float*>(srow + (h * HM + i + 1) * 64);
+          }
+          f32x4 pr[4];
 #pragma unroll
-          for (int v = FM; v < LOADS; ++v) load(v, sn, D);
+          for (int j = 0; j < 4; ++j) pr[j] = block_product(wf[j], af[i & 1]);
+          const float s0 = sr[i & 1] * fg, s1 = GU ? sr[i & 1] * fu : s0;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              acc[h * HM + i][j][x] = fmaf(j < 2 ? s0 : s1, pr[j][x], acc[h * HM + i][j][x]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
   };
@@ -325,13 +328,11 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
       if ((s & 63) == 0) weight_scales(ce, cn0, s);
       const bool odd = s + 1 < steps;  // the second step exists
       const bool last = s + 2 >= padded;
-      if (nv == FM) step(std::true_type{}, st0, st1, true, odd, s, s + 1);
-      else step(std::false_type{}, st0, st1, true, odd, s, s + 1);
+      step(st0, st1, true, odd, s, s + 1);
       landed();
       if (last && next < hi) set_tile(next);
       const bool more = !last || next < hi;
-      if (nv == FM) step(std::true_type{}, st1, st0, odd, more, s + 1, last ? 0 : s + 2);
-      else step(std::false_type{}, st1, st0, odd, more, s + 1, last ? 0 : s + 2);
+      step(st1, st0, odd, more, s + 1, last ? 0 : s + 2);
       if (!last) landed();
     }
     // ---- epilogue
