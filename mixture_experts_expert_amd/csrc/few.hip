@@ -664,7 +664,9 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
       put_x<FMT>(lds, st[B][d].x, 0);
       const int q = q0 + j * NB + d;
       int t = 0;
-      if (q < q1)
+      // Past the wavefront's steps nothing is multiplied: its zeros would meet
+      // rows that an earlier unit left in LDS, and zero times their NaN is NaN.
+      if (q < q1) {
         for (int r0 = XR; r0 < rows; r0 += XR) {
           if (r0 % 16 == 0) multiply_tile(t++, f);
           u32x4 x[XN];
@@ -678,7 +680,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
           }
           put_x<FMT>(lds, x, r0 % 16);
         }
-      multiply_tile(t, f);
+        multiply_tile(t, f);
+      }
     }
   };
   // A unit's end: the partial sums to LDS; wavefront t then sums row tile t,
