@@ -63,7 +63,8 @@ moe_status moe_gemm_fp8_block(int32_t M, int32_t E, int32_t N, int32_t K, const 
   if (any_null(aq, a_scale, wq, w_scale, out) || (offsets == nullptr && E != 1)) return MOE_EINVAL;
   if (misaligned(aq, wq, out)) return MOE_EINVAL;
   if (N % 8 != 0 || K % 16 != 0 || E > 1024) return MOE_EUNSUPPORTED;
-  if (static_cast<int64_t>(N) * K >= k2G || 256 * static_cast<int64_t>(K) >= k2G) return MOE_EUNSUPPORTED;
+  if (static_cast<int64_t>(N) * K >= k2G || 256 * static_cast<int64_t>(K) >= k2G || 512 * static_cast<int64_t>(N) >= k2G)
+    return MOE_EUNSUPPORTED;
   moe::BlockGemmArgs g{};
   g.M = g.arows = M;
   g.E = E;

@@ -29,6 +29,8 @@
 //
 // The gate/up forms end with a = silu(g) u quantised: a workgroup holds whole
 // 1 x 128 blocks of a, whose maxima meet in LDS.
+#include <type_traits>
+
 #include "moe_internal.h"
 
 namespace moe {
@@ -36,6 +38,7 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __amdgpu_buffer_rsrc_t rsrc_t;
 
@@ -109,6 +112,7 @@ __device__ __forceinline__ uint32_t codes4(const float (&v)[4], float up, float 
 // ---- many rows per expert ---------------------------------------------------
 
 constexpr int BN = 256;
+constexpr int kBand = 8;  // row tiles that run side by side over all columns: what an XCD's workgroups read meets in its L2
 
 // GU: N columns of each of w0 and w1 (128 per tile), else N of w0 (256 per tile).
 template <bool GU, int BM>
@@ -117,8 +121,8 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
   constexpr int NA = BM / 64;            // load instructions of a per wavefront and step
   constexpr int OB = BM * KS, OS = OB + BN * KS;
   constexpr int TN = GU ? BN / 2 : BN;
-  __shared__ __attribute__((aligned(1024))) uint8_t st0[OS + BM * 4];
-  __shared__ __attribute__((aligned(1024))) uint8_t st1[OS + BM * 4];
+  __shared__ __attribute__((aligned(1024))) uint8_t st0[OS + kThreads * 4];
+  __shared__ __attribute__((aligned(1024))) uint8_t st1[OS + kThreads * 4];
   __shared__ int tstart[1025];
   __shared__ int eoff[1025];
   __shared__ int wsum[kWaves];
@@ -171,7 +175,6 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
   // the multiplications and the epilogue use.
   int e = 0, row0 = 0, mvalid = 0, n0 = 0;
   uint32_t aoff[NA], boff[4], soff = kOutside;
-  float swg = 0.0f, swu = 0.0f;          // lane l: the weight scales of step l (of the current 64)
   auto set_tile = [&](int L) __attribute__((always_inline)) {
     int l = 0, h = E - 1;
     while (l < h) {
@@ -179,7 +182,8 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
       if (tstart[mid] * ntn <= L) l = mid; else h = mid - 1;
     }
     const int rem = L - tstart[l] * ntn, mte = tstart[l + 1] - tstart[l];
-    const int nt = rem / mte, mt = rem - nt * mte;
+    const int band = rem / (kBand * ntn), bm = min(kBand, mte - band * kBand);
+    const int nt = (rem - band * kBand * ntn) / bm, mt = band * kBand + rem - band * kBand * ntn - nt * bm;
     const int64_t cnt = eoff[l + 1] - eoff[l];  // the expert's rows, evenly over its tiles
     const int r0 = static_cast<int>(mt * cnt / mte);
     e = __builtin_amdgcn_readfirstlane(l);
@@ -195,62 +199,83 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
       const int row = GU ? (r < mvalid ? P.row_token[row0 + r] : 0) : r;
       aoff[t] = r < mvalid ? static_cast<uint32_t>(row) * K + c * 16 : kOutside;
     }
-    if (wave < BM / 64) {
+    {
       const int r = wave * 64 + lane;
       const int row = GU ? (r < mvalid ? P.row_token[row0 + r] : 0) : r;
-      soff = r < mvalid ? static_cast<uint32_t>(row) * KB * 4 : kOutside;
+      soff = r < mvalid ? static_cast<uint32_t>(row) * KB * 4 : kOutside;  // behind the tile's rows: zeros
     }
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const int r = (wave * 4 + t) * 8 + (lane >> 3);
       const int c = (lane & 7) ^ ((r >> 1) & 7);
       const int j = (r >> 4) & 3, q = r & 15;
-      const int n = GU ? n0 + (r >> 6) * 32 + 8 * (q >> 2) + 4 * (j & 1) + (q & 3)
-                       : n0 + (r >> 6) * 64 + 16 * (q >> 2) + 4 * j + (q & 3);
+      const int n = n0 + (r >> 6) * (GU ? 32 : 64) + (GU ? 0 : (j >> 1) * 32) + 8 * (q >> 2) + 4 * (j & 1) + (q & 3);
       boff[t] = n < P.N ? static_cast<uint32_t>(n) * K + c * 16 : kOutside;
     }
   };
-  // Load instruction v of step s into stage S: a rows, weight rows, scales.
+  // Load instruction v of a step: a rows, weight rows, scales. Every wavefront
+  // issues every one in every step (a branch in the loop costs more than the
+  // instruction): without a step to load the ranges are empty, and the chunks
+  // past a row's end lie outside; both read zeros.
   constexpr int LOADS = NA + 5;
   rsrc_t ra, rb, rs;
-  auto set_step = [&](int s) __attribute__((always_inline)) {
+  bool in[2];  // the lane's chunk of even and odd blocks of 8 rows ends before the row does
+  auto set_step = [&](int s, bool loads) __attribute__((always_inline)) {
     const int64_t k0 = static_cast<int64_t>(s) * KS;
-    if constexpr (GU) {
-      ra = make_rsrc(P.a + k0, static_cast<int64_t>(P.arows) * K - k0);
-      rs = make_rsrc(P.sa + s, (static_cast<int64_t>(P.arows) * KB - s) * 4);
-      rb = make_rsrc(((wave & 1) ? P.w1 : P.w0) + static_cast<int64_t>(e) * P.N * K + k0,
-                     static_cast<int64_t>(P.N) * K - k0);
-    } else {
-      ra = make_rsrc(P.a + static_cast<int64_t>(row0) * K + k0, static_cast<int64_t>(mvalid) * K - k0);
-      rs = make_rsrc(P.sa + static_cast<int64_t>(row0) * KB + s, (static_cast<int64_t>(mvalid) * KB - s) * 4);
-      rb = make_rsrc(P.w0 + static_cast<int64_t>(e) * P.N * K + k0, static_cast<int64_t>(P.N) * K - k0);
-    }
+    const int64_t arows = !loads ? 0 : GU ? P.arows : mvalid, wrows = loads ? P.N : 0;
+    const int64_t first = GU ? 0 : row0;
+    ra = make_rsrc(P.a + first * K + k0, max(arows * K - k0, int64_t{0}));
+    rs = make_rsrc(P.sa + first * KB + s, max((arows * KB - s) * 4, int64_t{0}));
+    rb = make_rsrc((GU && (wave & 1) ? P.w1 : P.w0) + static_cast<int64_t>(e) * P.N * K + k0,
+                   max(wrows * K - k0, int64_t{0}));
+    const int limit = s == steps - 1 ? tail : KS;
+    const int c = (lane_id & 7) ^ (lane_id >> 4);
+    in[0] = c * 16 < limit;
+    in[1] = (c ^ 4) * 16 < limit;
   };
-  auto load = [&](int v, int s, uint8_t* S) __attribute__((always_inline)) {
+  auto load = [&](int v, uint8_t* S) __attribute__((always_inline)) {
     typedef __attribute__((address_space(3))) void* lds_ptr;
     if (v == LOADS - 1) {
-      if (wave < BM / 64) __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)(S + OS + wave * 256), 4, soff, 0, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)(S + OS + wave * 256), 4, soff, 0, 0, 0);
       return;
     }
     const bool is_a = v < NA;
     const int blk = is_a ? wave * NA + v : wave * 4 + (v - NA);
-    uint32_t off = is_a ? aoff[v < NA ? v : 0] : boff[v < NA ? 0 : v - NA];
-    if (s == steps - 1 && tail != KS) {  // chunks past the row's end read zeros
-      const int r = blk * 8 + (lane_id >> 3);
-      if (((lane_id & 7) ^ ((r >> 1) & 7)) * 16 >= tail) off = kOutside;
-    }
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(is_a ? ra : rb, (lds_ptr)(S + (is_a ? 0 : OB) + blk * 1024), 16, off, 0, 0,
-                                             0);
+    const uint32_t off = is_a ? aoff[v < NA ? v : 0] : boff[v < NA ? 0 : v - NA];
+    const bool even = ((is_a ? v : v - NA) & 1) == 0;  // NA and 4 are even
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(is_a ? ra : rb, (lds_ptr)(S + (is_a ? 0 : OB) + blk * 1024), 16,
+                                             in[even ? 0 : 1] ? off : kOutside, 0, 0, 0);
   };
 
+  // lane l: the weight scales of step l (of the current 64) for the tile in
+  // work and for the next one.
+  float swg = 0.0f, swu = 0.0f, next_g = 0.0f, next_u = 0.0f;
+  auto weight_scales = [&](int we, int wn0, int s, float& g, float& u) __attribute__((always_inline)) {
+    const int b = min(s + lane_id, KB - 1);
+    const int nb = GU ? wn0 / 128 : min(wn0 + (wn >> 1) * 128, P.N - 1) / 128;
+    const int64_t at = (static_cast<int64_t>(we) * P.NB + nb) * KB + b;
+    g = P.sw0[at];
+    if constexpr (GU) u = P.sw1[at];
+  };
+  // All but the last PENDING memory instructions are done, and every wavefront is here.
+  auto landed = [&](auto pending) __attribute__((always_inline)) {
+    constexpr int n = decltype(pending)::value;
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070 | (n & 15) | (n >> 4) << 14);  // vmcnt(n) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  using none = std::integral_constant<int, 0>;
+
   f32x4 acc[FM][4];
-  int nv = 0;  // this wavefront's 16-row tiles that hold rows
-  // One step on stage C; the loads of step sn (of the load state's tile) into
-  // stage D meanwhile. Half of the wavefront's rows at a time, so that a tile
-  // with few rows skips what holds none; a's fragments one 16-row tile ahead.
-  auto step = [&](const uint8_t* C, uint8_t* D, bool live, bool loads, int s, int sn) __attribute__((always_inline)) {
-    constexpr int HM = FM / 2, HL = LOADS / 2;
-    if (loads) set_step(sn);
+  // One step on stage C for the wavefront's first NI 16-row tiles; meanwhile
+  // the LD load instructions of step sn go out (into stage D), in the first
+  // half. a's fragments are read one tile ahead. The empty asm keeps the order
+  // as written: the compiler otherwise joins the steps and spills.
+  auto step = [&](auto nic, auto ldc, const uint8_t* C, uint8_t* D, bool loads, int s, int sn)
+                  __attribute__((always_inline)) {
+    constexpr int NI = decltype(nic)::value, LD = decltype(ldc)::value;
+    if constexpr (LD > 0) set_step(sn, loads);
     int lane = lane_id;
     asm volatile("" : "+v"(lane));
     const int q = lane & 15, o = ((2 * (lane >> 4)) ^ ((q >> 1) & 7)) << 4;  // rows 16 apart: the same swizzle
@@ -260,87 +285,87 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
     const uint8_t* wrow = C + OB + (wn * 64 + q) * KS;
     const uint8_t* arow = C + (wm * (BM / 2) + q) * KS;
     const uint8_t* srow = C + OS + (wm * (BM / 2) + q) * 4;
-    i32x8 wf[4];
+    i32x8 wf[4], af[2];
+    float sr[2];
+    af[0] = chunk(arow);
+    sr[0] = *reinterpret_cast<const float*>(srow);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) wf[j] = chunk(wrow + j * 16 * KS);
     const float fg = lane_value(swg, s & 63), fu = GU ? lane_value(swu, s & 63) : 0.0f;
-    if (live && nv > 0)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) wf[j] = chunk(wrow + j * 16 * KS);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if (loads)
-#pragma unroll
-        for (int v = h * HL; v < (h ? LOADS : HL); ++v) load(v, sn, D);
-      if (live && nv > h * HM) {
-        i32x8 af[2];
-        float sr[2];
-        af[0] = chunk(arow + h * HM * 16 * KS);
-        sr[0] = *reinterpret_cast<const float*>(srow + h * HM * 64);
-#pragma unroll
-        for (int i = 0; i < HM; ++i) {
-          if (i + 1 < HM) {
-            af[(i + 1) & 1] = chunk(arow + (h * HM + i + 1) * 16 * KS);
-            sr[(i + 1) & 1] = *reinterpret_cast<const float*>(srow + (h * HM + i + 1) * 64);
-          }
-          f32x4 pr[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) pr[j] = block_product(wf[j], af[i & 1]);
-          const float s0 = sr[i & 1] * fg, s1 = GU ? sr[i & 1] * fu : s0;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int x = 0; x < 4; ++x)
-              acc[h * HM + i][j][x] = fmaf(j < 2 ? s0 : s1, pr[j][x], acc[h * HM + i][j][x]);
-          __builtin_amdgcn_sched_barrier(0);
-        }
+    for (int i = 0; i < NI; ++i) {
+      if (i + 1 < NI) {
+        af[(i + 1) & 1] = chunk(arow + (i + 1) * 16 * KS);
+        sr[(i + 1) & 1] = *reinterpret_cast<const float*>(srow + (i + 1) * 64);
       }
+      f32x4 pr[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) pr[j] = block_product(wf[j], af[i & 1]);
+#pragma unroll
+      for (int v = min(LD, i * LD * 2 / NI); v < min(LD, (i + 1) * LD * 2 / NI); ++v) load(v, D);
+      const float s0 = sr[i & 1] * fg, s1 = GU ? sr[i & 1] * fu : s0;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) acc[i][j][x] = fmaf(j < 2 ? s0 : s1, pr[j][x], acc[i][j][x]);
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("" : "+v"(acc[i][0]), "+v"(acc[i][1]), "+v"(acc[i][2]), "+v"(acc[i][3]));
     }
   };
-  auto landed = [&]() __attribute__((always_inline)) {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-  };
-  auto weight_scales = [&](int we, int wn0, int s) __attribute__((always_inline)) {
-    const int b = min(s + lane_id, KB - 1);
-    const int nb = GU ? wn0 / 128 : min(wn0 + (wn >> 1) * 128, P.N - 1) / 128;
-    const int64_t at = (static_cast<int64_t>(we) * P.NB + nb) * KB + b;
-    swg = P.sw0[at];
-    if constexpr (GU) swu = P.sw1[at];
-  };
 
+  // One tile. On entry step 0 is in st0 and step 1 is on its way to st1,
+  // ahead of STORES stores of the tile before: those run on under two steps.
+  constexpr int STORES = 2 * FM;
   int L = lo + slot;
-  if (L >= hi) return;
-  set_tile(L);
-  set_step(0);
-#pragma unroll
-  for (int v = 0; v < LOADS; ++v) load(v, 0, st0);
-  landed();
-  while (L < hi) {
+  auto tile = [&](auto nic) __attribute__((always_inline)) {
+    constexpr int NI = decltype(nic)::value;
+    using all = std::integral_constant<int, LOADS>;
     const int ce = e, crow0 = row0, cvalid = mvalid, cn0 = n0;
     const int next = L + nslots;
-    nv = min(max((cvalid - wm * (BM / 2) + 15) / 16, 0), FM);
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
+    for (int i = 0; i < NI; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
-    for (int s = 0; s < padded; s += 2) {
-      if ((s & 63) == 0) weight_scales(ce, cn0, s);
-      const bool odd = s + 1 < steps;  // the second step exists
-      const bool last = s + 2 >= padded;
-      step(st0, st1, true, odd, s, s + 1);
-      landed();
-      if (last && next < hi) set_tile(next);
-      const bool more = !last || next < hi;
-      step(st1, st0, odd, more, s + 1, last ? 0 : s + 2);
-      if (!last) landed();
+    auto advance = [&]() __attribute__((always_inline)) {
+      if (next < hi) {
+        set_tile(next);
+        weight_scales(e, n0, 0, next_g, next_u);
+      }
+    };
+    step(nic, none{}, st0, st1, false, 0, 0);
+    landed(std::integral_constant<int, STORES>{});
+    if (padded == 2) advance();
+    step(nic, all{}, st1, st0, padded > 2 || next < hi, 1, padded > 2 ? 2 : 0);
+    for (int s = 2; s < padded; s += 2) {
+      landed(none{});
+      if ((s & 63) == 0) {
+        weight_scales(ce, cn0, s, swg, swu);
+        asm volatile("" ::"v"(swg), "v"(swu));
+      }
+      const bool last = s + 2 == padded;
+      step(nic, all{}, st0, st1, s + 1 < steps, s, s + 1);  // an odd count's last step: zeros
+      landed(none{});
+      if (last) advance();
+      step(nic, all{}, st1, st0, !last || next < hi, s + 1, last ? 0 : s + 2);
     }
     // ---- epilogue
     const int lane = lane_id, g = lane >> 4, q = lane & 15;
+    auto next_loads = [&]() __attribute__((always_inline)) {
+      landed(none{});
+      swg = next_g;
+      swu = next_u;
+      set_step(1, next < hi && steps > 1);
+#pragma unroll
+      for (int v = 0; v < LOADS; ++v) load(v, st1);
+      asm volatile("" ::: "memory");
+    };
+    // Stores of rows and columns outside go out of range, so that their count is fixed.
     if constexpr (GU) {
       const int NBo = (P.N + 127) / 128;
+      const rsrc_t rq = make_rsrc(P.aq + static_cast<int64_t>(crow0) * P.N, static_cast<int64_t>(cvalid) * P.N);
+      const rsrc_t rm = make_rsrc(P.sout + static_cast<int64_t>(crow0) * NBo, static_cast<int64_t>(cvalid) * NBo * 4);
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
+      for (int i = 0; i < NI; ++i) {
         float m = 0.0f;
 #pragma unroll
         for (int j = 0; j < 2; ++j)
@@ -354,43 +379,71 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
         m = fmaxf(m, __shfl_xor(m, 32, kWave));
         if (g == 0) amax[wm * (BM / 2) + i * 16 + q][wn] = m;
       }
-      landed();
+      next_loads();
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const int r = wm * (BM / 2) + i * 16 + q;
-        if (r >= cvalid) continue;
-        const float m = fmaxf(fmaxf(amax[r][0], amax[r][1]), fmaxf(amax[r][2], amax[r][3]));
-        float up;
-        const float f = code_factor(m, up);
-        const int n = cn0 + wn * 32 + 8 * g;
-        const int64_t p = crow0 + r;
-        if (n < P.N) {
+        uint2 codes = make_uint2(0, 0);
+        float m = 0.0f;
+        if (i < NI) {
+          m = fmaxf(fmaxf(amax[r][0], amax[r][1]), fmaxf(amax[r][2], amax[r][3]));
+          float up;
+          const float f = code_factor(m, up);
           const float v0[4] = {acc[i][0][0], acc[i][0][1], acc[i][0][2], acc[i][0][3]};
           const float v1[4] = {acc[i][1][0], acc[i][1][1], acc[i][1][2], acc[i][1][3]};
-          *reinterpret_cast<uint2*>(P.aq + p * P.N + n) = make_uint2(codes4(v0, up, f), codes4(v1, up, f));
+          codes = make_uint2(codes4(v0, up, f), codes4(v1, up, f));
         }
-        if (wn == 0 && g == 0) P.sout[p * NBo + cn0 / 128] = m / 448.0f;
+        const int n = cn0 + wn * 32 + 8 * g;
+        const bool row = i < NI && r < cvalid;
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{codes.x, codes.y}, rq,
+                                              row && n < P.N ? static_cast<uint32_t>(r) * P.N + n : kOutside, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b32(
+            __float_as_uint(m / 448.0f), rm,
+            row && wn == 0 && g == 0 ? (static_cast<uint32_t>(r) * NBo + cn0 / 128) * 4 : kOutside, 0, 0);
       }
     } else {
-      landed();
+      const rsrc_t ro = make_rsrc(P.out + static_cast<int64_t>(crow0) * P.N, static_cast<int64_t>(cvalid) * P.N * 2);
+      float w[NI];
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int r = wm * (BM / 2) + i * 16 + q;
+        w[i] = P.row_weight && r < cvalid ? P.row_weight[crow0 + r] : 1.0f;
+      }
+      next_loads();
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const int r = wm * (BM / 2) + i * 16 + q;
-        if (r >= cvalid) continue;
-        const int64_t p = crow0 + r;
-        const float w = P.row_weight ? P.row_weight[p] : 1.0f;
-        const int n = cn0 + wn * 64 + 16 * g;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if (n + 8 * h >= P.N) continue;
-          const f32x4 u = acc[i][2 * h], v = acc[i][2 * h + 1];
-          *reinterpret_cast<uint4*>(P.out + p * P.N + n + 8 * h) =
-              make_uint4(pack_bf16x2(w * u[0], w * u[1]), pack_bf16x2(w * u[2], w * u[3]),
-                         pack_bf16x2(w * v[0], w * v[1]), pack_bf16x2(w * v[2], w * v[3]));
+          const int n = cn0 + wn * 64 + 32 * h + 8 * g;
+          u32x4 o{};
+          if (i < NI) {
+            const f32x4 u = acc[i][2 * h], v = acc[i][2 * h + 1];
+            const float x = w[i < NI ? i : 0];
+            o = u32x4{pack_bf16x2(x * u[0], x * u[1]), pack_bf16x2(x * u[2], x * u[3]),
+                      pack_bf16x2(x * v[0], x * v[1]), pack_bf16x2(x * v[2], x * v[3])};
+          }
+          __builtin_amdgcn_raw_buffer_store_b128(
+              o, ro, i < NI && r < cvalid && n < P.N ? (static_cast<uint32_t>(r) * P.N + n) * 2 : kOutside, 0, 0);
         }
       }
     }
     L = next;
+  };
+
+  if (L >= hi) return;
+  set_tile(L);
+  weight_scales(e, n0, 0, swg, swu);
+  set_step(0, true);
+#pragma unroll
+  for (int v = 0; v < LOADS; ++v) load(v, st0);
+  set_step(1, steps > 1);
+#pragma unroll
+  for (int v = 0; v < LOADS; ++v) load(v, st1);
+  landed(none{});
+  while (L < hi) {
+    if (mvalid - wm * (BM / 2) > BM / 4) tile(std::integral_constant<int, FM>{});
+    else tile(std::integral_constant<int, FM / 2>{});  // half the tiles hold every row there is
   }
 }
 
