@@ -115,18 +115,36 @@ constexpr int BN = 256;
 constexpr int kBand = 8;  // row tiles that run side by side over all columns: what an XCD's workgroups read meets in its L2
 
 // GU: N columns of each of w0 and w1 (128 per tile), else N of w0 (256 per tile).
+//
+// A tile's rows come in two halves; a wavefront has half of each. Step s lives
+// in stage s % 2, and its loads leave a step and a half before they are used:
+// the weights and the first half's rows as soon as every wavefront has taken
+// step s - 2's into registers (after that step's middle barrier), the second
+// half's rows once step s - 2 has ended. In order of issue:
+//   .. | W, A0 of s+1 | A1 of s+1 | W, A0 of s+2 | A1 of s+2 | ..
+//         step s-1, 2nd  step s, 1st   step s, 2nd  step s+1, 1st half
+// so at each barrier all but the last two groups have landed.
 template <bool GU, int BM>
 __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P) {
-  constexpr int FM = BM / 32;            // 16-row tiles of a per wavefront
-  constexpr int NA = BM / 64;            // load instructions of a per wavefront and step
-  constexpr int OB = BM * KS, OS = OB + BN * KS;
+  constexpr int FM = BM / 32, HM = FM / 2;  // 16-row tiles of a per wavefront, and of those per half
+  constexpr int HA = BM / 128;              // load instructions of half a's rows per wavefront
+  constexpr int OS = BM / 2 * KS;
   constexpr int TN = GU ? BN / 2 : BN;
-  __shared__ __attribute__((aligned(1024))) uint8_t st0[OS + kThreads * 4];
-  __shared__ __attribute__((aligned(1024))) uint8_t st1[OS + kThreads * 4];
+  constexpr int G1 = HA + 1, G2 = 4 + HA + 1, STORES = 2 * FM;
+  // A stage, in three arrays, so that the compiler sees which reads follow
+  // which loads: the weights' rows; the first half's rows of a and 8 x 64 scales
+  // (waves 0 ..: rows; 6 and 7: the weights'); the second half's rows and scales.
+  __shared__ __attribute__((aligned(1024))) uint8_t w0[BN * KS];
+  __shared__ __attribute__((aligned(1024))) uint8_t w1[BN * KS];
+  __shared__ __attribute__((aligned(1024))) uint8_t x0[OS + kThreads * 4];
+  __shared__ __attribute__((aligned(1024))) uint8_t x1[OS + kThreads * 4];
+  __shared__ __attribute__((aligned(1024))) uint8_t y0[OS + kThreads * 4];
+  __shared__ __attribute__((aligned(1024))) uint8_t y1[OS + kThreads * 4];
   __shared__ int tstart[1025];
   __shared__ int eoff[1025];
   __shared__ int wsum[kWaves];
   __shared__ float amax[GU ? BM : 1][4];
+  __shared__ __attribute__((aligned(256))) int per_row[kThreads];  // GU: the next tile's tokens, else this one's weights
 
   const int tid = threadIdx.x;
   const int lane_id = tid & 63;
@@ -170,92 +188,93 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
   const int hi = static_cast<int>(static_cast<int64_t>(total) * (xcd + 1) / 8);
   const int steps = KB, padded = (steps + 1) & ~1;
   const int tail = K - (steps - 1) * KS;  // k of the last step
+  int L = lo + slot;
+  if (L >= hi) return;
 
-  // Load state of the tile whose steps are being loaded, and the copy that
-  // the multiplications and the epilogue use.
-  int e = 0, row0 = 0, mvalid = 0, n0 = 0;
-  uint32_t aoff[NA], boff[4], soff = kOutside;
-  auto set_tile = [&](int L) __attribute__((always_inline)) {
+  struct Tile {
+    int e, row0, valid, n0;
+  };
+  auto find = [&](int at) __attribute__((always_inline)) {
     int l = 0, h = E - 1;
     while (l < h) {
       const int mid = (l + h + 1) >> 1;
-      if (tstart[mid] * ntn <= L) l = mid; else h = mid - 1;
+      if (tstart[mid] * ntn <= at) l = mid; else h = mid - 1;
     }
-    const int rem = L - tstart[l] * ntn, mte = tstart[l + 1] - tstart[l];
+    const int rem = at - tstart[l] * ntn, mte = tstart[l + 1] - tstart[l];
     const int band = rem / (kBand * ntn), bm = min(kBand, mte - band * kBand);
     const int nt = (rem - band * kBand * ntn) / bm, mt = band * kBand + rem - band * kBand * ntn - nt * bm;
-    const int64_t cnt = eoff[l + 1] - eoff[l];  // the expert's rows, evenly over its tiles
-    const int r0 = static_cast<int>(mt * cnt / mte);
-    e = __builtin_amdgcn_readfirstlane(l);
-    row0 = __builtin_amdgcn_readfirstlane(eoff[l] + r0);
-    mvalid = __builtin_amdgcn_readfirstlane(static_cast<int>((mt + 1) * cnt / mte) - r0);
-    n0 = __builtin_amdgcn_readfirstlane(nt * TN);
+    Tile t;
+    t.e = __builtin_amdgcn_readfirstlane(l);
+    t.row0 = __builtin_amdgcn_readfirstlane(eoff[l] + mt * BM);
+    t.valid = __builtin_amdgcn_readfirstlane(min(BM, eoff[l + 1] - eoff[l] - mt * BM));
+    t.n0 = __builtin_amdgcn_readfirstlane(nt * TN);
+    return t;
+  };
+  // The loads' state: resources of their tile, and the lane's offsets.
+  const void *pa, *pb, *ps[2];
+  int bytes_a = 0, bytes_b = 0, bytes_s[2] = {0, 0};
+  uint32_t aoff[2 * HA], boff[4], soff[2];
+  auto aim = [&](const Tile& t) __attribute__((always_inline)) {
     int lane = lane_id;  // opaque: the lane terms are recomputed here, not kept alive
     asm volatile("" : "+v"(lane));
+    const int64_t first = GU ? 0 : t.row0, rows = GU ? P.arows : t.valid;
+    bytes_a = static_cast<int>(rows * K);
+    bytes_b = P.N * K;
+    pa = P.a + first * K;
+    pb = (GU && (wave & 1) ? P.w1 : P.w0) + static_cast<int64_t>(t.e) * P.N * K;
+    bytes_s[0] = bytes_s[1] = static_cast<int>(rows * KB * 4);
+    ps[0] = ps[1] = P.sa + first * KB;
+    if (wave >= 6) {
+      const int nb = GU ? t.n0 / 128 : min(t.n0 + (wave - 6) * 128, P.N - 1) / 128;
+      bytes_s[0] = KB * 4;
+      ps[0] = (GU && wave == 7 ? P.sw1 : P.sw0) + (static_cast<int64_t>(t.e) * P.NB + nb) * KB;
+    }
 #pragma unroll
-    for (int t = 0; t < NA; ++t) {
-      const int r = (wave * NA + t) * 8 + (lane >> 3);
+    for (int i = 0; i < 2 * HA; ++i) {
+      const int r = (i / HA) * (BM / 2) + (wave * HA + i % HA) * 8 + (lane >> 3);
       const int c = (lane & 7) ^ ((r >> 1) & 7);
-      const int row = GU ? (r < mvalid ? P.row_token[row0 + r] : 0) : r;
-      aoff[t] = r < mvalid ? static_cast<uint32_t>(row) * K + c * 16 : kOutside;
-    }
-    {
-      const int r = wave * 64 + lane;
-      const int row = GU ? (r < mvalid ? P.row_token[row0 + r] : 0) : r;
-      soff = r < mvalid ? static_cast<uint32_t>(row) * KB * 4 : kOutside;  // behind the tile's rows: zeros
+      const int row = GU ? (r < t.valid ? per_row[r] : 0) : r;
+      aoff[i] = r < t.valid ? static_cast<uint32_t>(row) * K + c * 16 : kOutside;
     }
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int r = (wave * 4 + t) * 8 + (lane >> 3);
+    for (int h = 0; h < 2; ++h) {
+      const int r = h * (BM / 2) + wave * 64 + lane;
+      const bool in = wave < BM / 128 && r < t.valid;
+      const int row = GU ? (in ? per_row[r] : 0) : r;
+      soff[h] = in ? static_cast<uint32_t>(row) * KB * 4 : kOutside;
+    }
+    if (wave >= 6 && lane == 0) soff[0] = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = (wave * 4 + i) * 8 + (lane >> 3);
       const int c = (lane & 7) ^ ((r >> 1) & 7);
       const int j = (r >> 4) & 3, q = r & 15;
-      const int n = n0 + (r >> 6) * (GU ? 32 : 64) + (GU ? 0 : (j >> 1) * 32) + 8 * (q >> 2) + 4 * (j & 1) + (q & 3);
-      boff[t] = n < P.N ? static_cast<uint32_t>(n) * K + c * 16 : kOutside;
+      const int n = t.n0 + (r >> 6) * (GU ? 32 : 64) + (GU ? 0 : (j >> 1) * 32) + 8 * (q >> 2) + 4 * (j & 1) + (q & 3);
+      boff[i] = n < P.N ? static_cast<uint32_t>(n) * K + c * 16 : kOutside;
     }
   };
-  // Load instruction v of a step: a rows, weight rows, scales. Every wavefront
-  // issues every one in every step (a branch in the loop costs more than the
+  // Load instruction v of step s into stage S, of the first (weights, rows,
+  // scales) or the second half's group (rows, scales). Every wavefront issues
+  // every one in every step (a branch in the loop costs more than the
   // instruction): without a step to load the ranges are empty, and the chunks
   // past a row's end lie outside; both read zeros.
-  constexpr int LOADS = NA + 5;
-  rsrc_t ra, rb, rs;
-  bool in[2];  // the lane's chunk of even and odd blocks of 8 rows ends before the row does
-  auto set_step = [&](int s, bool loads) __attribute__((always_inline)) {
-    const int64_t k0 = static_cast<int64_t>(s) * KS;
-    const int64_t arows = !loads ? 0 : GU ? P.arows : mvalid, wrows = loads ? P.N : 0;
-    const int64_t first = GU ? 0 : row0;
-    ra = make_rsrc(P.a + first * K + k0, max(arows * K - k0, int64_t{0}));
-    rs = make_rsrc(P.sa + first * KB + s, max((arows * KB - s) * 4, int64_t{0}));
-    rb = make_rsrc((GU && (wave & 1) ? P.w1 : P.w0) + static_cast<int64_t>(e) * P.N * K + k0,
-                   max(wrows * K - k0, int64_t{0}));
-    const int limit = s == steps - 1 ? tail : KS;
-    const int c = (lane_id & 7) ^ (lane_id >> 4);
-    in[0] = c * 16 < limit;
-    in[1] = (c ^ 4) * 16 < limit;
+  typedef __attribute__((address_space(3))) void* lds_ptr;
+  auto chunk_offset = [&](bool odd, uint32_t off, int s) __attribute__((always_inline)) {
+    const int c = (lane_id & 7) ^ (lane_id >> 4) ^ (odd ? 4 : 0);  // in blocks of 8 rows, even and odd ones
+    return c * 16 < (s == steps - 1 ? tail : KS) ? off : kOutside;
   };
-  auto load = [&](int v, uint8_t* S) __attribute__((always_inline)) {
-    typedef __attribute__((address_space(3))) void* lds_ptr;
-    if (v == LOADS - 1) {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)(S + OS + wave * 256), 4, soff, 0, 0, 0);
+  auto load = [&](int h, int v, uint8_t* S, uint8_t* W, int s, bool live) __attribute__((always_inline)) {
+    if (v == (h ? G1 : G2) - 1) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(ps[h], live ? bytes_s[h] : 0), (lds_ptr)(S + OS + wave * 256), 4,
+                                               soff[h], s * 4, 0, 0);
       return;
     }
-    const bool is_a = v < NA;
-    const int blk = is_a ? wave * NA + v : wave * 4 + (v - NA);
-    const uint32_t off = is_a ? aoff[v < NA ? v : 0] : boff[v < NA ? 0 : v - NA];
-    const bool even = ((is_a ? v : v - NA) & 1) == 0;  // NA and 4 are even
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(is_a ? ra : rb, (lds_ptr)(S + (is_a ? 0 : OB) + blk * 1024), 16,
-                                             in[even ? 0 : 1] ? off : kOutside, 0, 0, 0);
-  };
-
-  // lane l: the weight scales of step l (of the current 64) for the tile in
-  // work and for the next one.
-  float swg = 0.0f, swu = 0.0f, next_g = 0.0f, next_u = 0.0f;
-  auto weight_scales = [&](int we, int wn0, int s, float& g, float& u) __attribute__((always_inline)) {
-    const int b = min(s + lane_id, KB - 1);
-    const int nb = GU ? wn0 / 128 : min(wn0 + (wn >> 1) * 128, P.N - 1) / 128;
-    const int64_t at = (static_cast<int64_t>(we) * P.NB + nb) * KB + b;
-    g = P.sw0[at];
-    if constexpr (GU) u = P.sw1[at];
+    const bool weights = !h && v < 4;
+    const int i = weights ? v : h ? v : v - 4, blk = wave * (weights ? 4 : HA) + i;  // eight rows of its array
+    const uint32_t to = weights ? boff[i & 3] : aoff[(h * HA + i) % (2 * HA)];
+    const uint32_t off = chunk_offset(blk & 1, to, s);
+    const rsrc_t r = weights ? make_rsrc(pb, live ? bytes_b : 0) : make_rsrc(pa, live ? bytes_a : 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)((weights ? W : S) + blk * 1024), 16, off, s * KS, 0, 0);
   };
   // All but the last PENDING memory instructions are done, and every wavefront is here.
   auto landed = [&](auto pending) __attribute__((always_inline)) {
@@ -266,104 +285,125 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
     asm volatile("" ::: "memory");
   };
   using none = std::integral_constant<int, 0>;
+  using one = std::integral_constant<int, 1>;
+  auto row_of = [&](int i, int q) __attribute__((always_inline)) {  // of the wavefront's 16-row tile i
+    return (i / HM) * (BM / 2) + wm * (BM / 4) + (i % HM) * 16 + q;
+  };
+  auto per_row_load = [&](const void* base, int row0, int valid) __attribute__((always_inline)) {
+    const int r = wave * 64 + lane_id;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(static_cast<const char*>(base) + static_cast<int64_t>(row0) * 4,
+                                                       valid * 4),
+                                             (lds_ptr)(reinterpret_cast<char*>(per_row) + wave * 256), 4, r * 4, 0, 0, 0);
+  };
 
   f32x4 acc[FM][4];
-  // One step on stage C for the wavefront's first NI 16-row tiles; meanwhile
-  // the LD load instructions of step sn go out (into stage D), in the first
-  // half. a's fragments are read one tile ahead. The empty asm keeps the order
-  // as written: the compiler otherwise joins the steps and spills.
-  auto step = [&](auto nic, auto ldc, const uint8_t* C, uint8_t* D, bool loads, int s, int sn)
-                  __attribute__((always_inline)) {
-    constexpr int NI = decltype(nic)::value, LD = decltype(ldc)::value;
-    if constexpr (LD > 0) set_step(sn, loads);
-    int lane = lane_id;
-    asm volatile("" : "+v"(lane));
-    const int q = lane & 15, o = ((2 * (lane >> 4)) ^ ((q >> 1) & 7)) << 4;  // rows 16 apart: the same swizzle
-    auto chunk = [&](const uint8_t* p) __attribute__((always_inline)) {
-      return join(*reinterpret_cast<const u32x4*>(p + o), *reinterpret_cast<const u32x4*>(p + (o ^ 16)));
-    };
-    const uint8_t* wrow = C + OB + (wn * 64 + q) * KS;
-    const uint8_t* arow = C + (wm * (BM / 2) + q) * KS;
-    const uint8_t* srow = C + OS + (wm * (BM / 2) + q) * 4;
-    i32x8 wf[4], af[2];
-    float sr[2];
-    af[0] = chunk(arow);
-    sr[0] = *reinterpret_cast<const float*>(srow);
+  i32x8 wf[4];
+  float fg = 0.0f, fu = 0.0f;
+  // Half a step on stage C (the wavefront's 16-row tiles of half h, if NI has
+  // them), while the group of step sn goes out into stage D. a's fragments are
+  // read one tile ahead. The empty asm keeps the order as written: the
+  // compiler otherwise joins the steps and spills.
+  auto half = [&](auto nic, auto hc, const uint8_t* C, const uint8_t* CW, uint8_t* D, uint8_t* DW,
+                  int sn, bool live) __attribute__((always_inline)) {
+    constexpr int NI = decltype(nic)::value, h = decltype(hc)::value;
+    constexpr int LD = h ? G2 : G1;  // the second half of a step sends the first half's group
+    using group = std::integral_constant<int, h ? 0 : 1>;
+    if constexpr (h * HM < NI) {
+      int lane = lane_id;
+      asm volatile("" : "+v"(lane));
+      const int q = lane & 15, o = ((2 * (lane >> 4)) ^ ((q >> 1) & 7)) << 4;  // rows 16 apart: the same swizzle
+      auto chunk = [&](const uint8_t* p) __attribute__((always_inline)) {
+        return join(*reinterpret_cast<const u32x4*>(p + o), *reinterpret_cast<const u32x4*>(p + (o ^ 16)));
+      };
+      const uint8_t* wrow = CW + (wn * 64 + q) * KS;
+      const uint8_t* arow = C + (wm * (BM / 4) + q) * KS;
+      const uint8_t* srow = C + OS + (wm * (BM / 4) + q) * 4;
+      i32x8 af[2];
+      float sr[2];
+      af[0] = chunk(arow);
+      sr[0] = *reinterpret_cast<const float*>(srow);
+      if constexpr (h == 0) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) wf[j] = chunk(wrow + j * 16 * KS);
-    const float fg = lane_value(swg, s & 63), fu = GU ? lane_value(swu, s & 63) : 0.0f;
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      if (i + 1 < NI) {
-        af[(i + 1) & 1] = chunk(arow + (i + 1) * 16 * KS);
-        sr[(i + 1) & 1] = *reinterpret_cast<const float*>(srow + (i + 1) * 64);
+        for (int j = 0; j < 4; ++j) wf[j] = chunk(wrow + j * 16 * KS);
+        fg = *reinterpret_cast<const float*>(C + OS + (GU ? 6 : 6 + (wn >> 1)) * 256);
+        if constexpr (GU) fu = *reinterpret_cast<const float*>(C + OS + 7 * 256);
       }
-      f32x4 pr[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) pr[j] = block_product(wf[j], af[i & 1]);
+      for (int i = 0; i < HM; ++i) {
+        if (i + 1 < HM) {
+          af[(i + 1) & 1] = chunk(arow + (i + 1) * 16 * KS);
+          sr[(i + 1) & 1] = *reinterpret_cast<const float*>(srow + (i + 1) * 64);
+        }
+        f32x4 pr[4];
 #pragma unroll
-      for (int v = min(LD, i * LD * 2 / NI); v < min(LD, (i + 1) * LD * 2 / NI); ++v) load(v, D);
-      const float s0 = sr[i & 1] * fg, s1 = GU ? sr[i & 1] * fu : s0;
+        for (int j = 0; j < 4; ++j) pr[j] = block_product(wf[j], af[i & 1]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+        for (int v = i * LD / HM; v < (i + 1) * LD / HM; ++v) load(group::value, v, D, DW, sn, live);
+        const float s0 = sr[i & 1] * fg, s1 = GU ? sr[i & 1] * fu : s0;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) acc[i][j][x] = fmaf(j < 2 ? s0 : s1, pr[j][x], acc[i][j][x]);
-      __builtin_amdgcn_sched_barrier(0);
-      asm volatile("" : "+v"(acc[i][0]), "+v"(acc[i][1]), "+v"(acc[i][2]), "+v"(acc[i][3]));
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            acc[h * HM + i][j][x] = fmaf(j < 2 ? s0 : s1, pr[j][x], acc[h * HM + i][j][x]);
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("" : "+v"(acc[h * HM + i][0]), "+v"(acc[h * HM + i][1]), "+v"(acc[h * HM + i][2]),
+                     "+v"(acc[h * HM + i][3]));
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < LD; ++v) load(group::value, v, D, DW, sn, live);
     }
   };
 
-  // One tile. On entry step 0 is in st0 and step 1 is on its way to st1,
-  // ahead of STORES stores of the tile before: those run on under two steps.
-  constexpr int STORES = 2 * FM;
-  int L = lo + slot;
+  Tile now = find(L), nx = now;
   auto tile = [&](auto nic) __attribute__((always_inline)) {
     constexpr int NI = decltype(nic)::value;
-    using all = std::integral_constant<int, LOADS>;
-    const int ce = e, crow0 = row0, cvalid = mvalid, cn0 = n0;
     const int next = L + nslots;
+    const bool more = next < hi;
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{};
-    auto advance = [&]() __attribute__((always_inline)) {
-      if (next < hi) {
-        set_tile(next);
-        weight_scales(e, n0, 0, next_g, next_u);
-      }
-    };
-    step(nic, none{}, st0, st1, false, 0, 0);
-    landed(std::integral_constant<int, STORES>{});
-    if (padded == 2) advance();
-    step(nic, all{}, st1, st0, padded > 2 || next < hi, 1, padded > 2 ? 2 : 0);
-    for (int s = 2; s < padded; s += 2) {
-      landed(none{});
-      if ((s & 63) == 0) {
-        weight_scales(ce, cn0, s, swg, swu);
-        asm volatile("" ::"v"(swg), "v"(swu));
-      }
+    // Steps s (x0, y0) and s + 1 (x1, y1). From the middle of the last
+    // pair on the loads are the next tile's.
+    auto pair = [&](auto firstc, int s) __attribute__((always_inline)) {
+      constexpr bool first = decltype(firstc)::value != 0;
+      using pending = std::integral_constant<int, G1 + G2 + (first ? STORES : 0)>;
       const bool last = s + 2 == padded;
-      step(nic, all{}, st0, st1, s + 1 < steps, s, s + 1);  // an odd count's last step: zeros
-      landed(none{});
-      if (last) advance();
-      step(nic, all{}, st1, st0, !last || next < hi, s + 1, last ? 0 : s + 2);
-    }
-    // ---- epilogue
-    const int lane = lane_id, g = lane >> 4, q = lane & 15;
-    auto next_loads = [&]() __attribute__((always_inline)) {
-      landed(none{});
-      swg = next_g;
-      swu = next_u;
-      set_step(1, next < hi && steps > 1);
-#pragma unroll
-      for (int v = 0; v < LOADS; ++v) load(v, st1);
-      asm volatile("" ::: "memory");
+      half(nic, none{}, x0, w0, y1, nullptr, s + 1, s + 1 < steps);  // an odd count's last step: zeros
+      landed(pending{});
+      if constexpr (first) {
+        if constexpr (GU) {
+          if (more) {
+            nx = find(next);
+            per_row_load(P.row_token, nx.row0, nx.valid);
+          }
+        } else if (P.row_weight != nullptr) {
+          per_row_load(P.row_weight, now.row0, now.valid);
+        }
+      }
+      if (last && more) {
+        if constexpr (!GU) nx = find(next);
+        if (GU && first) landed(none{});  // a reduction of one pair: the tokens were only just sent for
+        aim(nx);
+      }
+      half(nic, one{}, y0, nullptr, x0, w0, last ? 0 : s + 2, last ? more : s + 2 < steps);
+      landed(pending{});
+      half(nic, none{}, x1, w1, y0, nullptr, last ? 0 : s + 2, last ? more : s + 2 < steps);
+      landed(std::integral_constant<int, G1 + G2>{});
+      half(nic, one{}, y1, nullptr, x1, w1, last ? 1 : s + 3, last ? more && steps > 1 : s + 3 < steps);
+      landed(std::integral_constant<int, G1 + G2>{});
     };
-    // Stores of rows and columns outside go out of range, so that their count is fixed.
+    pair(one{}, 0);
+    for (int s = 2; s < padded; s += 2) pair(none{}, s);
+    // ---- epilogue; stores of rows and columns outside go out of range, so
+    // that their count is fixed: they run on under the next tile's first step.
+    const int lane = lane_id, g = lane >> 4, q = lane & 15;
+    const int row0 = now.row0, valid = now.valid, n0 = now.n0;
     if constexpr (GU) {
       const int NBo = (P.N + 127) / 128;
-      const rsrc_t rq = make_rsrc(P.aq + static_cast<int64_t>(crow0) * P.N, static_cast<int64_t>(cvalid) * P.N);
-      const rsrc_t rm = make_rsrc(P.sout + static_cast<int64_t>(crow0) * NBo, static_cast<int64_t>(cvalid) * NBo * 4);
+      const rsrc_t rq = make_rsrc(P.aq + static_cast<int64_t>(row0) * P.N, static_cast<int64_t>(valid) * P.N);
+      const rsrc_t rm = make_rsrc(P.sout + static_cast<int64_t>(row0) * NBo, static_cast<int64_t>(valid) * NBo * 4);
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         float m = 0.0f;
@@ -377,12 +417,15 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
           }
         m = fmaxf(m, __shfl_xor(m, 16, kWave));
         m = fmaxf(m, __shfl_xor(m, 32, kWave));
-        if (g == 0) amax[wm * (BM / 2) + i * 16 + q][wn] = m;
+        if (g == 0) amax[row_of(i, q)][wn] = m;
       }
-      next_loads();
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
-        const int r = wm * (BM / 2) + i * 16 + q;
+        const int r = row_of(i, q);
         uint2 codes = make_uint2(0, 0);
         float m = 0.0f;
         if (i < NI) {
@@ -393,57 +436,53 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
           const float v1[4] = {acc[i][1][0], acc[i][1][1], acc[i][1][2], acc[i][1][3]};
           codes = make_uint2(codes4(v0, up, f), codes4(v1, up, f));
         }
-        const int n = cn0 + wn * 32 + 8 * g;
-        const bool row = i < NI && r < cvalid;
+        const int n = n0 + wn * 32 + 8 * g;
+        const bool row = i < NI && r < valid;
         __builtin_amdgcn_raw_buffer_store_b64(u32x2{codes.x, codes.y}, rq,
                                               row && n < P.N ? static_cast<uint32_t>(r) * P.N + n : kOutside, 0, 0);
         __builtin_amdgcn_raw_buffer_store_b32(
             __float_as_uint(m / 448.0f), rm,
-            row && wn == 0 && g == 0 ? (static_cast<uint32_t>(r) * NBo + cn0 / 128) * 4 : kOutside, 0, 0);
+            row && wn == 0 && g == 0 ? (static_cast<uint32_t>(r) * NBo + n0 / 128) * 4 : kOutside, 0, 0);
       }
     } else {
-      const rsrc_t ro = make_rsrc(P.out + static_cast<int64_t>(crow0) * P.N, static_cast<int64_t>(cvalid) * P.N * 2);
-      float w[NI];
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int r = wm * (BM / 2) + i * 16 + q;
-        w[i] = P.row_weight && r < cvalid ? P.row_weight[crow0 + r] : 1.0f;
-      }
-      next_loads();
+      const rsrc_t ro = make_rsrc(P.out + static_cast<int64_t>(row0) * P.N, static_cast<int64_t>(valid) * P.N * 2);
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
-        const int r = wm * (BM / 2) + i * 16 + q;
+        const int r = row_of(i, q);
+        const float x = P.row_weight != nullptr ? __int_as_float(per_row[r]) : 1.0f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const int n = cn0 + wn * 64 + 32 * h + 8 * g;
+          const int n = n0 + wn * 64 + 32 * h + 8 * g;
           u32x4 o{};
           if (i < NI) {
             const f32x4 u = acc[i][2 * h], v = acc[i][2 * h + 1];
-            const float x = w[i < NI ? i : 0];
             o = u32x4{pack_bf16x2(x * u[0], x * u[1]), pack_bf16x2(x * u[2], x * u[3]),
                       pack_bf16x2(x * v[0], x * v[1]), pack_bf16x2(x * v[2], x * v[3])};
           }
           __builtin_amdgcn_raw_buffer_store_b128(
-              o, ro, i < NI && r < cvalid && n < P.N ? (static_cast<uint32_t>(r) * P.N + n) * 2 : kOutside, 0, 0);
+              o, ro, i < NI && r < valid && n < P.N ? (static_cast<uint32_t>(r) * P.N + n) * 2 : kOutside, 0, 0);
         }
       }
     }
+    now = nx;
     L = next;
   };
 
-  if (L >= hi) return;
-  set_tile(L);
-  weight_scales(e, n0, 0, swg, swu);
-  set_step(0, true);
+  if constexpr (GU) {
+    per_row_load(P.row_token, now.row0, now.valid);
+    landed(none{});
+  }
+  aim(now);
 #pragma unroll
-  for (int v = 0; v < LOADS; ++v) load(v, st0);
-  set_step(1, steps > 1);
+  for (int v = 0; v < G2; ++v) load(0, v, x0, w0, 0, true);
 #pragma unroll
-  for (int v = 0; v < LOADS; ++v) load(v, st1);
+  for (int v = 0; v < G1; ++v) load(1, v, y0, nullptr, 0, true);
+#pragma unroll
+  for (int v = 0; v < G2; ++v) load(0, v, x1, w1, 1, steps > 1);
   landed(none{});
   while (L < hi) {
-    if (mvalid - wm * (BM / 2) > BM / 4) tile(std::integral_constant<int, FM>{});
-    else tile(std::integral_constant<int, FM / 2>{});  // half the tiles hold every row there is
+    if (now.valid > BM / 2) tile(std::integral_constant<int, FM>{});
+    else tile(std::integral_constant<int, HM>{});  // the first half holds every row
   }
 }
 
