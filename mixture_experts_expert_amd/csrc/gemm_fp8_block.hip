@@ -211,24 +211,22 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
     return t;
   };
   // The loads' state: resources of their tile, and the lane's offsets.
-  const void *pa, *pb, *ps[2];
-  int bytes_a = 0, bytes_b = 0, bytes_s[2] = {0, 0};
+  rsrc_t ra, rb, rs;
   uint32_t aoff[2 * HA], boff[4], soff[2];
   auto aim = [&](const Tile& t) __attribute__((always_inline)) {
     int lane = lane_id;  // opaque: the lane terms are recomputed here, not kept alive
     asm volatile("" : "+v"(lane));
     const int64_t first = GU ? 0 : t.row0, rows = GU ? P.arows : t.valid;
-    bytes_a = static_cast<int>(rows * K);
-    bytes_b = P.N * K;
-    pa = P.a + first * K;
-    pb = (GU && (wave & 1) ? P.w1 : P.w0) + static_cast<int64_t>(t.e) * P.N * K;
-    bytes_s[0] = bytes_s[1] = static_cast<int>(rows * KB * 4);
-    ps[0] = ps[1] = P.sa + first * KB;
+    ra = make_rsrc(P.a + first * K, rows * K);
+    rb = make_rsrc((GU && (wave & 1) ? P.w1 : P.w0) + static_cast<int64_t>(t.e) * P.N * K, static_cast<int64_t>(P.N) * K);
+    const float* scales = P.sa + first * KB;
+    int64_t n_scales = rows * KB;
     if (wave >= 6) {
       const int nb = GU ? t.n0 / 128 : min(t.n0 + (wave - 6) * 128, P.N - 1) / 128;
-      bytes_s[0] = KB * 4;
-      ps[0] = (GU && wave == 7 ? P.sw1 : P.sw0) + (static_cast<int64_t>(t.e) * P.NB + nb) * KB;
+      scales = (GU && wave == 7 ? P.sw1 : P.sw0) + (static_cast<int64_t>(t.e) * P.NB + nb) * KB;
+      n_scales = KB;
     }
+    rs = make_rsrc(scales, n_scales * 4);
 #pragma unroll
     for (int i = 0; i < 2 * HA; ++i) {
       const int r = (i / HA) * (BM / 2) + (wave * HA + i % HA) * 8 + (lane >> 3);
@@ -253,28 +251,25 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
       boff[i] = n < P.N ? static_cast<uint32_t>(n) * K + c * 16 : kOutside;
     }
   };
-  // Load instruction v of step s into stage S, of the first (weights, rows,
-  // scales) or the second half's group (rows, scales). Every wavefront issues
-  // every one in every step (a branch in the loop costs more than the
-  // instruction): without a step to load the ranges are empty, and the chunks
-  // past a row's end lie outside; both read zeros.
+  // Load instruction v of step s, of the first (weights W, rows, scales) or the
+  // second half's group (rows, scales). Every wavefront issues every one in
+  // every step (a branch in the loop costs more than the instruction): chunks
+  // past a row's end, and all of a step that is not there, lie outside and
+  // read zeros.
   typedef __attribute__((address_space(3))) void* lds_ptr;
-  auto chunk_offset = [&](bool odd, uint32_t off, int s) __attribute__((always_inline)) {
-    const int c = (lane_id & 7) ^ (lane_id >> 4) ^ (odd ? 4 : 0);  // in blocks of 8 rows, even and odd ones
-    return c * 16 < (s == steps - 1 ? tail : KS) ? off : kOutside;
-  };
   auto load = [&](int h, int v, uint8_t* S, uint8_t* W, int s, bool live) __attribute__((always_inline)) {
     if (v == (h ? G1 : G2) - 1) {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(ps[h], live ? bytes_s[h] : 0), (lds_ptr)(S + OS + wave * 256), 4,
-                                               soff[h], s * 4, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)(S + OS + wave * 256), 4, live ? soff[h] : kOutside, s * 4, 0,
+                                               0);
       return;
     }
     const bool weights = !h && v < 4;
     const int i = weights ? v : h ? v : v - 4, blk = wave * (weights ? 4 : HA) + i;  // eight rows of its array
     const uint32_t to = weights ? boff[i & 3] : aoff[(h * HA + i) % (2 * HA)];
-    const uint32_t off = chunk_offset(blk & 1, to, s);
-    const rsrc_t r = weights ? make_rsrc(pb, live ? bytes_b : 0) : make_rsrc(pa, live ? bytes_a : 0);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)((weights ? W : S) + blk * 1024), 16, off, s * KS, 0, 0);
+    const int c = (lane_id & 7) ^ (lane_id >> 4) ^ ((blk & 1) * 4);
+    const uint32_t off = c * 16 < (!live ? 0 : s == steps - 1 ? tail : KS) ? to : kOutside;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(weights ? rb : ra, (lds_ptr)((weights ? W : S) + blk * 1024), 16, off, s * KS,
+                                             0, 0);
   };
   // All but the last PENDING memory instructions are done, and every wavefront is here.
   auto landed = [&](auto pending) __attribute__((always_inline)) {
@@ -328,26 +323,35 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
         fg = *reinterpret_cast<const float*>(C + OS + (GU ? 6 : 6 + (wn >> 1)) * 256);
         if constexpr (GU) fu = *reinterpret_cast<const float*>(C + OS + 7 * 256);
       }
+      f32x4 pr[2][4];
+      float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-      for (int i = 0; i < HM; ++i) {
+      for (int i = 0; i <= HM; ++i) {
         if (i + 1 < HM) {
           af[(i + 1) & 1] = chunk(arow + (i + 1) * 16 * KS);
           sr[(i + 1) & 1] = *reinterpret_cast<const float*>(srow + (i + 1) * 64);
         }
-        f32x4 pr[4];
+        const float f = i > 0 ? s0 : 0.0f, f1 = i > 0 ? s1 : 0.0f;
+        if (i < HM) {
+          s0 = sr[i & 1] * fg;
+          s1 = GU ? sr[i & 1] * fu : s0;
+        }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) pr[j] = block_product(wf[j], af[i & 1]);
+        for (int j = 0; j < 4; ++j) {
+          if (i < HM) pr[i & 1][j] = block_product(wf[j], af[i & 1]);
+          if (i > 0)
 #pragma unroll
-        for (int v = i * LD / HM; v < (i + 1) * LD / HM; ++v) load(group::value, v, D, DW, sn, live);
-        const float s0 = sr[i & 1] * fg, s1 = GU ? sr[i & 1] * fu : s0;
+            for (int x = 0; x < 4; ++x)
+              acc[h * HM + i - 1][j][x] = fmaf(j < 2 ? f : f1, pr[(i - 1) & 1][j][x], acc[h * HM + i - 1][j][x]);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (i < HM)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            acc[h * HM + i][j][x] = fmaf(j < 2 ? s0 : s1, pr[j][x], acc[h * HM + i][j][x]);
+          for (int v = i * LD / HM; v < (i + 1) * LD / HM; ++v) load(group::value, v, D, DW, sn, live);
         __builtin_amdgcn_sched_barrier(0);
-        asm volatile("" : "+v"(acc[h * HM + i][0]), "+v"(acc[h * HM + i][1]), "+v"(acc[h * HM + i][2]),
-                     "+v"(acc[h * HM + i][3]));
+        if (i > 0)
+          asm volatile("" : "+v"(acc[h * HM + i - 1][0]), "+v"(acc[h * HM + i - 1][1]), "+v"(acc[h * HM + i - 1][2]),
+                       "+v"(acc[h * HM + i - 1][3]));
       }
     } else {
 #pragma unroll
