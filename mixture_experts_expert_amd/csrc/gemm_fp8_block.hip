@@ -492,16 +492,24 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
 
 // ---- few rows per expert ----------------------------------------------------
 
-constexpr int kTiles = 4;  // 16-row tiles of a per pass over the weights
+constexpr int kTiles = 2;  // 16-row tiles of a per pass over the weights
 
 // One workgroup: expert e, and 16 columns per wavefront of w0 and w1 (GU), or
 // (kWaves / ks) * 16 columns of w0, each split over ks wavefronts along k.
+//
+// Eight lanes load a row's 128 bytes of a step (loads whose neighbouring lanes
+// are in different rows take four times the address cycles), AHEAD steps ahead
+// into registers; a wavefront's own piece of LDS turns them into fragments.
+// Every load is issued in every step, outside the matrix where there is
+// nothing to load: behind a condition the compiler waits for all of them.
 template <bool GU, int AHEAD>
 __global__ __launch_bounds__(kThreads, 2) void block_stream_kernel(const Params P, int ks, int groups) {
   __shared__ __attribute__((aligned(16))) float red[kWaves][16][20];
+  __shared__ __attribute__((aligned(16))) uint8_t stage[kWaves][GU ? 3 : 2][16 * KS];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int q = lane & 15, g = lane >> 4;
+  const int lr = lane >> 3, lc = lane & 7;  // as a loader: row, chunk
   const int e = blockIdx.x / groups, grp = blockIdx.x - e * groups;
   const int first = P.offsets ? P.offsets[e] : 0;
   const int rows = (P.offsets ? P.offsets[e + 1] : P.M) - first;
@@ -513,79 +521,114 @@ __global__ __launch_bounds__(kThreads, 2) void block_stream_kernel(const Params 
   const int64_t wbytes = static_cast<int64_t>(N) * K;
   const rsrc_t r0 = make_rsrc(P.w0 + e * wbytes, wbytes);
   const rsrc_t r1 = make_rsrc((GU ? P.w1 : P.w0) + e * wbytes, wbytes);
-  const uint32_t woff = n0 + q < N ? static_cast<uint32_t>(n0 + q) * K : kOutside;
   const int64_t srow = (static_cast<int64_t>(e) * P.NB + min(n0, N - 1) / 128) * KB;
-  auto chunk = [&](const rsrc_t& r, uint32_t row, int s) -> i32x8 {
-    const int k = s * KS + 32 * g;
-    const u32x4 lo = __builtin_amdgcn_raw_buffer_load_b128(r, row != kOutside && k < K ? row + k : kOutside, 0, 0);
-    const u32x4 hi =
-        __builtin_amdgcn_raw_buffer_load_b128(r, row != kOutside && k + 16 < K ? row + k + 16 : kOutside, 0, 0);
-    return join(lo, hi);
+  const rsrc_t rs0 = make_rsrc(P.sw0 + srow, KB * 4), rs1 = make_rsrc((GU ? P.sw1 : P.sw0) + srow, KB * 4);
+  uint32_t woff[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    woff[i] = n0 + lr + 8 * i < N ? static_cast<uint32_t>(n0 + lr + 8 * i) * K + lc * 16 : kOutside;
+  auto b128 = [&](const rsrc_t& r, uint32_t off) __attribute__((always_inline)) {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+  };
+  // A row's chunk of step s: outside past the wavefront's steps and the row's end.
+  auto at = [&](uint32_t off, int s) __attribute__((always_inline)) {
+    return s < s1 && s * KS + lc * 16 < K ? off + s * KS : kOutside;
+  };
+  struct Step {
+    u32x4 w0[2], w1[GU ? 2 : 1], x[2];
+    float sw0, sw1, sx;
+  };
+  auto put = [&](uint8_t* to, const u32x4(&v)[2]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = lr + 8 * i;
+      *reinterpret_cast<u32x4*>(to + r * KS + ((lc ^ ((r >> 1) & 7)) << 4)) = v[i];
+    }
+  };
+  auto fragment = [&](const uint8_t* from) __attribute__((always_inline)) {
+    const uint8_t* p = from + q * KS;
+    const int o = ((2 * g) ^ ((q >> 1) & 7)) << 4;
+    return join(*reinterpret_cast<const u32x4*>(p + o), *reinterpret_cast<const u32x4*>(p + (o ^ 16)));
   };
   for (int p0 = 0; p0 < rows; p0 += 16 * kTiles) {
-    i32x8 w0[AHEAD], w1[AHEAD];
-#pragma unroll
-    for (int d = 0; d < AHEAD; ++d)
-      if (s0 + d < s1) {
-        w0[d] = chunk(r0, woff, s0 + d);
-        if constexpr (GU) w1[d] = chunk(r1, woff, s0 + d);
-      }
     const int tiles = min(kTiles, (rows - p0 + 15) / 16);
     const int64_t base = GU ? 0 : first + p0;
-    const int64_t left = GU ? P.arows : rows - p0;
-    const rsrc_t ra = make_rsrc(P.a + base * K, min(left, static_cast<int64_t>(GU ? P.arows : 16 * kTiles)) * K);
-    const float* sa = P.sa + base * KB;
-    uint32_t aoff[kTiles];
-    int arow[kTiles];
+    const int64_t left = GU ? P.arows : min(rows - p0, 16 * kTiles);
+    const rsrc_t ra = make_rsrc(P.a + base * K, left * K), rsa = make_rsrc(P.sa + base * KB, left * KB * 4);
+    uint32_t xoff[kTiles][2], soff[kTiles];
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
-      const int r = p0 + 16 * t + q;
-      const bool in = r < rows;
-      arow[t] = in ? (GU ? P.row_token[first + r] : r - p0) : 0;
-      aoff[t] = in ? static_cast<uint32_t>(arow[t]) * K : kOutside;
+      auto row = [&](int i) {  // i: of the 16 rows
+        const int r = p0 + 16 * t + i;
+        return r < rows ? (GU ? P.row_token[first + r] : r - p0) : -1;
+      };
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int x = row(lr + 8 * i);
+        xoff[t][i] = x >= 0 ? static_cast<uint32_t>(x) * K + lc * 16 : kOutside;
+      }
+      const int x = row(q);
+      soff[t] = x >= 0 ? static_cast<uint32_t>(x) * KB * 4 : kOutside;
     }
-    float sw0 = 0.0f, sw1 = 0.0f;
+    auto f32 = [&](const rsrc_t& r, uint32_t off) __attribute__((always_inline)) {
+      return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+    };
+    Step st[AHEAD];
+    auto fetch = [&](Step& f, int s) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        f.w0[i] = b128(r0, at(woff[i], s));
+        if constexpr (GU) f.w1[i] = b128(r1, at(woff[i], s));
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) f.x[i] = b128(ra, at(xoff[0][i], s));
+      f.sw0 = f32(rs0, s * 4);
+      if constexpr (GU) f.sw1 = f32(rs1, s * 4);
+      f.sx = f32(rsa, s < s1 ? soff[0] + s * 4 : kOutside);
+    };
     f32x4 a0[kTiles], a1[kTiles];
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) a0[t] = a1[t] = f32x4{};
-    for (int s = s0; s < s1; s += AHEAD) {
-      if ((s - s0) % 64 == 0) {
-        const int b = min(s + lane, KB - 1);
-        sw0 = P.sw0[srow + b];
-        if constexpr (GU) sw1 = P.sw1[srow + b];
-      }
-      i32x8 af[AHEAD];
-      float sf[AHEAD];
 #pragma unroll
-      for (int d = 0; d < AHEAD; ++d)
-        if (s + d < s1) {
-          af[d] = chunk(ra, aoff[0], s + d);
-          sf[d] = sa[static_cast<int64_t>(arow[0]) * KB + s + d];
-        }
+    for (int d = 0; d < AHEAD; ++d) fetch(st[d], s0 + d);
+    auto batch = [&](auto more, int s) __attribute__((always_inline)) {
 #pragma unroll
       for (int d = 0; d < AHEAD; ++d) {
-        if (s + d >= s1) break;
-        const float f0 = lane_value(sw0, (s + d - s0) % 64), f1 = GU ? lane_value(sw1, (s + d - s0) % 64) : 0.0f;
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-          if (t >= tiles) break;
-          const i32x8 x = t == 0 ? af[d] : chunk(ra, aoff[t], s + d);
-          const float sr = t == 0 ? sf[d] : sa[static_cast<int64_t>(arow[t]) * KB + s + d];
-          const f32x4 m0 = block_product(w0[d], x);
+        const float f0 = st[d].sw0, f1 = GU ? st[d].sw1 : 0.0f;
+        uint8_t* own = stage[wave][0];
+        put(own, st[d].w0);
+        if constexpr (GU) put(own + 2 * 16 * KS, st[d].w1);
+        put(own + 16 * KS, st[d].x);
+        const i32x8 wf0 = fragment(own), wf1 = GU ? fragment(own + 2 * 16 * KS) : i32x8{};
+        const float sx = st[d].sx;
+        auto tile = [&](int t, float sr) __attribute__((always_inline)) {
+          const i32x8 x = fragment(own + 16 * KS);
+          const f32x4 m0 = block_product(wf0, x);
 #pragma unroll
           for (int i = 0; i < 4; ++i) a0[t][i] = fmaf(sr * f0, m0[i], a0[t][i]);
           if constexpr (GU) {
-            const f32x4 m1 = block_product(w1[d], x);
+            const f32x4 m1 = block_product(wf1, x);
 #pragma unroll
             for (int i = 0; i < 4; ++i) a1[t][i] = fmaf(sr * f1, m1[i], a1[t][i]);
           }
+        };
+        if (s + d < s1) {  // past the steps, zeros could meet an infinite scale
+          tile(0, sx);
+#pragma unroll
+          for (int t = 1; t < kTiles; ++t) {
+            if (t >= tiles) break;
+            const u32x4 x[2] = {b128(ra, at(xoff[t][0], s + d)), b128(ra, at(xoff[t][1], s + d))};
+            const float sr = f32(rsa, soff[t] + (s + d) * 4);
+            put(own + 16 * KS, x);
+            tile(t, sr);
+          }
         }
-        if (s + d + AHEAD < s1) {
-          w0[d] = chunk(r0, woff, s + d + AHEAD);
-          if constexpr (GU) w1[d] = chunk(r1, woff, s + d + AHEAD);
-        }
+        if constexpr (decltype(more)::value) fetch(st[d], s + d + AHEAD);
       }
-    }
+    };
+    int s = s0;
+    for (; s + AHEAD < s1; s += AHEAD) batch(std::true_type{}, s);
+    batch(std::false_type{}, s);
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
       if (t >= tiles) break;
@@ -668,7 +711,7 @@ hipError_t launch(const BlockGemmArgs& a, hipStream_t st) {
     if (!GU)
       while (ks < kWaves && static_cast<int64_t>(a.E) * ceil_div(a.N, 16 * kWaves / ks) < 2 * grid && ks < P.KB) ks *= 2;
     const int groups = ceil_div(a.N, 16 * kWaves / ks);
-    block_stream_kernel<GU, 4><<<static_cast<unsigned>(a.E) * groups, kThreads, 0, st>>>(P, ks, groups);
+    block_stream_kernel<GU, 2><<<static_cast<unsigned>(a.E) * groups, kThreads, 0, st>>>(P, ks, groups);
   } else if (avg <= 96) {
     block_tile_kernel<GU, 128><<<grid, kThreads, 0, st>>>(P);
   } else {
