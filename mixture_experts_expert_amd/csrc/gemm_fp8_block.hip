@@ -701,10 +701,20 @@ hipError_t launch(const BlockGemmArgs& a, hipStream_t st) {
   P.aq = a.aq;
   P.sout = a.a_out_scale;
   const unsigned grid = static_cast<unsigned>(gemm_grid());
-  // Rows per expert, on average: up to 32 the weights' bytes bound the
-  // product; beyond 96, 256-row tiles waste less than they save.
+  // Which kernel (times in us: gate/up + down at 128 experts, 2048 x 768,
+  // unless said otherwise; evenly spread rows / rows spread as 1 / rank^1.2):
+  //  - few rows: the stream kernel. At 2 rows per expert 65 / 70 against 99 / 69
+  //    for 128-row tiles, at 4 71 / 118 against 100 / 93, at 8 71 / 219 against
+  //    99 / 105: a long expert's rows pass 32 at a time through the few
+  //    workgroups of its columns. One expert has no such skew, and few tiles
+  //    fill few CUs: at 4096 x 4096 32 rows take 9 against 34, 192 rows 30
+  //    against 41, 256 rows 38 against 41, 512 rows 73 against 43.
+  //  - 256-row tiles against 128-row ones: at 96 rows per expert 146 / 232
+  //    against 128 / 181, at 128 180 / 250 against 192 / 217, at 256 295 / 340
+  //    against 297 / 308, at 512 493 / 487 against 521 / 524.
   const int64_t avg = (a.M + a.E - 1) / a.E;
-  if (avg <= 32) {
+  const bool one = a.E == 1 && a.M <= 192 && ceil_div(a.N, GU ? BN / 2 : BN) <= 32;
+  if (avg <= 4 || a.M <= 64 || one) {
     // Enough workgroups to fill the device: split the reduction when there
     // are too few columns.
     int ks = 1;
