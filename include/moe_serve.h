@@ -55,7 +55,7 @@ moe_status moe_quantize_fp8_block_weights(int32_t E, int32_t N, int32_t K, const
  * with 0 <= offsets[0] <= ... <= offsets[E] <= M (not checked on the device);
  * rows outside [offsets[0], offsets[E]) are not written. offsets may be NULL
  * when E == 1 (every row: the dense product). row_weight [M] f32 or NULL (1).
- * M >= 0; N % 8 == 0, K % 16 == 0, E <= 1024, N K and 256 K below 2^31
+ * M >= 0; N % 8 == 0, K % 16 == 0, E <= 1024, N K, 256 K and 512 N below 2^31
  * (MOE_EUNSUPPORTED otherwise). */
 moe_status moe_gemm_fp8_block(int32_t M, int32_t E, int32_t N, int32_t K, const uint8_t* aq, const float* a_scale,
                               const int32_t* offsets, const uint8_t* wq, const float* w_scale, const float* row_weight,

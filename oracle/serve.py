@@ -1,0 +1,103 @@
+"""The serving operators (include/moe_serve.h) in 64 bits, on the CPU: block-scaled
+E4M3 operands (activations 1 x 128, weights 128 x 128) and the few-token layer."""
+import torch
+
+_POS = torch.arange(127, dtype=torch.uint8).view(torch.float8_e4m3fn).double()  # codes 0 .. 0x7E
+
+
+def e4m3_codes(v):
+    """The codes nearest to v (float64), ties to the even code; 0x7F/0xFF for NaN."""
+    a = v.abs().clamp(max=448.0)
+    a = torch.where(a.isnan(), torch.zeros_like(a), a)
+    hi = torch.searchsorted(_POS, a).clamp(max=126)  # the first code not below a
+    lo = (hi - 1).clamp(min=0)
+    below, above = a - _POS[lo], _POS[hi] - a
+    up = (above < below) | ((above == below) & (hi % 2 == 0)) | (hi == lo)
+    code = torch.where(up, hi, lo)
+    code = torch.where(v.isnan(), torch.full_like(code, 127), code)
+    return (code + 128 * torch.signbit(v)).to(torch.uint8)
+
+
+def e4m3_values(code):
+    return code.view(torch.float8_e4m3fn).double()
+
+
+def _padded(v, dim):
+    n = -v.shape[dim] % 128
+    shape = list(v.shape)
+    shape[dim] = n
+    return torch.cat([v, v.new_zeros(shape)], dim)
+
+
+def _spread(scale, dim, n):
+    return scale.double().repeat_interleave(128, dim).narrow(dim, 0, n)
+
+
+def _codes(v, amax):
+    safe = torch.where(amax > 0, amax, torch.ones_like(amax))
+    return e4m3_codes(torch.where(amax > 0, 448.0 * v / safe, torch.zeros_like(v)))
+
+
+def quantize_rows(x):
+    """x [R,K] -> codes [R,K], scale [R,ceil(K/128)] (float64)."""
+    x = x.double()
+    amax = _padded(x, 1).view(x.shape[0], -1, 128).abs().amax(2)
+    return _codes(x, _spread(amax, 1, x.shape[1])), amax / 448.0
+
+
+def quantize_weights(w):
+    """w [E,N,K] -> codes, scale [E,ceil(N/128),ceil(K/128)] (float64)."""
+    w = w.double()
+    p = _padded(_padded(w, 1), 2)
+    amax = p.view(p.shape[0], p.shape[1] // 128, 128, p.shape[2] // 128, 128).abs().amax((2, 4))
+    return _codes(w, _spread(_spread(amax, 1, w.shape[1]), 2, w.shape[2])), amax / 448.0
+
+
+def dequantize_rows(q, scale):
+    return e4m3_values(q) * _spread(scale, 1, q.shape[1])
+
+
+def dequantize_weights(q, scale):
+    return e4m3_values(q) * _spread(_spread(scale, 1, q.shape[1]), 2, q.shape[2])
+
+
+def product(a, w):
+    """a [M,K] w [N,K]^T and what the matrix core may lose of it: it adds the
+    products of 8 consecutive k aligned to the largest one's exponent and drops
+    what lies 13 bits or more below, less than 8 2^-13 times the largest."""
+    K8 = -(-a.shape[1] // 8) * 8
+    pad = lambda v: torch.cat([v, v.new_zeros(v.shape[0], K8 - v.shape[1])], 1)
+    p = pad(a)[:, None, :] * pad(w)[None, :, :]
+    return p.sum(2), p.view(*p.shape[:2], -1, 8).abs().amax(3).sum(2) * 2.0**-10
+
+
+def silu_mul(g, u):
+    return g / (1.0 + torch.exp(-g)) * u
+
+
+def route(logits, k):
+    """topk_idx, topk_w: largest first, ties to the lower index, NaN last."""
+    key = torch.where(logits.isnan(), torch.full_like(logits, float("-inf")), logits)
+    idx = torch.argsort(key, dim=1, descending=True, stable=True)
+    last = logits.isnan().gather(1, idx)
+    idx = idx.gather(1, torch.argsort(last.to(torch.int8), dim=1, stable=True))[:, :k]
+    p = torch.softmax(logits.double(), 1).gather(1, idx)
+    return idx, p / (p.sum(1, keepdim=True) + 1e-20)
+
+
+def few(x, w_router, bias, k, gate, up, down, idx=None):
+    """The layer in float64: logits, idx, w, y, and y's sum of magnitudes
+    (the scale of what rounding a can change)."""
+    x = x.double()
+    logits = x @ w_router.double().T + (bias.double() if bias is not None else 0.0)
+    chosen, w = route(logits.float(), k)
+    if idx is None:
+        idx = chosen
+    y, mag = torch.zeros_like(x), torch.zeros_like(x)
+    for t in range(x.shape[0]):
+        for j in range(k):
+            e = idx[t, j]
+            a = w[t, j] * silu_mul(gate[e].double() @ x[t], up[e].double() @ x[t])
+            y[t] += down[e].double() @ a
+            mag[t] += down[e].double().abs() @ a.abs()
+    return logits, idx, w, y, mag

@@ -1,0 +1,132 @@
+"""include/moe_serve.h on the host: every declared symbol is exported, and bad
+arguments are refused before any HIP call (no call here reaches a launch). The
+64-bit definitions the GPU tests compare with are checked against torch's own
+E4M3 conversion."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+from oracle import serve as S
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+FAKE = ctypes.c_void_p(0x1000)  # never dereferenced
+ODD = ctypes.c_void_p(0x1008)   # not 16-byte aligned
+OK, EINVAL, EUNSUPPORTED, EWORKSPACE = 0, 1, 2, 3
+
+
+@pytest.fixture(scope="module")
+def B():
+    from mixture_experts_expert_amd import binding
+    return binding
+
+
+def test_every_declared_symbol_is_exported(B):
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(ROOT, "include", "moe_serve.h")).read(), flags=re.S)
+    names = sorted(set(re.findall(r"\b(moe_[a-z0-9_]+)\s*\(", text)))
+    assert len(names) == 9, names
+    for n in names:
+        assert hasattr(B.lib, n), n
+
+
+def _with(args, at, value):
+    args = list(args)
+    args[at] = value
+    return args
+
+
+@pytest.mark.parametrize("rows,K,code", [(-1, 64, EINVAL), (4, 0, EINVAL), (4, 12, EINVAL), (1 << 30, 1 << 10, EUNSUPPORTED)])
+def test_quantize_rows_refusals(B, rows, K, code):
+    assert B.lib.moe_quantize_fp8_block_rows(rows, K, FAKE, FAKE, FAKE, None) == code
+
+
+@pytest.mark.parametrize("E,N,K,code", [(0, 8, 8, EINVAL), (1, 0, 8, EINVAL), (1, 8, 4, EINVAL), (1, 8, 1 << 23, EUNSUPPORTED),
+                                        (1 << 20, 1 << 20, 8, EUNSUPPORTED)])
+def test_quantize_weights_refusals(B, E, N, K, code):
+    assert B.lib.moe_quantize_fp8_block_weights(E, N, K, FAKE, FAKE, FAKE, None) == code
+
+
+def test_quantizer_pointers(B):
+    for i in range(3):
+        assert B.lib.moe_quantize_fp8_block_rows(4, 64, *_with([FAKE] * 3, i, None), None) == EINVAL
+        assert B.lib.moe_quantize_fp8_block_weights(1, 4, 64, *_with([FAKE] * 3, i, None), None) == EINVAL
+    for i in range(2):
+        assert B.lib.moe_quantize_fp8_block_rows(4, 64, *_with([FAKE] * 3, i, ODD), None) == EINVAL
+        assert B.lib.moe_quantize_fp8_block_weights(1, 4, 64, *_with([FAKE] * 3, i, ODD), None) == EINVAL
+
+
+GEMM = [FAKE, FAKE, FAKE, FAKE, FAKE, None, FAKE]  # aq, a_scale, offsets, wq, w_scale, row_weight, out
+
+
+@pytest.mark.parametrize("M,E,N,K,code", [
+    (-1, 2, 64, 64, EINVAL), (8, 0, 64, 64, EINVAL), (8, 2, 0, 64, EINVAL), (8, 2, 64, 0, EINVAL),
+    (8, 2, 60, 64, EUNSUPPORTED),          # N % 8
+    (8, 2, 64, 72, EUNSUPPORTED),          # K % 16
+    (8, 1025, 64, 64, EUNSUPPORTED),
+    (8, 2, 1 << 16, 1 << 15, EUNSUPPORTED),  # N K
+    (8, 2, 8, 1 << 23, EUNSUPPORTED),      # 256 K
+    (8, 2, 1 << 22, 16, EUNSUPPORTED),     # 512 N
+])
+def test_gemm_shapes(B, M, E, N, K, code):
+    assert B.lib.moe_gemm_fp8_block(M, E, N, K, *GEMM, None) == code
+
+
+def test_gemm_pointers(B):
+    call = lambda args, E=2, M=8: B.lib.moe_gemm_fp8_block(M, E, 64, 64, *args, None)
+    for i in (0, 1, 2, 3, 4, 6):
+        assert call(_with(GEMM, i, None)) == EINVAL
+    for i in (0, 3, 6):
+        assert call(_with(GEMM, i, ODD)) == EINVAL
+    assert call(_with(GEMM, 2, None), E=1, M=0) == OK  # no rows: nothing is launched, and one expert needs no offsets
+
+
+SHAPES = [((0, 64, 4, 2, 64, "bf16"), EINVAL), ((8, 64, 4, 5, 64, "bf16"), EINVAL), ((8, 64, 2000, 2, 64, "bf16"), EINVAL),
+          ((8, 96, 4, 2, 64, "bf16"), EUNSUPPORTED), ((8, 64, 4, 2, 48, "bf16"), EUNSUPPORTED),
+          ((8, 64, 4, 2, 64, "f32"), EUNSUPPORTED)]
+
+
+def _calls(B):
+    """name -> (function, pointers, first of the optional ones, has a workspace)"""
+    L = B.lib
+    return {"gate_up": (L.moe_gemm_gate_up_fp8_block, 10, None, False), "experts": (L.moe_experts_fp8_block, 22, None, True),
+            "fused": (L.moe_forward_fused_fp8_block, 25, 2, True), "few": (L.moe_forward_few, 11, 2, True),
+            "few_fp8": (L.moe_forward_few_fp8_block, 14, 2, True)}
+
+
+@pytest.mark.parametrize("name", ["gate_up", "experts", "fused", "few", "few_fp8"])
+def test_layer_refusals(B, name):
+    fn, n, optional, has_ws = _calls(B)[name]
+    tail = [1 << 40, None] if has_ws else [None]
+    for dims, code in SHAPES:
+        assert fn(B.shape(*dims), *[FAKE] * n, *tail) == code, dims
+    s = B.shape(8, 64, 4, 2, 64, "bf16")
+    for i in range(n):
+        if i != optional:
+            assert fn(s, *_with([FAKE] * n, i, None), *tail) == EINVAL, i
+    assert fn(s, *_with([FAKE] * n, 0, ODD), *tail) == EINVAL
+    if has_ws:
+        assert fn(s, *[FAKE] * n, 16, None) == EWORKSPACE
+
+
+def test_few_limits(B):
+    assert B.moe_few_workspace_bytes(B.shape(64, 64, 32, 16, 64, "bf16")) > 0
+    for dims in ((65, 64, 32, 2, 64, "bf16"), (4, 64, 32, 17, 64, "bf16")):
+        assert B.moe_few_workspace_bytes(B.shape(*dims)) == 0
+        assert B.lib.moe_forward_few(B.shape(*dims), *[FAKE] * 11, 1 << 40, None) == EUNSUPPORTED
+    need = B.moe_few_workspace_bytes(B.shape(4, 64, 32, 2, 64, "bf16"))
+    assert B.lib.moe_forward_few(B.shape(4, 64, 32, 2, 64, "bf16"), *[FAKE] * 11, need - 1, None) == EWORKSPACE
+
+
+def test_e4m3_definition():
+    v = torch.cat([torch.linspace(-448, 448, 20001), torch.randn(20000) * 0.01, S._POS.float(), -S._POS.float(),
+                   (S._POS[1:] + S._POS[:-1]).float() / 2])
+    assert torch.equal(S.e4m3_codes(v.double()), v.to(torch.float8_e4m3fn).view(torch.uint8))
+
+
+def test_route_definition():
+    inf, nan = float("inf"), float("nan")
+    idx, w = S.route(torch.tensor([[1.0, 3.0, 3.0, -inf], [nan, -inf, 2.0, nan]]), 3)
+    assert idx.tolist() == [[1, 2, 0], [2, 1, 0]]
+    assert abs(w[0].sum() - 1) < 1e-12
