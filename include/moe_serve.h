@@ -11,7 +11,7 @@
  *   prefill: moe_forward_fused_fp8_block = moe_route -> moe_experts_fp8_block
  *            moe_experts_fp8_block = moe_permute_fused ->
  *              moe_quantize_fp8_block_rows (x) -> moe_gemm_gate_up_fp8_block ->
- *              moe_gemm_fp8_block (down) -> moe_unpermute_sum
+ *              the down product -> the per-token sum
  *   decode:  moe_forward_few (bf16 weights), moe_forward_few_fp8_block
  */
 #ifndef MOE_SERVE_H_
@@ -74,8 +74,11 @@ moe_status moe_gemm_gate_up_fp8_block(moe_shape s, const uint8_t* xq, const floa
 /* The expert stage on block-scaled weights for routing that the caller
  * computed (topk_idx [T,k] in [0,E), topk_w [T,k] f32): moe_permute_fused,
  * the quantisation of x, the two GEMMs and the per-token sum (y [T,H] bf16).
- * Every buffer is caller-owned and overwritten; wq_down [E,H,I] with scales
- * [E,ceil(H/128),ceil(I/128)]; ws of ws_bytes >= moe_workspace_bytes(s). */
+ * o_perm [T*k,H], 2 bytes per element, is scratch: the rows of the down
+ * product times row_weight, eight columns to 16 bytes with a common exponent
+ * and 15 bits each, so that only y is rounded to bf16 (before, at most
+ * 2^-14 of the largest of the eight). Every buffer is caller-owned and overwritten; wq_down [E,H,I] with scales
+ * [E,ceil(H/128),ceil(I/128)]; H and I below 2^22; ws of ws_bytes >= moe_workspace_bytes(s). */
 moe_status moe_experts_fp8_block(moe_shape s, const void* x, const int32_t* topk_idx, const float* topk_w,
                                  const uint8_t* wq_gate, const float* w_gate_scale, const uint8_t* wq_up,
                                  const float* w_up_scale, const uint8_t* wq_down, const float* w_down_scale,

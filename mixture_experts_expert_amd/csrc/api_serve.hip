@@ -26,7 +26,9 @@ moe_status check_bf16_shape(const moe_shape& s) {
   if (s.T <= 0 || s.H <= 0 || s.E <= 0 || s.k <= 0 || s.I <= 0) return MOE_EINVAL;
   if (s.k > s.E || s.E > 1024 || static_cast<int64_t>(s.T) * s.k >= k2G) return MOE_EINVAL;
   if (s.dtype != MOE_BF16 || moe_workspace_bytes(s) == 0) return MOE_EUNSUPPORTED;
-  if (static_cast<int64_t>(s.T) * s.H >= k2G) return MOE_EUNSUPPORTED;
+  if (static_cast<int64_t>(s.T) * s.H >= k2G || 512 * static_cast<int64_t>(s.H) >= k2G ||
+      512 * static_cast<int64_t>(s.I) >= k2G)
+    return MOE_EUNSUPPORTED;
   return MOE_OK;
 }
 
@@ -129,10 +131,21 @@ moe_status moe_experts_fp8_block(moe_shape s, const void* x, const int32_t* topk
   if ((st = moe_gemm_gate_up_fp8_block(s, xq, x_scale, row_token, offsets, wq_gate, w_gate_scale, wq_up, w_up_scale, aq,
                                        a_scale, stream)) != MOE_OK)
     return st;
-  if ((st = moe_gemm_fp8_block(s.T * s.k, s.E, s.H, s.I, aq, a_scale, offsets, wq_down, w_down_scale, row_weight,
-                               o_perm, stream)) != MOE_OK)
-    return st;
-  return moe_unpermute_sum(s, o_perm, flat_to_sorted, y, stream);
+  moe::BlockGemmArgs g{};
+  g.M = g.arows = s.T * s.k;
+  g.E = s.E;
+  g.N = s.H;
+  g.K = s.I;
+  g.a = aq;
+  g.a_scale = a_scale;
+  g.offsets = offsets;
+  g.w0 = wq_down;
+  g.w0_scale = w_down_scale;
+  g.row_weight = row_weight;
+  g.out = o_perm;
+  g.shared8 = true;
+  if ((st = from_hip(moe::launch_gemm_fp8_block(g, stream))) != MOE_OK) return st;
+  return from_hip(moe::launch_sum_shared8(s, o_perm, flat_to_sorted, y, stream));
 }
 
 moe_status moe_forward_fused_fp8_block(moe_shape s, const void* x, const void* w_router, const float* logit_bias,

@@ -6,7 +6,7 @@
 // handles one token; each lane owns 16-byte column chunks, so every row read
 // and the output row write are contiguous across the wavefront, and a
 // token's rows are read in batches so that several are in flight at once.
-#include "moe_internal.h"
+#include "shared8.h"
 
 namespace moe {
 namespace {
@@ -42,6 +42,13 @@ template <> struct Vec<bf16_t> {
       w[i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
     return make_uint4(w[0], w[1], w[2], w[3]);
   }
+};
+
+struct shared8_t;
+template <> struct Vec<shared8_t> {  // read in that form, written as bf16
+  static constexpr int N = 8;
+  __device__ __forceinline__ static void unpack(const uint4& v, float* o) { shared8_unpack(v, o); }
+  __device__ __forceinline__ static uint4 pack(const float* o) { return Vec<bf16_t>::pack(o); }
 };
 
 // Rows of one token in flight together: a batch's row indices (and weights)
@@ -231,6 +238,10 @@ hipError_t launch_unpermute_sum(const moe_shape& s, const void* dx_perm, const i
                                 hipStream_t st) {
   return s.dtype == MOE_BF16 ? gather_sum<bf16_t, false>(s, dx_perm, nullptr, f2s, dx, st)
                              : gather_sum<float, false>(s, dx_perm, nullptr, f2s, dx, st);
+}
+
+hipError_t launch_sum_shared8(const moe_shape& s, const void* o_perm, const int32_t* f2s, void* y, hipStream_t st) {
+  return gather_sum<shared8_t, false>(s, o_perm, nullptr, f2s, y, st);
 }
 
 hipError_t launch_combine_bwd(const moe_shape& s, const void* dy, const void* o_perm, const float* w,

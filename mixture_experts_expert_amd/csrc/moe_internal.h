@@ -110,6 +110,7 @@ size_t sort_hist_bytes(const moe_shape& s);
 hipError_t launch_permute_fused_noalloc(const moe_shape& s, const int32_t* idx, const float* w, int32_t* counts,
                                         int32_t* offsets, int32_t* s2f, int32_t* f2s, int32_t* row_token,
                                         float* row_weight, hipStream_t st);
+hipError_t launch_sum_shared8(const moe_shape& s, const void* o_perm, const int32_t* f2s, void* y, hipStream_t st);
 hipError_t launch_unpermute_sum(const moe_shape& s, const void* dx_perm, const int32_t* f2s, void* dx,
                                 hipStream_t st);
 
@@ -276,6 +277,7 @@ struct BlockGemmArgs {
   const float *w0_scale, *w1_scale;
   const float* row_weight;
   void* out;
+  bool shared8;            // out in shared8.h's form, for launch_sum_shared8
   uint8_t* aq;
   float* a_out_scale;
 };

@@ -71,6 +71,18 @@ def product(a, w):
     return p.sum(2), p.view(*p.shape[:2], -1, 8).abs().amax(3).sum(2) * 2.0**-10
 
 
+def shared8_values(raw):
+    """What rows [R,N] of 2-byte elements hold, eight columns to 16 bytes with a
+    common exponent (mixture_experts_expert_amd/csrc/shared8.h)."""
+    h = raw.view(torch.int16).long().view(raw.shape[0], -1, 4, 2)
+    bit = h & 1
+    i = torch.arange(4)
+    s = ((bit[..., 0] << i) + (bit[..., 1] << (i + 4))).sum(2)[..., None, None]
+    fixed = (h >> 1).double() * torch.exp2(s.double() - 125) / 32767
+    other = (h & ~1).to(torch.int16).view(torch.bfloat16).double()
+    return torch.where(s == 255, other, fixed).reshape(raw.shape[0], -1)
+
+
 def silu_mul(g, u):
     return g / (1.0 + torch.exp(-g)) * u
 

@@ -2,7 +2,8 @@
 definitions (oracle/serve.py).
 
 Tolerances. A rounding to bf16 is off by at most 2^-8 of the value, one to E4M3
-by 2^-4 of the value or half the smallest code, 2^-10. The matrix core adds the
+by 2^-4 of the value or half the smallest code, 2^-10; one to the shared
+exponent of eight columns by 2^-14 of the largest. The matrix core adds the
 products of 8 consecutive k aligned to the largest exponent and drops what lies
 13 bits below (oracle/serve.py, product): that much is allowed on top, and 2^-20
 of the magnitudes for the fp32 sums. Products of small whole numbers lose nothing
@@ -240,6 +241,7 @@ def test_experts_stage_by_stage(T, H, E, k, I, skew):
     xd = S.dequantize_rows(xq.cpu(), xs.cpu())[rt]
     got_a = S.dequantize_rows(aq.cpu(), sa.cpu())
     gate, up, down = st["exact"]
+    od = S.shared8_values(op.cpu())
     for e in range(E):
         lo, hi = off[e], off[e + 1]
         if lo == hi:
@@ -256,11 +258,48 @@ def test_experts_stage_by_stage(T, H, E, k, I, skew):
         assert ((got_a[lo:hi] - a).abs() <= step * (1 + 2.0**-4) + 2 * da).all()
         want, lost = S.product(got_a[lo:hi], down[e])
         f = rw[lo:hi, None].double()
-        tol = (want.abs() * U + (lost + got_a[lo:hi].abs() @ down[e].abs().T * 2.0**-20) * (1 + U)) * f
-        assert ((op.cpu()[lo:hi].double() - want * f).abs() <= tol).all()
-    parts = op.cpu().double()[f2s].view(T, k, H)
+        tol = (lost + got_a[lo:hi].abs() @ down[e].abs().T * 2.0**-20) * f
+        eight = (want.abs() * f + tol).view(hi - lo, -1, 8).amax(2).repeat_interleave(8, 1)
+        assert ((od[lo:hi] - want * f).abs() <= tol + eight * 2.0**-14 * (1 + 2.0**-10)).all()
+    parts = od[f2s].view(T, k, H)
     want = parts.sum(1)
     assert ((y.cpu().double() - want).abs() <= want.abs() * U + parts.abs().sum(1) * 2.0**-20).all()
+
+
+def _experts(st, dims, idx, w, down_scale=1.0):
+    T, H, E, k, I = dims
+    s = B.shape(*dims, BF)
+    w8 = _weights(st, "fp8")
+    M, KB, IB = T * k, -(-H // 128), -(-I // 128)
+    e = lambda *n, dt=torch.float32: torch.empty(*n, dtype=dt, device="cuda")
+    i32, u8 = torch.int32, torch.uint8
+    y = e(T, H, dt=BF)
+    B.moe_experts_fp8_block(s, *dev(st["x"], idx.to(i32), w.float()), *w8.gate, *w8.up, w8.down[0], w8.down[1] * down_scale,
+                            e(E, dt=i32), e(E + 1, dt=i32), e(M, dt=i32), e(M, dt=i32), e(M, dt=i32), e(M), e(T, H, dt=u8),
+                            e(T, KB), e(M, I, dt=u8), e(M, IB), e(M, H, dt=BF), y, e(B.moe_workspace_bytes(s), dt=u8))
+    return y.cpu()
+
+
+@pytest.mark.parametrize("T", [5, 150, 500])  # each of the product's kernels
+def test_experts_range_and_not_finite(T):
+    """Powers of two on the weights' scales come out as such, near both ends of the range
+    within the coarser form there; a token with NaN or infinity touches no other."""
+    dims = (T, 192, 4, 2, 128)
+    st = _layer(*dims, 15, "fp8")
+    idx, w = S.route(torch.randn(T, 4, generator=gen(16)), 2)
+    y = _experts(st, dims, idx, w).double()
+    assert y.isfinite().all() and y.abs().max() < 8
+    for p in (-80, -13, 60):
+        assert torch.equal(_experts(st, dims, idx, w, 2.0**p).double(), y * 2.0**p)
+    big = _experts(st, dims, idx, w, 2.0**123).double() * 2.0**-123
+    # seven bits (2^-6 each) of both parts, and no more than their largest of eight
+    assert (big - y).norm() <= 2.0**-5 * y.norm()
+    assert _experts(st, dims, idx, w, 2.0**-140).abs().max() <= 2.0**-100
+    bad = torch.arange(T) % 4 == 2
+    st["x"][bad, 3] = float("nan")
+    st["x"][2, 100] = float("inf")
+    out = _experts(st, dims, idx, w).double()
+    assert out[bad].isnan().all() and torch.equal(out[~bad], y[~bad])
 
 
 # ---- the few-token layer -----------------------------------------------------
