@@ -201,6 +201,14 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
   int L = lo + slot;
   if (L >= hi) return;
 
+  // The arguments, read again where a tile begins or ends: kept in scalar
+  // registers through the loop they cost spills, whose reloads wait for every
+  // load in flight.
+  auto args = [&]() __attribute__((always_inline)) {
+    uintptr_t u = reinterpret_cast<uintptr_t>(__builtin_amdgcn_kernarg_segment_ptr());
+    asm volatile("" : "+s"(u));
+    return reinterpret_cast<const __attribute__((address_space(4))) Params*>(u);
+  };
   struct Tile {
     int e, row0, valid, n0;
   };
@@ -224,16 +232,17 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
   rsrc_t ra, rb, rs;
   uint32_t aoff[2 * HA], boff[4], soff[2];
   auto aim = [&](const Tile& t) __attribute__((always_inline)) {
+    const auto* A = args();
     int lane = lane_id;  // opaque: the lane terms are recomputed here, not kept alive
     asm volatile("" : "+v"(lane));
-    const int64_t first = GU ? 0 : t.row0, rows = GU ? P.arows : t.valid;
-    ra = make_rsrc(P.a + first * K, rows * K);
-    rb = make_rsrc((GU && (wave & 1) ? P.w1 : P.w0) + static_cast<int64_t>(t.e) * P.N * K, static_cast<int64_t>(P.N) * K);
-    const float* scales = P.sa + first * KB;
+    const int64_t first = GU ? 0 : t.row0, rows = GU ? A->arows : t.valid;
+    ra = make_rsrc(A->a + first * K, rows * K);
+    rb = make_rsrc((GU && (wave & 1) ? A->w1 : A->w0) + static_cast<int64_t>(t.e) * A->N * K, static_cast<int64_t>(A->N) * K);
+    const float* scales = A->sa + first * KB;
     int64_t n_scales = rows * KB;
     if (wave >= 6) {
-      const int nb = GU ? t.n0 / 128 : min(t.n0 + (wave - 6) * 128, P.N - 1) / 128;
-      scales = (GU && wave == 7 ? P.sw1 : P.sw0) + (static_cast<int64_t>(t.e) * P.NB + nb) * KB;
+      const int nb = GU ? t.n0 / 128 : min(t.n0 + (wave - 6) * 128, A->N - 1) / 128;
+      scales = (GU && wave == 7 ? A->sw1 : A->sw0) + (static_cast<int64_t>(t.e) * A->NB + nb) * KB;
       n_scales = KB;
     }
     rs = make_rsrc(scales, n_scales * 4);
@@ -258,7 +267,7 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
       const int c = (lane & 7) ^ ((r >> 1) & 7);
       const int j = (r >> 4) & 3, q = r & 15;
       const int n = t.n0 + (r >> 6) * (GU ? 32 : 64) + (GU ? 0 : (j >> 1) * 32) + 8 * (q >> 2) + 4 * (j & 1) + (q & 3);
-      boff[i] = n < P.N ? static_cast<uint32_t>(n) * K + c * 16 : kOutside;
+      boff[i] = n < A->N ? static_cast<uint32_t>(n) * K + c * 16 : kOutside;
     }
   };
   // Load instruction v of step s, of the first (weights W, rows, scales) or the
@@ -390,10 +399,10 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
         if constexpr (GU) {
           if (more) {
             nx = find(next);
-            per_row_load(P.row_token, nx.row0, nx.valid);
+            per_row_load(args()->row_token, nx.row0, nx.valid);
           }
-        } else if (P.row_weight != nullptr) {
-          per_row_load(P.row_weight, now.row0, now.valid);
+        } else if (const float* w = args()->row_weight; w != nullptr) {
+          per_row_load(w, now.row0, now.valid);
         }
       }
       if (last && more) {
@@ -412,12 +421,13 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
     for (int s = 2; s < padded; s += 2) pair(none{}, s);
     // ---- epilogue; stores of rows and columns outside go out of range, so
     // that their count is fixed: they run on under the next tile's first step.
+    const auto* A = args();
     const int lane = lane_id, g = lane >> 4, q = lane & 15;
     const int row0 = now.row0, valid = now.valid, n0 = now.n0;
     if constexpr (GU) {
-      const int NBo = (P.N + 127) / 128;
-      const rsrc_t rq = make_rsrc(P.aq + static_cast<int64_t>(row0) * P.N, static_cast<int64_t>(valid) * P.N);
-      const rsrc_t rm = make_rsrc(P.sout + static_cast<int64_t>(row0) * NBo, static_cast<int64_t>(valid) * NBo * 4);
+      const int NBo = (A->N + 127) / 128;
+      const rsrc_t rq = make_rsrc(A->aq + static_cast<int64_t>(row0) * A->N, static_cast<int64_t>(valid) * A->N);
+      const rsrc_t rm = make_rsrc(A->sout + static_cast<int64_t>(row0) * NBo, static_cast<int64_t>(valid) * NBo * 4);
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         float m = 0.0f;
@@ -453,17 +463,17 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
         const int n = n0 + wn * 32 + 8 * g;
         const bool row = i < NI && r < valid;
         __builtin_amdgcn_raw_buffer_store_b64(u32x2{codes.x, codes.y}, rq,
-                                              row && n < P.N ? static_cast<uint32_t>(r) * P.N + n : kOutside, 0, 0);
+                                              row && n < A->N ? static_cast<uint32_t>(r) * A->N + n : kOutside, 0, 0);
         __builtin_amdgcn_raw_buffer_store_b32(
             __float_as_uint(m / 448.0f), rm,
             row && wn == 0 && g == 0 ? (static_cast<uint32_t>(r) * NBo + n0 / 128) * 4 : kOutside, 0, 0);
       }
     } else {
-      const rsrc_t ro = make_rsrc(P.out + static_cast<int64_t>(row0) * P.N, static_cast<int64_t>(valid) * P.N * 2);
+      const rsrc_t ro = make_rsrc(A->out + static_cast<int64_t>(row0) * A->N, static_cast<int64_t>(valid) * A->N * 2);
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
         const int r = row_of(i, q);
-        const float x = P.row_weight != nullptr ? __int_as_float(per_row[r]) : 1.0f;
+        const float x = A->row_weight != nullptr ? __int_as_float(per_row[r]) : 1.0f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int n = n0 + wn * 64 + 32 * h + 8 * g;
@@ -476,13 +486,13 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
               m = __builtin_elementwise_maximum(m, fabsf(v[c]));  // NaN if one is
             }
             float f = 0.0f;
-            const uint32_t s = P.shared8 ? shared8_exponent(m, f) : 0;
+            const uint32_t s = A->shared8 ? shared8_exponent(m, f) : 0;
 #pragma unroll
             for (int c = 0; c < 4; ++c)
-              o[c] = P.shared8 ? shared8_word(v[2 * c], v[2 * c + 1], s, f, c) : pack_bf16x2(v[2 * c], v[2 * c + 1]);
+              o[c] = A->shared8 ? shared8_word(v[2 * c], v[2 * c + 1], s, f, c) : pack_bf16x2(v[2 * c], v[2 * c + 1]);
           }
           __builtin_amdgcn_raw_buffer_store_b128(
-              o, ro, i < NI && r < valid && n < P.N ? (static_cast<uint32_t>(r) * P.N + n) * 2 : kOutside, 0, 0);
+              o, ro, i < NI && r < valid && n < A->N ? (static_cast<uint32_t>(r) * A->N + n) * 2 : kOutside, 0, 0);
         }
       }
     }
