@@ -36,13 +36,14 @@ extern "C" {
  * infinite. */
 
 /* Rows [rows, K] of bf16 -> codes q [rows, K], scale [rows, ceil(K/128)].
- * rows >= 0 and K > 0, K % 8 == 0 (MOE_EINVAL otherwise). */
+ * rows >= 0 and K > 0, K % 8 == 0 (MOE_EINVAL otherwise); rows * ceil(K/128)
+ * below 2^28 (MOE_EUNSUPPORTED). */
 moe_status moe_quantize_fp8_block_rows(int32_t rows, int32_t K, const void* in, uint8_t* q, float* scale,
                                        hipStream_t stream);
 
 /* A stacked weight w [E, N, K] of bf16 -> codes q [E, N, K] and
  * scale [E, ceil(N/128), ceil(K/128)]. K % 8 == 0 (MOE_EINVAL otherwise);
- * E * ceil(N/128) and ceil(K/128) below 2^31 and 65536 (MOE_EUNSUPPORTED). */
+ * E * ceil(N/128) * ceil(K/128) below 2^24 (MOE_EUNSUPPORTED otherwise). */
 moe_status moe_quantize_fp8_block_weights(int32_t E, int32_t N, int32_t K, const void* w, uint8_t* q, float* scale,
                                           hipStream_t stream);
 
@@ -55,7 +56,7 @@ moe_status moe_quantize_fp8_block_weights(int32_t E, int32_t N, int32_t K, const
  * with 0 <= offsets[0] <= ... <= offsets[E] <= M (not checked on the device);
  * rows outside [offsets[0], offsets[E]) are not written. offsets may be NULL
  * when E == 1 (every row: the dense product). row_weight [M] f32 or NULL (1).
- * M >= 0; N % 8 == 0, K % 16 == 0, E <= 1024, N K, 256 K and 512 N below 2^31
+ * 0 <= M < 2^30; N % 8 == 0, K % 16 == 0, E <= 1024, N K, 256 K and 512 N below 2^31
  * (MOE_EUNSUPPORTED otherwise). */
 moe_status moe_gemm_fp8_block(int32_t M, int32_t E, int32_t N, int32_t K, const uint8_t* aq, const float* a_scale,
                               const int32_t* offsets, const uint8_t* wq, const float* w_scale, const float* row_weight,
@@ -107,7 +108,8 @@ moe_status moe_forward_fused_fp8_block(moe_shape s, const void* x, const void* w
  *   y[t] = bf16(sum over j of a[t,j] W_down[e]^T)     (fp32 accumulation).
  * It equals moe_forward_fused up to rounding (there the logits are an fp32
  * chain and the weight multiplies the down product). T <= 64, k <= 16,
- * shape.dtype MOE_BF16 (MOE_EUNSUPPORTED otherwise: moe_forward_fused).
+ * T k I below 2^30, shape.dtype MOE_BF16 (MOE_EUNSUPPORTED otherwise:
+ * moe_forward_fused).
  * logits [T,E] f32, topk_idx [T,k], topk_w [T,k] f32 and y [T,H] bf16 are
  * outputs. Workspace: ws of ws_bytes >= moe_few_workspace_bytes(s), its
  * contents arbitrary; calls that share one must not overlap in time (a

@@ -834,6 +834,15 @@ class ServingStage:
         self.w = (*weights.gate, *weights.up, *weights.down) if self.block else tuple(weights)
         self.E, self.I, self.H = self.w[0].shape
         E, I, H, T, M, dev = self.E, self.I, self.H, max_T, max_T * k, self.w[0].device
+        want = [(E, I, H), (E, I, H), (E, H, I)]
+        if self.block:
+            want = [d for E, N, K in want for d in ((E, N, K), (E, -(-N // 128), -(-K // 128)))]
+        if [tuple(w.shape) for w in self.w] != want or tuple(w_router.shape) != (E, H):
+            raise ValueError(f"weights have to be {want}, the router's {(E, H)}")
+        if not all(w.is_contiguous() for w in (*self.w, w_router)):
+            raise ValueError("weights have to be contiguous")
+        if logit_bias is not None and tuple(logit_bias.shape) != (E,):
+            raise ValueError(f"logit_bias has to be ({E},)")
         i32, u8, bf16 = torch.int32, torch.uint8, torch.bfloat16
         e = lambda *sz, dt=torch.float32: torch.empty(*sz, dtype=dt, device=dev)  # noqa: E731
         self.buf: Dict[str, torch.Tensor] = {"logits": e(T, E), "topk_idx": e(T, k, dt=i32), "topk_w": e(T, k),
@@ -857,6 +866,10 @@ class ServingStage:
 
     def forward(self, x, stream=None):
         T, b = x.shape[0], self.buf
+        if x.dim() != 2 or x.shape[1] != self.H or x.dtype != torch.bfloat16 or not x.is_contiguous():
+            raise ValueError(f"x has to be [T, {self.H}] in bf16, contiguous")
+        if x.device != b["y"].device:
+            raise ValueError(f"x is on {x.device}, the stage on {b['y'].device}")
         if T > self.max_T:
             raise ValueError(f"{T} tokens; the stage holds buffers for {self.max_T}")
         s = shape(T, self.H, self.E, self.k, self.I, torch.bfloat16)

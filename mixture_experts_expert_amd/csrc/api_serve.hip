@@ -19,6 +19,8 @@ bool misaligned(P... p) {
 }
 
 constexpr int64_t k2G = static_cast<int64_t>(1) << 31;
+constexpr int64_t kMaxThreads = static_cast<int64_t>(1) << 32;  // of one launch
+constexpr int64_t kMaxRows = static_cast<int64_t>(1) << 30;     // rows are counted in int32, rounded up to tiles
 
 // moe_workspace_bytes is 0 for the shapes that moe.h's calls reject; which of
 // the two codes those get is settled here, in the same order.
@@ -26,6 +28,7 @@ moe_status check_bf16_shape(const moe_shape& s) {
   if (s.T <= 0 || s.H <= 0 || s.E <= 0 || s.k <= 0 || s.I <= 0) return MOE_EINVAL;
   if (s.k > s.E || s.E > 1024 || static_cast<int64_t>(s.T) * s.k >= k2G) return MOE_EINVAL;
   if (s.dtype != MOE_BF16 || moe_workspace_bytes(s) == 0) return MOE_EUNSUPPORTED;
+  if (static_cast<int64_t>(s.T) * s.k >= kMaxRows) return MOE_EUNSUPPORTED;
   if (static_cast<int64_t>(s.T) * s.H >= k2G || 512 * static_cast<int64_t>(s.H) >= k2G ||
       512 * static_cast<int64_t>(s.I) >= k2G)
     return MOE_EUNSUPPORTED;
@@ -35,7 +38,8 @@ moe_status check_bf16_shape(const moe_shape& s) {
 moe_status check_few(const moe_shape& s) {
   const moe_status st = check_bf16_shape(s);
   if (st != MOE_OK) return st;
-  return s.T > moe::kFewMaxT || s.k > moe::kFewMaxK ? MOE_EUNSUPPORTED : MOE_OK;
+  if (s.T > moe::kFewMaxT || s.k > moe::kFewMaxK) return MOE_EUNSUPPORTED;
+  return static_cast<int64_t>(s.T) * s.k * s.I * 2 >= k2G ? MOE_EUNSUPPORTED : MOE_OK;  // 32-bit offsets into a
 }
 
 }  // namespace
@@ -46,7 +50,7 @@ moe_status moe_quantize_fp8_block_rows(int32_t rows, int32_t K, const void* in, 
                                        hipStream_t stream) {
   if (rows < 0 || K <= 0 || K % 8 != 0) return MOE_EINVAL;
   if (any_null(in, q, scale) || misaligned(in, q)) return MOE_EINVAL;
-  if (static_cast<int64_t>(rows) * moe::ceil_div(K, 128) >= k2G) return MOE_EUNSUPPORTED;
+  if (static_cast<int64_t>(rows) * moe::ceil_div(K, 128) * 16 >= kMaxThreads) return MOE_EUNSUPPORTED;
   return from_hip(moe::launch_quantize_fp8_block_rows(rows, K, in, q, scale, stream));
 }
 
@@ -54,7 +58,8 @@ moe_status moe_quantize_fp8_block_weights(int32_t E, int32_t N, int32_t K, const
                                           hipStream_t stream) {
   if (E <= 0 || N <= 0 || K <= 0 || K % 8 != 0) return MOE_EINVAL;
   if (any_null(w, q, scale) || misaligned(w, q)) return MOE_EINVAL;
-  if (E * moe::ceil_div64(N, 128) >= k2G || moe::ceil_div64(K, 128) >= 65536) return MOE_EUNSUPPORTED;
+  if (E * moe::ceil_div64(N, 128) >= kMaxThreads || E * moe::ceil_div64(N, 128) * moe::ceil_div64(K, 128) * 256 >= kMaxThreads)
+    return MOE_EUNSUPPORTED;
   return from_hip(moe::launch_quantize_fp8_block_weights(E, N, K, w, q, scale, stream));
 }
 
@@ -64,7 +69,7 @@ moe_status moe_gemm_fp8_block(int32_t M, int32_t E, int32_t N, int32_t K, const 
   if (M < 0 || E <= 0 || N <= 0 || K <= 0) return MOE_EINVAL;
   if (any_null(aq, a_scale, wq, w_scale, out) || (offsets == nullptr && E != 1)) return MOE_EINVAL;
   if (misaligned(aq, wq, out)) return MOE_EINVAL;
-  if (N % 8 != 0 || K % 16 != 0 || E > 1024) return MOE_EUNSUPPORTED;
+  if (N % 8 != 0 || K % 16 != 0 || E > 1024 || M >= kMaxRows) return MOE_EUNSUPPORTED;
   if (static_cast<int64_t>(N) * K >= k2G || 256 * static_cast<int64_t>(K) >= k2G || 512 * static_cast<int64_t>(N) >= k2G)
     return MOE_EUNSUPPORTED;
   moe::BlockGemmArgs g{};

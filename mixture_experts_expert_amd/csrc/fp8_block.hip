@@ -90,12 +90,15 @@ __global__ __launch_bounds__(kThreads) void quantize_block_rows_kernel(uint32_t 
 }
 
 // One 128 x 128 block per workgroup: 16 lanes along k, 16 rows at a time.
-__global__ __launch_bounds__(kThreads) void quantize_block_weights_kernel(int N, int K, int NB,
+// Neighbouring workgroups hold neighbouring blocks of the same rows, so that
+// together they walk whole rows: 128 x 768 x 2048 in 110 us (5.5 TB/s), 142 with
+// the blocks below one another side by side.
+__global__ __launch_bounds__(kThreads) void quantize_block_weights_kernel(int N, int K, int NB, int KB,
                                                                           const uint4* __restrict__ w,
                                                                           uint2* __restrict__ q,
                                                                           float* __restrict__ scale) {
   __shared__ float part[kThreads / kWave];
-  const int e = blockIdx.x / NB, nb = blockIdx.x % NB, b = blockIdx.y;
+  const int rows_of = blockIdx.x / KB, b = blockIdx.x - rows_of * KB, e = rows_of / NB, nb = rows_of - e * NB;
   const int chunks = K / 8, c = b * 16 + static_cast<int>(threadIdx.x) % 16;
   const int r0 = nb * 128 + static_cast<int>(threadIdx.x) / 16;
   const int64_t base = (static_cast<int64_t>(e) * N + r0) * chunks + c;
@@ -114,7 +117,7 @@ __global__ __launch_bounds__(kThreads) void quantize_block_weights_kernel(int N,
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (c < chunks && r0 + 16 * i < N) q[base + static_cast<int64_t>(16 * i) * chunks] = codes8(v[i], amax);
-  if (threadIdx.x == 0) scale[static_cast<int64_t>(blockIdx.x) * gridDim.y + b] = amax / 448.0f;
+  if (threadIdx.x == 0) scale[blockIdx.x] = amax / 448.0f;
 }
 
 }  // namespace
@@ -131,9 +134,9 @@ hipError_t launch_quantize_fp8_block_rows(int rows, int K, const void* in, uint8
 
 hipError_t launch_quantize_fp8_block_weights(int E, int N, int K, const void* w, uint8_t* q, float* scale,
                                              hipStream_t st) {
-  const int NB = ceil_div(N, 128);
-  const dim3 grid(static_cast<unsigned>(E) * static_cast<unsigned>(NB), static_cast<unsigned>(ceil_div(K, 128)));
-  quantize_block_weights_kernel<<<grid, kThreads, 0, st>>>(N, K, NB, static_cast<const uint4*>(w),
+  const int NB = ceil_div(N, 128), KB = ceil_div(K, 128);
+  const unsigned grid = static_cast<unsigned>(E) * static_cast<unsigned>(NB) * static_cast<unsigned>(KB);
+  quantize_block_weights_kernel<<<grid, kThreads, 0, st>>>(N, K, NB, KB, static_cast<const uint4*>(w),
                                                            reinterpret_cast<uint2*>(q), scale);
   return hipGetLastError();
 }

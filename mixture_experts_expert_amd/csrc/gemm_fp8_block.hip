@@ -750,7 +750,8 @@ hipError_t launch(const BlockGemmArgs& a, hipStream_t st) {
   //    against 297 / 308, at 512 493 / 487 against 521 / 524.
   const int64_t avg = (a.M + a.E - 1) / a.E;
   const bool one = a.E == 1 && a.M <= 192 && ceil_div(a.N, GU ? BN / 2 : BN) <= 32;
-  if (avg <= 4 || a.M <= 64 || one) {
+  const bool fits = static_cast<int64_t>(a.E) * ceil_div(a.N, 128) < 1 << 20;  // a launch has less than 2^32 threads
+  if ((avg <= 4 || a.M <= 64 || one) && fits) {
     // Enough workgroups to fill the device: split the reduction when there
     // are too few columns.
     int ks = 1;

@@ -37,13 +37,14 @@ def _with(args, at, value):
     return args
 
 
-@pytest.mark.parametrize("rows,K,code", [(-1, 64, EINVAL), (4, 0, EINVAL), (4, 12, EINVAL), (1 << 30, 1 << 10, EUNSUPPORTED)])
+@pytest.mark.parametrize("rows,K,code", [(-1, 64, EINVAL), (4, 0, EINVAL), (4, 12, EINVAL), (1 << 30, 1 << 10, EUNSUPPORTED),
+                                         (1 << 28, 128, EUNSUPPORTED)])
 def test_quantize_rows_refusals(B, rows, K, code):
     assert B.lib.moe_quantize_fp8_block_rows(rows, K, FAKE, FAKE, FAKE, None) == code
 
 
-@pytest.mark.parametrize("E,N,K,code", [(0, 8, 8, EINVAL), (1, 0, 8, EINVAL), (1, 8, 4, EINVAL), (1, 8, 1 << 23, EUNSUPPORTED),
-                                        (1 << 20, 1 << 20, 8, EUNSUPPORTED)])
+@pytest.mark.parametrize("E,N,K,code", [(0, 8, 8, EINVAL), (1, 0, 8, EINVAL), (1, 8, 4, EINVAL), (1 << 10, 8, 1 << 23, EUNSUPPORTED),
+                                        (1 << 20, 1 << 20, 8, EUNSUPPORTED), (1 << 30, 1 << 30, 1 << 30, EUNSUPPORTED)])
 def test_quantize_weights_refusals(B, E, N, K, code):
     assert B.lib.moe_quantize_fp8_block_weights(E, N, K, FAKE, FAKE, FAKE, None) == code
 
@@ -68,6 +69,7 @@ GEMM = [FAKE, FAKE, FAKE, FAKE, FAKE, None, FAKE]  # aq, a_scale, offsets, wq, w
     (8, 2, 1 << 16, 1 << 15, EUNSUPPORTED),  # N K
     (8, 2, 8, 1 << 23, EUNSUPPORTED),      # 256 K
     (8, 2, 1 << 22, 16, EUNSUPPORTED),     # 512 N
+    (1 << 30, 2, 64, 64, EUNSUPPORTED),
 ])
 def test_gemm_shapes(B, M, E, N, K, code):
     assert B.lib.moe_gemm_fp8_block(M, E, N, K, *GEMM, None) == code
@@ -112,11 +114,28 @@ def test_layer_refusals(B, name):
 
 def test_few_limits(B):
     assert B.moe_few_workspace_bytes(B.shape(64, 64, 32, 16, 64, "bf16")) > 0
-    for dims in ((65, 64, 32, 2, 64, "bf16"), (4, 64, 32, 17, 64, "bf16")):
+    for dims in ((65, 64, 32, 2, 64, "bf16"), (4, 64, 32, 17, 64, "bf16"), (64, 64, 32, 16, 1 << 20, "bf16")):
         assert B.moe_few_workspace_bytes(B.shape(*dims)) == 0
         assert B.lib.moe_forward_few(B.shape(*dims), *[FAKE] * 11, 1 << 40, None) == EUNSUPPORTED
     need = B.moe_few_workspace_bytes(B.shape(4, 64, 32, 2, 64, "bf16"))
     assert B.lib.moe_forward_few(B.shape(4, 64, 32, 2, 64, "bf16"), *[FAKE] * 11, need - 1, None) == EWORKSPACE
+
+
+def test_serving_stage_refusals(B):
+    bf = torch.bfloat16
+    z = lambda *d, dt=bf: torch.zeros(*d, dtype=dt)
+    w, wr = [z(4, 64, 128), z(4, 64, 128), z(4, 128, 64)], z(4, 128)
+    stage = B.ServingStage(8, 2, wr, w, None)  # buffers only
+    for x in (z(9, 128), z(4, 64), z(4, 128, dt=torch.float32), z(128), z(4, 256)[:, ::2], z(128, 4).T):
+        with pytest.raises(ValueError):
+            stage.forward(x)
+    for weights, router, bias in (([w[0], w[1], w[0]], wr, None), (w, z(3, 128), None), (w, wr, z(5)),
+                                  ([w[0], w[1], z(4, 64, 128).transpose(1, 2)], wr, None)):
+        with pytest.raises(ValueError):
+            B.ServingStage(8, 2, router, weights, bias)
+    codes = [z(*t.shape, dt=torch.uint8) for t in w]
+    with pytest.raises(ValueError):
+        B.ServingStage(8, 2, wr, B.FP8BlockWeights(stored=[(c, torch.zeros(4, 2, 2)) for c in codes]), None)
 
 
 def test_e4m3_definition():
