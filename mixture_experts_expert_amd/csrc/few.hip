@@ -4,7 +4,7 @@
 // is read once from memory and multiplied by the handful of rows that chose
 // it, so the kernel is bound by the weights' bytes and, for one token, by
 // latency (75 MB at the 30B shape in bf16: 36 us; 64 tokens reach nearly all of
-// the 1.2 GB: 264 us, 4.5 TB/s). Everything here serves that: the
+// the 1.2 GB: 259 us, 4.6 TB/s). Everything here serves that: the
 // weights go straight from memory into registers in 16-byte loads, several
 // steps ahead and on into the next unit; gate/up and down are one launch, so
 // that the down weights' first loads are in flight while the last gate/up
@@ -18,12 +18,13 @@
 //   few_kernel: one persistent workgroup of 8 wavefronts per CU. Each selects
 //     the experts of all tokens for itself (no third launch), then takes
 //     its share of the units:
-//     - gate/up unit: one expert, 8 columns (8 rows of W_gate and 8 of W_up).
-//       The reduction is split over the 8 wavefronts, so each token row's part
-//       is loaded by one of them (wavefronts that work side by side on one
-//       expert's columns wait for each other's pending lines in the vector
-//       cache: 300 instead of 165 us for 64 tokens' gate and up). The partial
-//       sums meet in LDS; a = bf16(w silu(g) u) goes to the workspace.
+//     - gate/up unit: one expert, 8 or 16 columns (8 rows of W_gate and 8 of
+//       W_up per wavefront). The reduction is split over the wavefronts, so
+//       each token row's part is loaded by one or two of them (eight that work
+//       side by side on one expert's columns wait for each other's pending
+//       lines in the vector cache: 300 instead of 165 us for 64 tokens' gate
+//       and up). The partial sums meet in LDS; a = bf16(w silu(g) u) goes to
+//       the workspace.
 //     - down unit: one group of experts, 16 columns of y. The (expert, k)
 //       steps are split over the wavefronts, each adding its experts' products
 //       into its own y tile in LDS; the eight tiles are then summed in order.
@@ -559,6 +560,12 @@ template <int FMT, int TILES, int XR, int NB, int NC>
 __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
   constexpr int ESZ = FMT == kBf16 ? 2 : 1;
   constexpr int RPI = kRPI<FMT>, XN = XR / RPI;
+  // A gate/up unit: GW times 8 columns, each 8 split along k over KW
+  // wavefronts. Two share a unit's end and its barrier, at twice the loads of
+  // token rows (us, one / two: 64 tokens in bf16 266 / 259, 33 in E4M3 184 / 174
+  // at 128 experts, k = 8); not for a few units (1 token, E4M3: 34 / 43), nor
+  // where the token rows are many (64 tokens, 8 experts, k = 2: 58 / 83).
+  constexpr int GW = TILES > 1 && XR == 8 ? 2 : 1, GC = kGC * GW, KW = kNW / GW;
   constexpr int kBatchLoads = NB * (2 + XN);
   __shared__ FewLists L;
   __shared__ __attribute__((aligned(16))) FewScratch<TILES> S;
@@ -574,7 +581,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
   if (wave == 0) claims.request(P);
   few_select<TILES, NC>(P, L, S);
   const int na = L.na, size = few_group(na), ngrp = (na + size - 1) / size;
-  const int gpe = I / kGC, dpg = H / kDC;  // gate/up units per expert, down units per group
+  const int part = wave / KW, kw = wave % KW;  // columns and reduction part of a gate/up unit
+  const int gpe = I / GC, dpg = H / kDC;  // gate/up units per expert, down units per group
   const int hsteps = (H + kStep<FMT> - 1) / kStep<FMT>, spe = (I + kStep<FMT> - 1) / kStep<FMT>;
   const bool hhalf = H % kStep<FMT> != 0, ihalf = I % kStep<FMT> != 0;
   const int down = ngrp * dpg;
@@ -614,14 +622,14 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
     else multiply<FMT>(acc[TILES > 1 ? 3 : 0], lds, f);
   };
   // ---- gate/up units: the steps [q0, q1) of each are this wavefront's
-  const int q0 = wave * hsteps / kNW, q1 = (wave + 1) * hsteps / kNW;
-  const int batches = ((hsteps + kNW - 1) / kNW + NB - 1) / NB;  // the same for all wavefronts
+  const int q0 = kw * hsteps / KW, q1 = (kw + 1) * hsteps / KW;
+  const int batches = ((hsteps + KW - 1) / KW + NB - 1) / NB;  // the same for all wavefronts
   // Batch j of unit u into set B (u < 0: reads nothing).
   auto fetch = [&](auto setc, int u, int j) __attribute__((always_inline)) {
     constexpr int B = decltype(setc)::value;
     const int v = max(u, 0), a = v / gpe, c = v - a * gpe, e = L.expert[a], first = L.start[a];
     const int rows = u < 0 ? 0 : L.start[a + 1] - first;
-    const int64_t at = (static_cast<int64_t>(e) * I + c * kGC) * H * ESZ;
+    const int64_t at = (static_cast<int64_t>(e) * I + c * GC + part * kGC) * H * ESZ;
     const rsrc_t r0 = make_rsrc(static_cast<const char*>(P.w0) + at, u < 0 ? 0 : kGC * H * ESZ);
     const rsrc_t r1 = make_rsrc(static_cast<const char*>(P.w1) + at, u < 0 ? 0 : kGC * H * ESZ);
     const uint32_t wo = static_cast<uint32_t>(wr) * H * ESZ + 16 * wc;
@@ -644,7 +652,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
       for (int i = 0; i < XN; ++i) st[B][d].x[i] = load_b128(Cached{}, xs, (xd & kNoRow) | (xo[i] + xd));
     }
     if constexpr (FMT == kFp8) {
-      const int64_t sc = (static_cast<int64_t>(e) * ((I + 127) / 128) + c * kGC / 128) * hsteps +
+      const int64_t sc = (static_cast<int64_t>(e) * ((I + 127) / 128) + c * GC / 128) * hsteps +
                          min(qb + lane % NB, hsteps - 1);
       sa[B] = P.s0[sc];
       sb[B] = P.s1[sc];
@@ -702,13 +710,13 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
     for (int t = 0; t < TILES; ++t)
       if (t < tiles) *reinterpret_cast<f32x4*>(&S.red[turn][t][wave][col][4 * g]) = acc[t];
     lds_barrier();
-    if (wave < tiles) {
-      const int t = wave < TILES ? wave : 0, row = lane / 4, c0 = 2 * (lane % 4);
+    if (kw < tiles) {
+      const int t = kw < TILES ? kw : 0, row = lane / 4, c0 = 2 * (lane % 4);
       float2 vg = make_float2(0.0f, 0.0f), vu = vg;
 #pragma unroll
-      for (int v = 0; v < kNW; ++v) {
-        const float2 x = *reinterpret_cast<const float2*>(&S.red[turn][t][v][row][c0]);
-        const float2 y = *reinterpret_cast<const float2*>(&S.red[turn][t][v][row][8 + c0]);
+      for (int v = 0; v < KW; ++v) {
+        const float2 x = *reinterpret_cast<const float2*>(&S.red[turn][t][part * KW + v][row][c0]);
+        const float2 y = *reinterpret_cast<const float2*>(&S.red[turn][t][part * KW + v][row][8 + c0]);
         vg.x += x.x;
         vg.y += x.y;
         vu.x += y.x;
@@ -717,7 +725,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
       if (16 * t + row < rows) {
         const int pair = L.list[first + 16 * t + row];
         const float pw = L.weight[pair];
-        __hip_atomic_store(reinterpret_cast<uint32_t*>(P.act + static_cast<int64_t>(pair) * I + c * kGC + c0),
+        __hip_atomic_store(reinterpret_cast<uint32_t*>(P.act + static_cast<int64_t>(pair) * I + c * GC + part * kGC + c0),
                            pack_bf16x2(pw * (vg.x * sigmoidf_dev(vg.x) * vu.x), pw * (vg.y * sigmoidf_dev(vg.y) * vu.y)),
                            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
@@ -890,7 +898,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
     for (int i = lane; i < T * kDC; i += kWave) tile[i / kDC * TS + i % kDC] = 0.0f;
     // The group's activations are there once all its tiles are counted.
     uint32_t want = 0;
-    for (int a = a0; a < a_end; ++a) want += (L.start[a + 1] - L.start[a] + 15) / 16 * gpe;
+    for (int a = a0; a < a_end; ++a) want += (L.start[a + 1] - L.start[a] + 15) / 16 * gpe * GW;
     wait_count(P.cnt + (kLists + grp) * kLine, want);
     if (cx.q < d1) {
       row_offsets(cx.a, 0, xo);
