@@ -806,6 +806,8 @@ class FP8BlockWeights:
 
     def __init__(self, w_gate=None, w_up=None, w_down=None, stream=None, stored=None):
         def quant(w):
+            if w.dtype != torch.bfloat16 or not w.is_contiguous():
+                raise ValueError("weights have to be bf16, contiguous")
             E, N, K = w.shape
             q = torch.empty(E, N, K, dtype=torch.uint8, device=w.device)
             scale = torch.empty(E, -(-N // 128), -(-K // 128), dtype=torch.float32, device=w.device)
@@ -841,6 +843,11 @@ class ServingStage:
             raise ValueError(f"weights have to be {want}, the router's {(E, H)}")
         if not all(w.is_contiguous() for w in (*self.w, w_router)):
             raise ValueError("weights have to be contiguous")
+        bf = (w_router,) if self.block else (*self.w, w_router)
+        f32 = (self.w[1::2] if self.block else ()) + (() if logit_bias is None else (logit_bias,))
+        if any(w.dtype != torch.bfloat16 for w in bf) or any(w.dtype != torch.float32 for w in f32) or (
+                self.block and any(w.element_size() != 1 for w in self.w[::2])):
+            raise ValueError("bf16 weights, or 8-bit codes with float32 scales; a bf16 router, a float32 bias")
         if logit_bias is not None and tuple(logit_bias.shape) != (E,):
             raise ValueError(f"logit_bias has to be ({E},)")
         i32, u8, bf16 = torch.int32, torch.uint8, torch.bfloat16

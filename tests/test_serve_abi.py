@@ -129,10 +129,12 @@ def test_serving_stage_refusals(B):
     for x in (z(9, 128), z(4, 64), z(4, 128, dt=torch.float32), z(128), z(4, 256)[:, ::2], z(128, 4).T):
         with pytest.raises(ValueError):
             stage.forward(x)
-    for weights, router, bias in (([w[0], w[1], w[0]], wr, None), (w, z(3, 128), None), (w, wr, z(5)),
+    for weights, router, bias in (([w[0], w[1], w[0]], wr, None), (w, z(3, 128), None), (w, wr, z(5)), (w, wr, z(4)), ([t.float() for t in w], wr, None),
                                   ([w[0], w[1], z(4, 64, 128).transpose(1, 2)], wr, None)):
         with pytest.raises(ValueError):
             B.ServingStage(8, 2, router, weights, bias)
+    with pytest.raises(ValueError):
+        B.FP8BlockWeights(*[t.float() for t in w])
     codes = [z(*t.shape, dt=torch.uint8) for t in w]
     with pytest.raises(ValueError):
         B.ServingStage(8, 2, wr, B.FP8BlockWeights(stored=[(c, torch.zeros(4, 2, 2)) for c in codes]), None)
