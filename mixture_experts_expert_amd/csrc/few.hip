@@ -11,10 +11,10 @@
 // units finish; no activation row but the selected experts' (T k I bf16) is
 // ever written.
 //
-//   few_router_kernel: logits, one workgroup per expert and 8 tokens. x and
-//     w_router products are exact in fp32 (bf16 factors) and summed in fp64,
-//     so the logit is the exact sum rounded once, whatever the split. It also
-//     clears the second kernel's counters.
+//   few_router_kernel: logits, one workgroup per expert and 8 tokens.
+//     Products and sums are taken in fp64, where a product of two bf16
+//     numbers is exact at both ends of the range (in fp32 it overflows or
+//     vanishes there). It also clears the second kernel's counters.
 //   few_kernel: one persistent workgroup of 8 wavefronts per CU. Each selects
 //     the experts of all tokens for itself (no third launch), then takes
 //     its share of the units:
@@ -145,13 +145,19 @@ __global__ __launch_bounds__(kRouterWaves* kWave) void few_router_kernel(int T, 
     u32x4 xv[kRouterTokens];
 #pragma unroll
     for (int i = 0; i < kRouterTokens; ++i) xv[i] = i < nt ? x4[static_cast<int64_t>(i) * chunks + c] : wv;
+    double lo[4], hi[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      lo[q] = static_cast<double>(__uint_as_float(wv[q] << 16));
+      hi[q] = static_cast<double>(__uint_as_float(wv[q] & 0xffff0000u));
+    }
 #pragma unroll
     for (int i = 0; i < kRouterTokens; ++i) {
       if (i >= nt) break;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        acc[i] += static_cast<double>(__uint_as_float(xv[i][q] << 16) * __uint_as_float(wv[q] << 16));
-        acc[i] += static_cast<double>(__uint_as_float(xv[i][q] & 0xffff0000u) * __uint_as_float(wv[q] & 0xffff0000u));
+        acc[i] = fma(static_cast<double>(__uint_as_float(xv[i][q] << 16)), lo[q], acc[i]);
+        acc[i] = fma(static_cast<double>(__uint_as_float(xv[i][q] & 0xffff0000u)), hi[q], acc[i]);
       }
     }
   }
