@@ -478,7 +478,7 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
         for (int h = 0; h < 2; ++h) {
           const int n = n0 + wn * 64 + 32 * h + 8 * g;
           u32x4 o{};
-          if (i < NI) {
+          if (i < NI && row_of(i, 0) < valid) {  // 16 rows past the end are not packed
             float v[8], m = 0.0f;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {

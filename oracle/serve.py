@@ -78,9 +78,12 @@ def shared8_values(raw):
     bit = h & 1
     i = torch.arange(4)
     s = ((bit[..., 0] << i) + (bit[..., 1] << (i + 4))).sum(2)[..., None, None]
-    fixed = (h >> 1).double() * torch.exp2(s.double() - 125) / 32767
+    u = h >> 1 & 0x3FFF
+    low = torch.where(u == 0, 0, u + 8833).to(torch.int16).view(torch.bfloat16).double()  # 128 is 8319 + 8833
+    scaled = torch.where(u > 8319, (u - 8191).double(), low)  # 8192: 2^(s-126)
+    held = torch.where(h < 0, -scaled, scaled) * torch.exp2(s.double() - 139)
     other = (h & ~1).to(torch.int16).view(torch.bfloat16).double()
-    return torch.where(s == 255, other, fixed).reshape(raw.shape[0], -1)
+    return torch.where(s == 255, other, held).reshape(raw.shape[0], -1)
 
 
 def silu_mul(g, u):

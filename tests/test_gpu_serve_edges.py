@@ -1,13 +1,15 @@
 """GPU tests of the serving operators (include/moe_serve.h) at the ends of the
-number range."""
+number range and with outlying values."""
 import pytest
 import torch
 
 from mixture_experts_expert_amd import binding as B
+from oracle import serve as S
 
 pytestmark = pytest.mark.gpu
 
-BF = torch.bfloat16
+BF, F8 = torch.bfloat16, torch.float8_e4m3fn
+U = 2.0**-8  # one rounding to bf16
 
 
 def _few_logits(x, wr, bias=None):
@@ -45,3 +47,41 @@ def test_few_logits_of_products_below_fp32(T):
     x = torch.full((T, 64), 2.0**-75).to(BF)
     w = torch.full((3, 64), 2.0**-75).to(BF)
     assert torch.equal(_few_logits(x, w), torch.full((T, 3), 2.0**-144))
+
+
+@pytest.mark.parametrize("ratio", [64, 4096])
+@pytest.mark.parametrize("T", [5, 150, 500])  # each of the product's kernels
+def test_experts_beside_outlying_columns(T, ratio):
+    """One column in eight is `ratio` times the others, as some channels of a residual
+    stream are: the others come out as exactly as from bf16 rows. Bounds: 2^-8 of
+    each expert's result for its row, 2^-8 of y, and the product's own (oracle/serve.py)."""
+    H, E, k, I = 192, 4, 2, 128
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(T, H, generator=g).to(BF)
+    gate, up = ((torch.randn(E, I, H, generator=g) / H**0.5).to(BF) for _ in range(2))
+    down = torch.randint(-7, 8, (E, H, I), generator=g) * 2.0**-6
+    down[:, 3::8] *= ratio
+    codes = [S.quantize_weights(gate), S.quantize_weights(up), (down.to(F8).view(torch.uint8), torch.ones(E, 2, 1).double())]
+    w8 = B.FP8BlockWeights(stored=[(q.cuda(), s.float().cuda()) for q, s in codes])
+    idx, w = S.route(torch.randn(T, E, generator=g), k)
+    M, e = T * k, lambda *n, dt=torch.float32: torch.empty(*n, dtype=dt, device="cuda")
+    i32, u8 = torch.int32, torch.uint8
+    off, f2s, rw, aq, sa, op, y = e(E + 1, dt=i32), e(M, dt=i32), e(M), e(M, I, dt=u8), e(M, 1), e(M, H, dt=BF), e(T, H, dt=BF)
+    s = B.shape(T, H, E, k, I, BF)
+    B.moe_experts_fp8_block(s, x.cuda(), idx.to(i32).cuda(), w.float().cuda(), *w8.gate, *w8.up, *w8.down, e(E, dt=i32), off,
+                            e(M, dt=i32), f2s, e(M, dt=i32), rw, e(T, H, dt=u8), e(T, 2), aq, sa, op, y,
+                            e(B.moe_workspace_bytes(s), dt=u8))
+    off, f2s, rw, y = off.cpu(), f2s.cpu().long(), rw.cpu().double(), y.cpu().double()
+    a = S.dequantize_rows(aq.cpu(), sa.cpu())
+    want, tol = torch.zeros(M, H).double(), torch.zeros(M, H).double()
+    for n in range(E):
+        lo, hi = off[n], off[n + 1]
+        v, lost = S.product(a[lo:hi], down[n].double())
+        f = rw[lo:hi, None]
+        want[lo:hi] = v * f
+        tol[lo:hi] = (lost + a[lo:hi].abs() @ down[n].double().abs().T * 2.0**-20) * f
+    parts, slack = want[f2s].view(T, k, H), tol[f2s].view(T, k, H).sum(1)
+    sums, mag = parts.sum(1), parts.abs().sum(1)
+    assert ((y - sums).abs() <= sums.abs() * U + (mag * (U + 2.0**-20) + slack) * (1 + 2 * U)).all()
+    held = S.shared8_values(op.cpu())
+    assert ((held - want).abs() <= want.abs() * U + tol * (1 + U)).all()
