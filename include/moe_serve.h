@@ -76,9 +76,11 @@ moe_status moe_gemm_gate_up_fp8_block(moe_shape s, const uint8_t* xq, const floa
  * computed (topk_idx [T,k] in [0,E), topk_w [T,k] f32): moe_permute_fused,
  * the quantisation of x, the two GEMMs and the per-token sum (y [T,H] bf16).
  * o_perm [T*k,H], 2 bytes per element, is scratch: the rows of the down
- * product times row_weight, eight columns to 16 bytes with a common exponent
- * and 15 bits each, so that only y is rounded to bf16 (before, at most
- * 2^-14 of the largest of the eight). Every buffer is caller-owned and overwritten; wq_down [E,H,I] with scales
+ * product times row_weight, eight columns to 16 bytes with a common exponent,
+ * so that only y is rounded to bf16. A number in it is off by at most 2^-8 of
+ * itself, as in bf16 (from 2^-62 of the largest of the eight down it fades to
+ * zero), and by at most 2^-13 of the largest where that is 2^-114 or more.
+ * Every buffer is caller-owned and overwritten; wq_down [E,H,I] with scales
  * [E,ceil(H/128),ceil(I/128)]; H and I below 2^22; ws of ws_bytes >= moe_workspace_bytes(s). */
 moe_status moe_experts_fp8_block(moe_shape s, const void* x, const int32_t* topk_idx, const float* topk_w,
                                  const uint8_t* wq_gate, const float* w_gate_scale, const uint8_t* wq_up,
