@@ -114,9 +114,9 @@ moe_status moe_forward_fused_fp8_block(moe_shape s, const void* x, const void* w
  * moe_forward_fused).
  * logits [T,E] f32, topk_idx [T,k], topk_w [T,k] f32 and y [T,H] bf16 are
  * outputs. Workspace: ws of ws_bytes >= moe_few_workspace_bytes(s), its
- * contents arbitrary; calls that share one must not overlap in time (a
- * kernel whose workspace another call overwrites ends with wrong results
- * after at most a few seconds, it does not hang). */
+ * contents arbitrary; calls that share one must not overlap in time (their
+ * results are then undefined; a wait inside the kernel that is never answered
+ * ends after some seconds of running, and y is NaN there). */
 size_t moe_few_workspace_bytes(moe_shape s);
 moe_status moe_forward_few(moe_shape s, const void* x, const void* w_router, const float* logit_bias,
                            const void* w_gate, const void* w_up, const void* w_down, float* logits, int32_t* topk_idx,

@@ -43,8 +43,9 @@
 // are claimed. A down unit waits for its group's gate/up units; by then
 // running workgroups hold all of those, and gate/up units wait for nothing:
 // the wait ends whatever else occupies the device. (If another call
-// overwrites the workspace, against the interface, the wait gives up after
-// two seconds.) Claiming unit by unit instead stalls the loads: an atomic's
+// overwrites the workspace, against the interface, the count may never be
+// reached: the wait gives up after kFewPolls looks, seconds of running, and y
+// becomes NaN there.) Claiming unit by unit instead stalls the loads: an atomic's
 // answer comes back behind all loads issued before it.
 //
 // Tile: v_mfma_f32_16x16x32_bf16 with the weights as A (16 rows) and up to 16
@@ -78,7 +79,6 @@ constexpr int kLists = 8;           // counters of claimed shares, one per XCD
 constexpr int kLine = 32;           // counters that workgroups add to lie 128 bytes apart
 constexpr int kMaxPairs = kFewMaxT * kFewMaxK;
 constexpr uint32_t kNoRow = 0x80000000u;  // an offset past every row, whatever is added to it
-constexpr uint64_t kSpinTicks = 200000000;  // two seconds of the 100 MHz clock
 
 // The workspace's counters (uint32, in lines): [0, 8) gate/up shares claimed,
 // then gate/up tiles done per group; after the lines, down units done per
@@ -94,6 +94,7 @@ struct FewParams {
   bf16_t* y;
   uint32_t* cnt;
   uint32_t* cnt_down;
+  uint32_t polls;               // looks at a count before a wait gives up
   bf16_t* act;                  // [T*k][I], weighted
   float* part;                  // [groups][T][H]
 };
@@ -547,14 +548,16 @@ struct Claims {
   }
 };
 
-// Waits until *p reaches `want`.
-__device__ __forceinline__ void wait_count(const uint32_t* p, uint32_t want) {
-  const uint64_t t0 = __builtin_amdgcn_s_memrealtime();
-  while (__hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < want) {
-    if (__builtin_amdgcn_s_memrealtime() - t0 > kSpinTicks) break;
-    __builtin_amdgcn_s_sleep(1);
+// Waits until *p reaches `want`; false after `polls` looks at it (a count of
+// the wavefront's own, so that time in which it is suspended does not pass).
+__device__ __forceinline__ bool wait_count(const uint32_t* p, uint32_t want, uint32_t polls) {
+  bool there = false;
+  for (uint32_t n = 0; n < polls && !there; ++n) {
+    there = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) >= want;
+    if (!there) __builtin_amdgcn_s_sleep(1);
   }
   asm volatile("" ::: "memory");  // what follows is read after it
+  return there;
 }
 
 // TILES: 16-row tiles of one expert's tokens (one for T <= 16, else four); XR:
@@ -901,11 +904,14 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
     typedef std::integral_constant<int, 1> Set1;
     fetch_w(Set0{});
     fetch_w(Set1{});
-    for (int i = lane; i < T * kDC; i += kWave) tile[i / kDC * TS + i % kDC] = 0.0f;
+    auto fill = [&](float v) __attribute__((always_inline)) {
+      for (int i = lane; i < T * kDC; i += kWave) tile[i / kDC * TS + i % kDC] = v;
+    };
+    fill(0.0f);
     // The group's activations are there once all its tiles are counted.
     uint32_t want = 0;
     for (int a = a0; a < a_end; ++a) want += (L.start[a + 1] - L.start[a] + 15) / 16 * gpe * GW;
-    wait_count(P.cnt + (kLists + grp) * kLine, want);
+    if (!wait_count(P.cnt + (kLists + grp) * kLine, want, P.polls)) fill(__builtin_nanf(""));
     if (cx.q < d1) {
       row_offsets(cx.a, 0, xo);
       open(cu.a);
@@ -1025,6 +1031,7 @@ hipError_t launch_few(const moe_shape& s, const FewArgs& a, void* ws, hipStream_
   P.topk_idx = a.topk_idx;
   P.topk_w = a.topk_w;
   P.y = static_cast<bf16_t*>(a.y);
+  P.polls = a.polls;
   P.cnt = reinterpret_cast<uint32_t*>(base);
   P.act = reinterpret_cast<bf16_t*>(base + l.act);
   P.part = reinterpret_cast<float*>(base + l.part);

@@ -285,6 +285,7 @@ hipError_t launch_gemm_fp8_block(const BlockGemmArgs& a, hipStream_t st);
 
 // The whole layer for a few tokens (few.hip).
 constexpr int kFewMaxT = 64, kFewMaxK = 16;
+constexpr uint32_t kFewPolls = 1u << 23;  // at about a microsecond each
 struct FewLayout {  // byte offsets in the workspace; the counters come first
   int counters, groups;
   size_t act, part, total;
@@ -299,6 +300,7 @@ struct FewArgs {
   int32_t* topk_idx;
   float* topk_w;
   void* y;
+  uint32_t polls = kFewPolls;  // before a wait inside the kernel gives up
 };
 hipError_t launch_few(const moe_shape& s, const FewArgs& a, void* ws, hipStream_t st);
 

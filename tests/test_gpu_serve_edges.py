@@ -1,5 +1,7 @@
 """GPU tests of the serving operators (include/moe_serve.h) at the ends of the
-number range and with outlying values."""
+number range, with outlying values and with a wait that gives up."""
+import ctypes
+
 import pytest
 import torch
 
@@ -85,3 +87,37 @@ def test_experts_beside_outlying_columns(T, ratio):
     assert ((y - sums).abs() <= sums.abs() * U + (mag * (U + 2.0**-20) + slack) * (1 + 2 * U)).all()
     held = S.shared8_values(op.cpu())
     assert ((held - want).abs() <= want.abs() * U + tol * (1 + U)).all()
+
+
+class _FewArgs(ctypes.Structure):  # moe::FewArgs (csrc/moe_internal.h)
+    _fields_ = [(n, ctypes.c_void_p) for n in ("x", "w_router", "bias", "w_gate", "w_up", "w_down", "gate_scale", "up_scale",
+                                               "down_scale", "logits", "topk_idx", "topk_w", "y")] + [("polls", ctypes.c_uint32)]
+
+
+@pytest.mark.parametrize("dims", [(1, 64, 4, 2, 64), (40, 320, 60, 6, 192)], ids=str)  # one group of experts, and several
+def test_few_wait_that_gives_up_shows(dims):
+    """A wait for the activations that ends early leaves NaN, never numbers made without them."""
+    T, H, E, k, I = dims
+    launch = B.lib["_ZN3moe10launch_fewERK9moe_shapeRKNS_7FewArgsEPvP12ihipStream_t"]
+    launch.argtypes = [ctypes.c_void_p] * 4
+    g = torch.Generator().manual_seed(3)
+    ins = [torch.randn(T, H, generator=g), torch.randn(E, H, generator=g) / 8, torch.randn(E, I, H, generator=g) / 8,
+           torch.randn(E, I, H, generator=g) / 8, torch.randn(E, H, I, generator=g) / 8]
+    x, wr, gate, up, down = (t.to(BF).cuda() for t in ins)
+    s = B.shape(*dims, BF)
+    ws = torch.zeros(B.moe_few_workspace_bytes(s), dtype=torch.uint8, device="cuda")
+    new = lambda: (torch.empty(T, E, device="cuda"), torch.empty(T, k, dtype=torch.int32, device="cuda"),
+                   torch.empty(T, k, device="cuda"), torch.empty(T, H, dtype=BF, device="cuda"))
+    right = new()
+    B.moe_forward_few(s, x, wr, None, gate, up, down, *right, ws)
+    for polls in (0, 1, 1 << 23):
+        out = new()
+        ws.zero_()  # activations of zeros, were they read too early
+        a = _FewArgs(x.data_ptr(), wr.data_ptr(), None, gate.data_ptr(), up.data_ptr(), down.data_ptr(), None, None, None,
+                     *(t.data_ptr() for t in out), polls)
+        assert launch(ctypes.addressof(s), ctypes.addressof(a), ws.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(out[:3], right[:3]))
+        lost = out[3].isnan()
+        assert torch.equal(out[3][~lost], right[3][~lost])
+        assert {0: lost.all(), 1: True}.get(polls, not lost.any())
