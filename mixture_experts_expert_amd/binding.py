@@ -848,8 +848,8 @@ class ServingStage:
         if any(w.dtype != torch.bfloat16 for w in bf) or any(w.dtype != torch.float32 for w in f32) or (
                 self.block and any(w.element_size() != 1 for w in self.w[::2])):
             raise ValueError("bf16 weights, or 8-bit codes with float32 scales; a bf16 router, a float32 bias")
-        if logit_bias is not None and tuple(logit_bias.shape) != (E,):
-            raise ValueError(f"logit_bias has to be ({E},)")
+        if logit_bias is not None and (tuple(logit_bias.shape) != (E,) or not logit_bias.is_contiguous()):
+            raise ValueError(f"logit_bias has to be ({E},), contiguous")
         i32, u8, bf16 = torch.int32, torch.uint8, torch.bfloat16
         e = lambda *sz, dt=torch.float32: torch.empty(*sz, dtype=dt, device=dev)  # noqa: E731
         self.buf: Dict[str, torch.Tensor] = {"logits": e(T, E), "topk_idx": e(T, k, dt=i32), "topk_w": e(T, k),

@@ -1,0 +1,35 @@
+"""ServingStage and FP8BlockWeights refuse tensors that the kernels would read
+wrongly, before any call of the library (no GPU needed)."""
+import pytest
+import torch
+
+BF = torch.bfloat16
+E, I, H, K = 4, 64, 128, 2
+
+
+@pytest.fixture(scope="module")
+def B():
+    from mixture_experts_expert_amd import binding
+    return binding
+
+
+def _z(*d, dt=BF, dev="cpu"):
+    return torch.zeros(*d, dtype=dt, device=dev)
+
+
+def _bf16(dev="cpu"):
+    return [_z(E, I, H, dev=dev), _z(E, I, H, dev=dev), _z(E, H, I, dev=dev)]
+
+
+def _stored(dt=torch.uint8, dev="cpu", scale_dev=None):
+    f = lambda *d: _z(*d, dt=torch.float32, dev=scale_dev or dev)
+    return [(_z(E, I, H, dt=dt, dev=dev), f(E, 1, 1)), (_z(E, I, H, dt=dt, dev=dev), f(E, 1, 1)),
+            (_z(E, H, I, dt=dt, dev=dev), f(E, 1, 1))]
+
+
+def test_bias_has_to_be_contiguous(B):
+    wide = _z(E, 2, dt=torch.float32)
+    B.ServingStage(8, K, _z(E, H), _bf16(), wide[:, 0].contiguous())
+    for bias in (wide[:, 0], _z(1, dt=torch.float32).expand(E)):
+        with pytest.raises(ValueError):
+            B.ServingStage(8, K, _z(E, H), _bf16(), bias)
