@@ -841,6 +841,8 @@ class ServingStage:
             want = [d for E, N, K in want for d in ((E, N, K), (E, -(-N // 128), -(-K // 128)))]
         if [tuple(w.shape) for w in self.w] != want or tuple(w_router.shape) != (E, H):
             raise ValueError(f"weights have to be {want}, the router's {(E, H)}")
+        if any(w.device != dev for w in (*self.w, w_router) + (() if logit_bias is None else (logit_bias,))):
+            raise ValueError(f"weights, scales, router and bias have to be on one device, {dev}")
         if not all(w.is_contiguous() for w in (*self.w, w_router)):
             raise ValueError("weights have to be contiguous")
         bf = (w_router,) if self.block else (*self.w, w_router)

@@ -33,3 +33,14 @@ def test_bias_has_to_be_contiguous(B):
     for bias in (wide[:, 0], _z(1, dt=torch.float32).expand(E)):
         with pytest.raises(ValueError):
             B.ServingStage(8, K, _z(E, H), _bf16(), bias)
+
+
+def test_one_device(B):
+    """`meta` stands for any device but the weights' own."""
+    bias = _z(E, dt=torch.float32)
+    for weights, router, b in ((_bf16(), _z(E, H, dev="meta"), bias), (_bf16(), _z(E, H), bias.to("meta")),
+                               (_bf16()[:2] + _bf16("meta")[2:], _z(E, H), bias), (_bf16("meta"), _z(E, H), bias),
+                               (B.FP8BlockWeights(stored=_stored(scale_dev="meta")), _z(E, H), bias),
+                               (B.FP8BlockWeights(stored=_stored()[:2] + _stored(dev="meta")[2:]), _z(E, H), bias)):
+        with pytest.raises(ValueError):
+            B.ServingStage(8, K, router, weights, b)
