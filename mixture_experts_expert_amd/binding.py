@@ -800,7 +800,7 @@ def moe_forward_few_fp8_block(s, x, w_router, logit_bias, wq_gate, w_gate_scale,
 
 class FP8BlockWeights:
     """Expert weights in E4M3 with a float32 scale per 128 x 128 block: codes
-    gate/up [E,I,H], down [E,H,I] (uint8) and their scales. From bf16 weights
+    gate/up [E,I,H], down [E,H,I] (uint8 or float8_e4m3fn) and their scales. From bf16 weights
     (moe_quantize_fp8_block_weights), or, with ``stored``, a checkpoint's own
     (codes, scales) pairs as they are."""
 
@@ -848,8 +848,9 @@ class ServingStage:
         bf = (w_router,) if self.block else (*self.w, w_router)
         f32 = (self.w[1::2] if self.block else ()) + (() if logit_bias is None else (logit_bias,))
         if any(w.dtype != torch.bfloat16 for w in bf) or any(w.dtype != torch.float32 for w in f32) or (
-                self.block and any(w.element_size() != 1 for w in self.w[::2])):
-            raise ValueError("bf16 weights, or 8-bit codes with float32 scales; a bf16 router, a float32 bias")
+                self.block and any(w.dtype not in (torch.uint8, torch.float8_e4m3fn) for w in self.w[::2])):
+            raise ValueError("bf16 weights, or E4M3 codes (uint8, float8_e4m3fn) with float32 scales; a bf16 router, "
+                             "a float32 bias")
         if logit_bias is not None and (tuple(logit_bias.shape) != (E,) or not logit_bias.is_contiguous()):
             raise ValueError(f"logit_bias has to be ({E},), contiguous")
         i32, u8, bf16 = torch.int32, torch.uint8, torch.bfloat16

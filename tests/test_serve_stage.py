@@ -44,3 +44,13 @@ def test_one_device(B):
                                (B.FP8BlockWeights(stored=_stored()[:2] + _stored(dev="meta")[2:]), _z(E, H), bias)):
         with pytest.raises(ValueError):
             B.ServingStage(8, K, router, weights, b)
+
+
+@pytest.mark.parametrize("dt", [torch.int8, torch.bool, torch.float8_e5m2, torch.float8_e4m3fnuz, torch.float8_e5m2fnuz])
+def test_codes_of_another_format(B, dt):
+    for good in (torch.uint8, torch.float8_e4m3fn):
+        B.ServingStage(8, K, _z(E, H), B.FP8BlockWeights(stored=_stored(good)))
+    with pytest.raises(ValueError):
+        B.ServingStage(8, K, _z(E, H), B.FP8BlockWeights(stored=_stored(dt)))
+    with pytest.raises(ValueError):
+        B.ServingStage(8, K, _z(E, H), B.FP8BlockWeights(stored=_stored()[:2] + _stored(dt)[2:]))
