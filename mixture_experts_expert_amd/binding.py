@@ -806,8 +806,8 @@ class FP8BlockWeights:
 
     def __init__(self, w_gate=None, w_up=None, w_down=None, stream=None, stored=None):
         def quant(w):
-            if w.dtype != torch.bfloat16 or not w.is_contiguous():
-                raise ValueError("weights have to be bf16, contiguous")
+            if w.dtype != torch.bfloat16 or w.device.type != "cuda" or not w.is_contiguous():
+                raise ValueError("weights have to be bf16, contiguous, on the GPU")
             E, N, K = w.shape
             q = torch.empty(E, N, K, dtype=torch.uint8, device=w.device)
             scale = torch.empty(E, -(-N // 128), -(-K // 128), dtype=torch.float32, device=w.device)
@@ -875,11 +875,12 @@ class ServingStage:
             self.buf["o_perm"] = e(M, H, dt=bf16)
 
     def forward(self, x, stream=None):
-        T, b = x.shape[0], self.buf
+        b = self.buf
         if x.dim() != 2 or x.shape[1] != self.H or x.dtype != torch.bfloat16 or not x.is_contiguous():
             raise ValueError(f"x has to be [T, {self.H}] in bf16, contiguous")
-        if x.device != b["y"].device:
-            raise ValueError(f"x is on {x.device}, the stage on {b['y'].device}")
+        if x.device != b["y"].device or x.device.type != "cuda":
+            raise ValueError(f"x is on {x.device}, the stage on {b['y'].device}; both have to be on one GPU")
+        T = x.shape[0]
         if T > self.max_T:
             raise ValueError(f"{T} tokens; the stage holds buffers for {self.max_T}")
         s = shape(T, self.H, self.E, self.k, self.I, torch.bfloat16)

@@ -54,3 +54,19 @@ def test_codes_of_another_format(B, dt):
         B.ServingStage(8, K, _z(E, H), B.FP8BlockWeights(stored=_stored(dt)))
     with pytest.raises(ValueError):
         B.ServingStage(8, K, _z(E, H), B.FP8BlockWeights(stored=_stored()[:2] + _stored(dt)[2:]))
+
+
+def test_nothing_runs_on_host_tensors(B):
+    for weights in (_bf16(), B.FP8BlockWeights(stored=_stored())):
+        stage = B.ServingStage(8, K, _z(E, H), weights)
+        with pytest.raises(ValueError):
+            stage.forward(_z(3, H))
+    with pytest.raises(ValueError):
+        B.FP8BlockWeights(*_bf16())
+
+
+def test_shape_of_x(B):
+    stage = B.ServingStage(8, K, _z(E, H), _bf16())
+    for x in (torch.tensor(1.0, dtype=BF), _z(H), _z(1, 2, H)):
+        with pytest.raises(ValueError):
+            stage.forward(x)
