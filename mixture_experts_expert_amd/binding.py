@@ -811,7 +811,8 @@ class FP8BlockWeights:
             E, N, K = w.shape
             q = torch.empty(E, N, K, dtype=torch.uint8, device=w.device)
             scale = torch.empty(E, -(-N // 128), -(-K // 128), dtype=torch.float32, device=w.device)
-            moe_quantize_fp8_block_weights(E, N, K, w, q, scale, stream=stream)
+            with torch.cuda.device(w.device):
+                moe_quantize_fp8_block_weights(E, N, K, w, q, scale, stream=stream)
             return q, scale
 
         self.gate, self.up, self.down = stored if stored is not None else (quant(w_gate), quant(w_up), quant(w_down))
@@ -827,7 +828,8 @@ class ServingStage:
     moe_forward_fused_fp8_block for the others; it returns y [T,H], a view of
     a held buffer (overwritten by the next call), and leaves topk_idx and
     topk_w in ``buf``. Calls of one stage share its workspaces: enqueue them
-    on one stream, or order the streams.
+    on one stream, or order the streams. They run on the weights' device,
+    whichever is current; ``stream`` (its current one by default) belongs to it.
     """
 
     def __init__(self, max_T: int, k: int, w_router, weights, logit_bias=None):
@@ -885,14 +887,15 @@ class ServingStage:
             raise ValueError(f"{T} tokens; the stage holds buffers for {self.max_T}")
         s = shape(T, self.H, self.E, self.k, self.I, torch.bfloat16)
         y = b["y"][:T]
-        if T <= self.few_T:
-            fn = moe_forward_few_fp8_block if self.block else moe_forward_few
-            fn(s, x, self.w_router, self.logit_bias, *self.w, b["logits"], b["topk_idx"], b["topk_w"], y, self.few_ws,
-               stream=stream)
-        else:
-            fn = moe_forward_fused_fp8_block if self.block else moe_forward_fused
-            fn(s, x, self.w_router, self.logit_bias, *self.w, *[t for n, t in b.items() if n != "y"], y, self.ws,
-               stream=stream)
+        with torch.cuda.device(x.device):
+            if T <= self.few_T:
+                fn = moe_forward_few_fp8_block if self.block else moe_forward_few
+                fn(s, x, self.w_router, self.logit_bias, *self.w, b["logits"], b["topk_idx"], b["topk_w"], y, self.few_ws,
+                   stream=stream)
+            else:
+                fn = moe_forward_fused_fp8_block if self.block else moe_forward_fused
+                fn(s, x, self.w_router, self.logit_bias, *self.w, *[t for n, t in b.items() if n != "y"], y, self.ws,
+                   stream=stream)
         return y
 
 

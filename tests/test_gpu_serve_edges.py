@@ -121,3 +121,24 @@ def test_few_wait_that_gives_up_shows(dims):
         lost = out[3].isnan()
         assert torch.equal(out[3][~lost], right[3][~lost])
         assert {0: lost.all(), 1: True}.get(polls, not lost.any())
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8"])
+def test_stage_enqueues_on_its_own_device(fmt, monkeypatch):
+    """Whatever the current device is: the calls run with the tensors' device made current."""
+    made_current, real = [], torch.cuda.device
+    def device(d):
+        made_current.append(torch.device(d))
+        return real(d)
+    E, I, H, k = 4, 64, 128, 2
+    g = torch.Generator().manual_seed(4)
+    w = [(torch.randn(E, *d, generator=g) / 8).to(BF).cuda() for d in ((I, H), (I, H), (H, I))]
+    wr, x = torch.randn(E, H, generator=g).to(BF).cuda(), torch.randn(70, H, generator=g).to(BF).cuda()
+    monkeypatch.setattr(torch.cuda, "device", device)
+    weights = B.FP8BlockWeights(*w) if fmt == "fp8" else w
+    assert made_current == [x.device] * (3 if fmt == "fp8" else 0)
+    stage = B.ServingStage(70, k, wr, weights)
+    made_current.clear()
+    for T in (3, 70):
+        assert stage.forward(x[:T]).isfinite().all()
+    assert made_current == [x.device] * 2
