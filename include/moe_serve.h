@@ -5,7 +5,8 @@
  * The conventions of moe.h hold here too: device pointers to dense row-major
  * arrays, int32 indices, caller-owned buffers, nothing allocated, nothing
  * synchronised, every argument checked on the host before any HIP call,
- * results deterministic. Every array starts at a multiple of 16 bytes (as
+ * results deterministic. Arrays of no rows (rows or M of 0) may be NULL; nothing
+ * is done then. Every other array starts at a multiple of 16 bytes (as
  * allocations do; MOE_EINVAL otherwise where the kernels depend on it).
  *
  *   prefill: moe_forward_fused_fp8_block = moe_route -> moe_experts_fp8_block

@@ -885,8 +885,10 @@ class ServingStage:
         T = x.shape[0]
         if T > self.max_T:
             raise ValueError(f"{T} tokens; the stage holds buffers for {self.max_T}")
-        s = shape(T, self.H, self.E, self.k, self.I, torch.bfloat16)
         y = b["y"][:T]
+        if T == 0:
+            return y
+        s = shape(T, self.H, self.E, self.k, self.I, torch.bfloat16)
         with torch.cuda.device(x.device):
             if T <= self.few_T:
                 fn = moe_forward_few_fp8_block if self.block else moe_forward_few

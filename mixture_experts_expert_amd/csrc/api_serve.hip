@@ -49,6 +49,7 @@ extern "C" {
 moe_status moe_quantize_fp8_block_rows(int32_t rows, int32_t K, const void* in, uint8_t* q, float* scale,
                                        hipStream_t stream) {
   if (rows < 0 || K <= 0 || K % 8 != 0) return MOE_EINVAL;
+  if (rows == 0) return MOE_OK;
   if (any_null(in, q, scale) || misaligned(in, q)) return MOE_EINVAL;
   if (static_cast<int64_t>(rows) * moe::ceil_div(K, 128) * 16 >= kMaxThreads) return MOE_EUNSUPPORTED;
   return from_hip(moe::launch_quantize_fp8_block_rows(rows, K, in, q, scale, stream));
@@ -67,7 +68,8 @@ moe_status moe_gemm_fp8_block(int32_t M, int32_t E, int32_t N, int32_t K, const 
                               const int32_t* offsets, const uint8_t* wq, const float* w_scale, const float* row_weight,
                               void* out, hipStream_t stream) {
   if (M < 0 || E <= 0 || N <= 0 || K <= 0) return MOE_EINVAL;
-  if (any_null(aq, a_scale, wq, w_scale, out) || (offsets == nullptr && E != 1)) return MOE_EINVAL;
+  if (any_null(wq, w_scale) || (offsets == nullptr && E != 1)) return MOE_EINVAL;
+  if (M > 0 && any_null(aq, a_scale, out)) return MOE_EINVAL;
   if (misaligned(aq, wq, out)) return MOE_EINVAL;
   if (N % 8 != 0 || K % 16 != 0 || E > 1024 || M >= kMaxRows) return MOE_EUNSUPPORTED;
   if (static_cast<int64_t>(N) * K >= k2G || 256 * static_cast<int64_t>(K) >= k2G || 512 * static_cast<int64_t>(N) >= k2G)

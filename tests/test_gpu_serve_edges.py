@@ -142,3 +142,17 @@ def test_stage_enqueues_on_its_own_device(fmt, monkeypatch):
     for T in (3, 70):
         assert stage.forward(x[:T]).isfinite().all()
     assert made_current == [x.device] * 2
+
+
+def test_no_rows():
+    """Empty tensors, as they are, through the calls and the stage."""
+    E, I, H, k = 4, 64, 128, 2
+    e = lambda *d, dt=BF: torch.empty(*d, dtype=dt, device="cuda")
+    u8, f32 = torch.uint8, torch.float32
+    B.moe_quantize_fp8_block_rows(0, H, e(0, H), e(0, H, dt=u8), e(0, 1, dt=f32))
+    w, sw = torch.zeros(E, I, H, dtype=u8, device="cuda"), torch.zeros(E, 1, 1, device="cuda")
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    B.moe_gemm_fp8_block(0, E, I, H, e(0, H, dt=u8), e(0, 1, dt=f32), off, w, sw, e(0, dt=f32), e(0, I))
+    stage = B.ServingStage(70, k, torch.zeros(E, H, dtype=BF, device="cuda"), [t.to(BF) for t in (w, w, w.transpose(1, 2).contiguous())])
+    y = stage.forward(e(0, H))
+    assert y.shape == (0, H) and y.dtype == BF

@@ -1,0 +1,24 @@
+"""Limits of include/moe_serve.h on the host: empty calls, the largest launches,
+and the shapes of large models. No call here reaches a launch."""
+import ctypes
+
+import pytest
+import torch
+
+FAKE = ctypes.c_void_p(0x1000)  # never dereferenced
+OK, EINVAL, EUNSUPPORTED, EWORKSPACE = 0, 1, 2, 3
+
+
+@pytest.fixture(scope="module")
+def B():
+    from mixture_experts_expert_amd import binding
+    return binding
+
+
+def test_no_rows_need_no_pointers(B):
+    """An empty tensor has none."""
+    assert B.lib.moe_quantize_fp8_block_rows(0, 64, None, None, None, None) == OK
+    assert B.lib.moe_quantize_fp8_block_rows(0, 12, None, None, None, None) == EINVAL
+    gemm = lambda E, off, wq: B.lib.moe_gemm_fp8_block(0, E, 64, 64, None, None, off, wq, FAKE, None, None, None)
+    assert gemm(1, None, FAKE) == OK and gemm(2, FAKE, FAKE) == OK
+    assert gemm(2, None, FAKE) == EINVAL and gemm(2, FAKE, None) == EINVAL
