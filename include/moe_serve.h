@@ -38,7 +38,7 @@ extern "C" {
 
 /* Rows [rows, K] of bf16 -> codes q [rows, K], scale [rows, ceil(K/128)].
  * rows >= 0 and K > 0, K % 8 == 0 (MOE_EINVAL otherwise); rows * ceil(K/128)
- * below 2^28 (MOE_EUNSUPPORTED). */
+ * at most 2^28 - 16 (MOE_EUNSUPPORTED otherwise). */
 moe_status moe_quantize_fp8_block_rows(int32_t rows, int32_t K, const void* in, uint8_t* q, float* scale,
                                        hipStream_t stream);
 

@@ -51,7 +51,8 @@ moe_status moe_quantize_fp8_block_rows(int32_t rows, int32_t K, const void* in, 
   if (rows < 0 || K <= 0 || K % 8 != 0) return MOE_EINVAL;
   if (rows == 0) return MOE_OK;
   if (any_null(in, q, scale) || misaligned(in, q)) return MOE_EINVAL;
-  if (static_cast<int64_t>(rows) * moe::ceil_div(K, 128) * 16 >= kMaxThreads) return MOE_EUNSUPPORTED;
+  // 16 threads per block of 128, in workgroups of 256
+  if (moe::ceil_div64(static_cast<int64_t>(rows) * moe::ceil_div64(K, 128), 16) * 256 >= kMaxThreads) return MOE_EUNSUPPORTED;
   return from_hip(moe::launch_quantize_fp8_block_rows(rows, K, in, q, scale, stream));
 }
 
@@ -59,8 +60,8 @@ moe_status moe_quantize_fp8_block_weights(int32_t E, int32_t N, int32_t K, const
                                           hipStream_t stream) {
   if (E <= 0 || N <= 0 || K <= 0 || K % 8 != 0) return MOE_EINVAL;
   if (any_null(w, q, scale) || misaligned(w, q)) return MOE_EINVAL;
-  if (E * moe::ceil_div64(N, 128) >= kMaxThreads || E * moe::ceil_div64(N, 128) * moe::ceil_div64(K, 128) * 256 >= kMaxThreads)
-    return MOE_EUNSUPPORTED;
+  const int64_t most = kMaxThreads / 256, bands = E * moe::ceil_div64(N, 128);  // a workgroup per block
+  if (bands >= most || bands * moe::ceil_div64(K, 128) >= most) return MOE_EUNSUPPORTED;
   return from_hip(moe::launch_quantize_fp8_block_weights(E, N, K, w, q, scale, stream));
 }
 

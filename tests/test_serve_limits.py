@@ -22,3 +22,15 @@ def test_no_rows_need_no_pointers(B):
     gemm = lambda E, off, wq: B.lib.moe_gemm_fp8_block(0, E, 64, 64, None, None, off, wq, FAKE, None, None, None)
     assert gemm(1, None, FAKE) == OK and gemm(2, FAKE, FAKE) == OK
     assert gemm(2, None, FAKE) == EINVAL and gemm(2, FAKE, None) == EINVAL
+
+
+@pytest.mark.parametrize("rows", [(1 << 28) - 1, (1 << 28) - 15])
+def test_quantize_rows_whole_workgroups(B, rows):
+    """The limit counts the launch's threads, rounded up to workgroups of 16 blocks."""
+    assert B.lib.moe_quantize_fp8_block_rows(rows, 8, FAKE, FAKE, FAKE, None) == EUNSUPPORTED
+
+
+def test_quantize_weights_largest_product(B):
+    top = (1 << 31) - 1
+    for E, N, K in ((255, top, top - 7), (129, top, top - 7), (top, 128, top - 7), (256, top, top - 7)):
+        assert B.lib.moe_quantize_fp8_block_weights(E, N, K, FAKE, FAKE, FAKE, None) == EUNSUPPORTED, (E, N, K)
