@@ -67,7 +67,10 @@ moe_status moe_gemm_fp8_block(int32_t M, int32_t E, int32_t N, int32_t K, const 
  *   a = silu(g) * u,  g = deq(xq[row_token[p]]) deq(Wg[e])^T, u likewise (fp32),
  *   aq [T*k,I], a_scale [T*k,ceil(I/128)]: a in blocks of 1 x 128, from fp32.
  * xq [T,H], x_scale [T,ceil(H/128)]; wq_gate, wq_up [E,I,H] with scales
- * [E,ceil(I/128),ceil(H/128)]. Shapes as moe_gemm_gate_up_fp8. */
+ * [E,ceil(I/128),ceil(H/128)]. A layer's shape, here and below: shape.dtype
+ * MOE_BF16, H and I multiples of 64 below 2^22, I H and T H below 2^31, T k below
+ * 2^30 (MOE_EUNSUPPORTED otherwise), k <= E <= 1024; no limit on E I H, unlike
+ * the calls of moe.h. */
 moe_status moe_gemm_gate_up_fp8_block(moe_shape s, const uint8_t* xq, const float* x_scale, const int32_t* row_token,
                                       const int32_t* offsets, const uint8_t* wq_gate, const float* w_gate_scale,
                                       const uint8_t* wq_up, const float* w_up_scale, uint8_t* aq, float* a_scale,
@@ -82,7 +85,11 @@ moe_status moe_gemm_gate_up_fp8_block(moe_shape s, const uint8_t* xq, const floa
  * itself, as in bf16 (from 2^-62 of the largest of the eight down it fades to
  * zero), and by at most 2^-13 of the largest where that is 2^-114 or more.
  * Every buffer is caller-owned and overwritten; wq_down [E,H,I] with scales
- * [E,ceil(H/128),ceil(I/128)]; H and I below 2^22; ws of ws_bytes >= moe_workspace_bytes(s). */
+ * [E,ceil(H/128),ceil(I/128)]; ws of ws_bytes >=
+ * MOE_FP8_BLOCK_WORKSPACE_BYTES(T, k, E), which moe_workspace_bytes(s) covers
+ * where it is not 0. */
+#define MOE_FP8_BLOCK_WORKSPACE_BYTES(T, k, E) \
+  ((((size_t)(T) * (size_t)(k) + 1023) / 1024 * (size_t)(E) * 4 + 255) / 256 * 256)
 moe_status moe_experts_fp8_block(moe_shape s, const void* x, const int32_t* topk_idx, const float* topk_w,
                                  const uint8_t* wq_gate, const float* w_gate_scale, const uint8_t* wq_up,
                                  const float* w_up_scale, const uint8_t* wq_down, const float* w_down_scale,
@@ -111,8 +118,7 @@ moe_status moe_forward_fused_fp8_block(moe_shape s, const void* x, const void* w
  *   y[t] = bf16(sum over j of a[t,j] W_down[e]^T)     (fp32 accumulation).
  * It equals moe_forward_fused up to rounding (there the logits are an fp32
  * chain and the weight multiplies the down product). T <= 64, k <= 16,
- * T k I below 2^30, shape.dtype MOE_BF16 (MOE_EUNSUPPORTED otherwise:
- * moe_forward_fused).
+ * T k I below 2^30 (MOE_EUNSUPPORTED otherwise: moe_forward_fused).
  * logits [T,E] f32, topk_idx [T,k], topk_w [T,k] f32 and y [T,H] bf16 are
  * outputs. Workspace: ws of ws_bytes >= moe_few_workspace_bytes(s), its
  * contents arbitrary; calls that share one must not overlap in time (their

@@ -780,6 +780,11 @@ def moe_forward_fused_fp8_block(s, x, w_router, logit_bias, wq_gate, w_gate_scal
         s, *[_ptr(t) for t in args], _nbytes(ws, ws_bytes), _stream(stream)))
 
 
+def fp8_block_workspace_bytes(s: moe_shape) -> int:
+    """MOE_FP8_BLOCK_WORKSPACE_BYTES of include/moe_serve.h."""
+    return ((s.T * s.k + 1023) // 1024 * s.E * 4 + 255) // 256 * 256
+
+
 def moe_few_workspace_bytes(s: moe_shape) -> int:
     return int(lib.moe_few_workspace_bytes(s))
 
@@ -863,9 +868,10 @@ class ServingStage:
         self.few_T = min(T, 64) if few else 0
         self.few_ws = e(few, dt=u8) if few else None
         if self.few_T < T:
-            ws = moe_workspace_bytes(shape(T, H, E, k, I, bf16))
-            if ws == 0:
-                raise MoEError("moe_workspace_bytes", 1, "shape rejected")
+            s = shape(T, H, E, k, I, bf16)
+            ws = fp8_block_workspace_bytes(s) if self.block else moe_workspace_bytes(s)
+            if ws <= 0 or (self.block and moe_few_workspace_bytes(shape(1, H, E, min(k, 16), I, bf16)) == 0):
+                raise MoEError("ServingStage", 2, "shape rejected")
             self.ws = e(ws, dt=u8)
             self.buf.update({"counts": e(E, dt=i32), "offsets": e(E + 1, dt=i32), "sorted_to_flat": e(M, dt=i32),
                              "flat_to_sorted": e(M, dt=i32), "row_token": e(M, dt=i32), "row_weight": e(M)})

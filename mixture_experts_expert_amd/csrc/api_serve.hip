@@ -22,21 +22,28 @@ constexpr int64_t k2G = static_cast<int64_t>(1) << 31;
 constexpr int64_t kMaxThreads = static_cast<int64_t>(1) << 32;  // of one launch
 constexpr int64_t kMaxRows = static_cast<int64_t>(1) << 30;     // rows are counted in int32, rounded up to tiles
 
-// moe_workspace_bytes is 0 for the shapes that moe.h's calls reject; which of
-// the two codes those get is settled here, in the same order.
-moe_status check_bf16_shape(const moe_shape& s) {
+// What the serving kernels need: 16-byte rows in whole half steps, offsets
+// within one expert's weights, x, and a tile's rows in 32 bits (an expert's
+// base is formed in 64). Sums over the experts have no limit here.
+moe_status check_serve_shape(const moe_shape& s) {
   if (s.T <= 0 || s.H <= 0 || s.E <= 0 || s.k <= 0 || s.I <= 0) return MOE_EINVAL;
   if (s.k > s.E || s.E > 1024 || static_cast<int64_t>(s.T) * s.k >= k2G) return MOE_EINVAL;
-  if (s.dtype != MOE_BF16 || moe_workspace_bytes(s) == 0) return MOE_EUNSUPPORTED;
-  if (static_cast<int64_t>(s.T) * s.k >= kMaxRows) return MOE_EUNSUPPORTED;
+  if (s.dtype != MOE_BF16 || s.H % 64 != 0 || s.I % 64 != 0) return MOE_EUNSUPPORTED;
+  if (static_cast<int64_t>(s.T) * s.k >= kMaxRows || static_cast<int64_t>(s.I) * s.H >= k2G) return MOE_EUNSUPPORTED;
   if (static_cast<int64_t>(s.T) * s.H >= k2G || 512 * static_cast<int64_t>(s.H) >= k2G ||
       512 * static_cast<int64_t>(s.I) >= k2G)
     return MOE_EUNSUPPORTED;
   return MOE_OK;
 }
 
+// The sort's counts: E per block of 1024 (token, slot) pairs.
+size_t fp8_block_workspace_bytes(const moe_shape& s) {
+  static_assert(moe::kPermBlock == 1024, "the header's formula");
+  return MOE_FP8_BLOCK_WORKSPACE_BYTES(s.T, s.k, s.E);
+}
+
 moe_status check_few(const moe_shape& s) {
-  const moe_status st = check_bf16_shape(s);
+  const moe_status st = check_serve_shape(s);
   if (st != MOE_OK) return st;
   if (s.T > moe::kFewMaxT || s.k > moe::kFewMaxK) return MOE_EUNSUPPORTED;
   return static_cast<int64_t>(s.T) * s.k * s.I * 2 >= k2G ? MOE_EUNSUPPORTED : MOE_OK;  // 32-bit offsets into a
@@ -94,7 +101,7 @@ moe_status moe_gemm_gate_up_fp8_block(moe_shape s, const uint8_t* xq, const floa
                                       const int32_t* offsets, const uint8_t* wq_gate, const float* w_gate_scale,
                                       const uint8_t* wq_up, const float* w_up_scale, uint8_t* aq, float* a_scale,
                                       hipStream_t stream) {
-  const moe_status st = check_bf16_shape(s);
+  const moe_status st = check_serve_shape(s);
   if (st != MOE_OK) return st;
   if (any_null(xq, x_scale, row_token, offsets, wq_gate, w_gate_scale, wq_up, w_up_scale, aq, a_scale))
     return MOE_EINVAL;
@@ -125,15 +132,15 @@ moe_status moe_experts_fp8_block(moe_shape s, const void* x, const int32_t* topk
                                  int32_t* row_token, float* row_weight, uint8_t* xq, float* x_scale, uint8_t* aq,
                                  float* a_scale, void* o_perm, void* y, void* ws, size_t ws_bytes,
                                  hipStream_t stream) {
-  moe_status st = check_bf16_shape(s);
+  moe_status st = check_serve_shape(s);
   if (st != MOE_OK) return st;
   if (any_null(x, topk_idx, topk_w, wq_gate, w_gate_scale, wq_up, w_up_scale, wq_down, w_down_scale, counts, offsets,
                sorted_to_flat, flat_to_sorted, row_token, row_weight, xq, x_scale, aq, a_scale, o_perm, y, ws))
     return MOE_EINVAL;
   if (misaligned(x, wq_gate, wq_up, wq_down, xq, aq, o_perm, y)) return MOE_EINVAL;
-  if (ws_bytes < moe_workspace_bytes(s)) return MOE_EWORKSPACE;
-  if ((st = moe_permute_fused(s, topk_idx, topk_w, counts, offsets, sorted_to_flat, flat_to_sorted, row_token,
-                              row_weight, ws, ws_bytes, stream)) != MOE_OK)
+  if (ws_bytes < fp8_block_workspace_bytes(s)) return MOE_EWORKSPACE;
+  if ((st = from_hip(moe::launch_permute_fused(s, topk_idx, topk_w, counts, offsets, sorted_to_flat, flat_to_sorted,
+                                               row_token, row_weight, ws, stream))) != MOE_OK)
     return st;
   if ((st = moe_quantize_fp8_block_rows(s.T, s.H, x, xq, x_scale, stream)) != MOE_OK) return st;
   if ((st = moe_gemm_gate_up_fp8_block(s, xq, x_scale, row_token, offsets, wq_gate, w_gate_scale, wq_up, w_up_scale, aq,
@@ -164,15 +171,15 @@ moe_status moe_forward_fused_fp8_block(moe_shape s, const void* x, const void* w
                                        int32_t* row_token, float* row_weight, uint8_t* xq, float* x_scale, uint8_t* aq,
                                        float* a_scale, void* o_perm, void* y, void* ws, size_t ws_bytes,
                                        hipStream_t stream) {
-  moe_status st = check_bf16_shape(s);
+  moe_status st = check_serve_shape(s);
   if (st != MOE_OK) return st;
   if (any_null(x, w_router, wq_gate, w_gate_scale, wq_up, w_up_scale, wq_down, w_down_scale, logits, topk_idx, topk_w,
                counts, offsets, sorted_to_flat, flat_to_sorted, row_token, row_weight, xq, x_scale, aq, a_scale, o_perm,
                y, ws))
     return MOE_EINVAL;
   if (misaligned(x, w_router, wq_gate, wq_up, wq_down, xq, aq, o_perm, y)) return MOE_EINVAL;
-  if (ws_bytes < moe_workspace_bytes(s)) return MOE_EWORKSPACE;
-  if ((st = moe_route(s, x, w_router, logit_bias, logits, topk_idx, topk_w, stream)) != MOE_OK) return st;
+  if (ws_bytes < fp8_block_workspace_bytes(s)) return MOE_EWORKSPACE;
+  if ((st = from_hip(moe::launch_route(s, x, w_router, logit_bias, logits, topk_idx, topk_w, stream))) != MOE_OK) return st;
   return moe_experts_fp8_block(s, x, topk_idx, topk_w, wq_gate, w_gate_scale, wq_up, w_up_scale, wq_down, w_down_scale,
                                counts, offsets, sorted_to_flat, flat_to_sorted, row_token, row_weight, xq, x_scale, aq,
                                a_scale, o_perm, y, ws, ws_bytes, stream);

@@ -126,10 +126,13 @@ def test_few_wait_that_gives_up_shows(dims):
 @pytest.mark.parametrize("fmt", ["bf16", "fp8"])
 def test_stage_enqueues_on_its_own_device(fmt, monkeypatch):
     """Whatever the current device is: the calls run with the tensors' device made current."""
-    made_current, real = [], torch.cuda.device
-    def device(d):
-        made_current.append(torch.device(d))
-        return real(d)
+    made_current = []
+
+    class device(torch.cuda.device):
+        def __init__(self, d):
+            made_current.append(torch.device(d))
+            super().__init__(d)
+
     E, I, H, k = 4, 64, 128, 2
     g = torch.Generator().manual_seed(4)
     w = [(torch.randn(E, *d, generator=g) / 8).to(BF).cuda() for d in ((I, H), (I, H), (H, I))]
@@ -156,3 +159,54 @@ def test_no_rows():
     stage = B.ServingStage(70, k, torch.zeros(E, H, dtype=BF, device="cuda"), [t.to(BF) for t in (w, w, w.transpose(1, 2).contiguous())])
     y = stage.forward(e(0, H))
     assert y.shape == (0, H) and y.dtype == BF
+
+
+def _definition(x, wr, k, idx, w, pairs, t):
+    """Token t of the layer on block-scaled weights, float64: y and the sum of magnitudes."""
+    H = x.shape[1]
+    y, mag = torch.zeros(H, dtype=torch.float64, device="cuda"), torch.zeros(H, dtype=torch.float64, device="cuda")
+    for j in range(k):
+        e = int(idx[t, j])
+        gate, up, down = (_weights64(q[e], s[e]) for q, s in pairs)
+        a = float(w[t, j]) * S.silu_mul(gate @ x[t].double(), up @ x[t].double())
+        y += down @ a
+        mag += down.abs() @ a.abs()
+    return y, mag
+
+
+def _weights64(q, s):
+    N, K = q.shape
+    return q.view(F8).double() * s.double().repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+
+
+def test_layer_past_2_to_31_weights():
+    """520 experts of 2048 x 2048: expert bases past 2^31 bytes, in both forms, through the
+    stage, whose workspace holds the sort's counts and nothing else."""
+    E, I, H, k, T = 520, 2048, 2048, 3, 70
+    g = torch.Generator("cuda").manual_seed(5)
+    codes = torch.randint(0, 256, (1 << 22,), generator=g, device="cuda", dtype=torch.uint8)
+    codes = (codes & 0xBF) | 0x10  # magnitudes of 1/32 to 2, and the sign
+    pairs = []
+    for N, K in ((I, H), (I, H), (H, I)):
+        q = torch.empty(E, N, K, dtype=torch.uint8, device="cuda")
+        for e in range(E):
+            q[e] = codes.roll(1009 * e + len(pairs)).view(N, K)
+        pairs.append((q, torch.rand(E, N // 128, K // 128, generator=g, device="cuda") * 0.02))
+    x = torch.randn(T, H, generator=g, device="cuda").to(BF)
+    wr = (torch.randn(E, H, generator=g, device="cuda") / 64).to(BF)
+    bias = torch.zeros(E, device="cuda")
+    bias[-6:] = 3.0  # the last experts, whose bases lie furthest out
+    stage = B.ServingStage(T, k, wr, B.FP8BlockWeights(stored=pairs), bias)
+    whole = torch.full((stage.ws.numel() + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    stage.ws = whole[: stage.ws.numel()]
+    for n in (5, T):
+        y = stage.forward(x[:n]).double()
+        idx = stage.buf["topk_idx"].view(-1)[: n * k].view(n, k)
+        w = stage.buf["topk_w"].view(-1)[: n * k].view(n, k)
+        assert idx.max() == E - 1
+        for t in (0, 3, n - 1):
+            want, mag = _definition(x, wr, k, idx, w, pairs, t)
+            # rounded a and y, in the norm; 70 tokens also quantise x and a: 2^-4 at most each
+            tol = 2**0.5 * U if n <= 64 else 2**0.5 * 2.0**-4 + 2 * U
+            assert (y[t] - want).norm() <= tol * want.norm()
+    assert whole[stage.ws.numel():].eq(0xA5).all()
