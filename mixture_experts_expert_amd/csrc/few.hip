@@ -297,8 +297,8 @@ __device__ __forceinline__ uint32_t row_extreme(uint32_t v) {
 // of logits n + 16 c (sel_key's upper word; 0 for a NaN). A round takes the
 // largest, then the lowest index that has it, and marks that one as taken. The
 // weights follow at once: softmax and renormalisation as moe_route.
-template <int NC, class S_t>
-__device__ __forceinline__ void few_select_rows(const FewParams& P, FewLists& L, S_t& S) {
+template <int NC>
+__device__ __forceinline__ void few_select_rows(const FewParams& P, FewLists& L) {
   const int tid = threadIdx.x, n = tid % 16;
   const int E = P.E, k = P.k;
   for (int t0 = 0; t0 < P.T; t0 += kThreads / 16) {
@@ -359,8 +359,8 @@ __device__ __forceinline__ void few_select_rows(const FewParams& P, FewLists& L,
 
 // Selection for up to 16 tokens: a wavefront per token, logits lane + 64 c.
 // The rounds are the same; the lowest index comes from a ballot.
-template <int NC, class S_t>
-__device__ __forceinline__ void few_select_waves(const FewParams& P, FewLists& L, S_t& S) {
+template <int NC>
+__device__ __forceinline__ void few_select_waves(const FewParams& P, FewLists& L) {
   const int lane = threadIdx.x % kWave;
   const int E = P.E, k = P.k;
   for (int t = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave); t < P.T; t += kNW) {
@@ -434,8 +434,8 @@ template <int TILES, int NC>
 __device__ __forceinline__ void few_select(const FewParams& P, FewLists& L, FewScratch<TILES>& S) {
   const int tid = threadIdx.x, lane = tid % kWave;
   const int E = P.E, pairs = P.T * P.k;
-  if constexpr (TILES == 1) few_select_waves<(NC + 3) / 4>(P, L, S);
-  else few_select_rows<NC>(P, L, S);
+  if constexpr (TILES == 1) few_select_waves<(NC + 3) / 4>(P, L);
+  else few_select_rows<NC>(P, L);
   __syncthreads();
   if (pairs <= kWave) {  // one wavefront, a pair per lane
     if (tid < kWave) {

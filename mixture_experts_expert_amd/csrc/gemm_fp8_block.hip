@@ -85,10 +85,6 @@ __device__ __forceinline__ f32x4 block_product(const i32x8& w, const i32x8& a) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, a, f32x4{}, 0, 0, 0, 0, 0, 0);
 }
 
-__device__ __forceinline__ float lane_value(float v, int src) {
-  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), src));
-}
-
 // silu(g) u with the hardware exponential and reciprocal (about 1 ulp each;
 // the result is rounded to 8 bits).
 __device__ __forceinline__ float silu_mul(float g, float u) {
@@ -521,16 +517,17 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
 // ---- few rows per expert ----------------------------------------------------
 
 constexpr int kTiles = 2;  // 16-row tiles of a per pass over the weights
+constexpr int kAhead = 2;  // steps in registers before their products
 
 // One workgroup: expert e, and 16 columns per wavefront of w0 and w1 (GU), or
 // (kWaves / ks) * 16 columns of w0, each split over ks wavefronts along k.
 //
 // Eight lanes load a row's 128 bytes of a step (loads whose neighbouring lanes
-// are in different rows take four times the address cycles), AHEAD steps ahead
+// are in different rows take four times the address cycles), kAhead steps ahead
 // into registers; a wavefront's own piece of LDS turns them into fragments.
 // Every load is issued in every step, outside the matrix where there is
 // nothing to load: behind a condition the compiler waits for all of them.
-template <bool GU, int AHEAD>
+template <bool GU>
 __global__ __launch_bounds__(kThreads, 2) void block_stream_kernel(const Params P, int ks, int groups) {
   __shared__ __attribute__((aligned(16))) float red[kWaves][16][20];
   __shared__ __attribute__((aligned(16))) uint8_t stage[kWaves][GU ? 3 : 2][16 * KS];
@@ -601,7 +598,7 @@ __global__ __launch_bounds__(kThreads, 2) void block_stream_kernel(const Params 
     auto f32 = [&](const rsrc_t& r, uint32_t off) __attribute__((always_inline)) {
       return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
     };
-    Step st[AHEAD];
+    Step st[kAhead];
     auto fetch = [&](Step& f, int s) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -618,10 +615,10 @@ __global__ __launch_bounds__(kThreads, 2) void block_stream_kernel(const Params 
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) a0[t] = a1[t] = f32x4{};
 #pragma unroll
-    for (int d = 0; d < AHEAD; ++d) fetch(st[d], s0 + d);
+    for (int d = 0; d < kAhead; ++d) fetch(st[d], s0 + d);
     auto batch = [&](auto more, int s) __attribute__((always_inline)) {
 #pragma unroll
-      for (int d = 0; d < AHEAD; ++d) {
+      for (int d = 0; d < kAhead; ++d) {
         const float f0 = st[d].sw0, f1 = GU ? st[d].sw1 : 0.0f;
         uint8_t* own = stage[wave][0];
         put(own, st[d].w0);
@@ -651,11 +648,11 @@ __global__ __launch_bounds__(kThreads, 2) void block_stream_kernel(const Params 
             tile(t, sr);
           }
         }
-        if constexpr (decltype(more)::value) fetch(st[d], s + d + AHEAD);
+        if constexpr (decltype(more)::value) fetch(st[d], s + d + kAhead);
       }
     };
     int s = s0;
-    for (; s + AHEAD < s1; s += AHEAD) batch(std::true_type{}, s);
+    for (; s + kAhead < s1; s += kAhead) batch(std::true_type{}, s);
     batch(std::false_type{}, s);
 #pragma unroll
     for (int t = 0; t < kTiles; ++t) {
@@ -758,7 +755,7 @@ hipError_t launch(const BlockGemmArgs& a, hipStream_t st) {
     if (!GU)
       while (ks < kWaves && static_cast<int64_t>(a.E) * ceil_div(a.N, 16 * kWaves / ks) < 2 * grid && ks < P.KB) ks *= 2;
     const int groups = ceil_div(a.N, 16 * kWaves / ks);
-    block_stream_kernel<GU, 2><<<static_cast<unsigned>(a.E) * groups, kThreads, 0, st>>>(P, ks, groups);
+    block_stream_kernel<GU><<<static_cast<unsigned>(a.E) * groups, kThreads, 0, st>>>(P, ks, groups);
   } else if (avg <= 96) {
     block_tile_kernel<GU, 128><<<grid, kThreads, 0, st>>>(P);
   } else {
