@@ -806,18 +806,20 @@ def moe_forward_few_fp8_block(s, x, w_router, logit_bias, wq_gate, w_gate_scale,
 class FP8BlockWeights:
     """Expert weights in E4M3 with a float32 scale per 128 x 128 block: codes
     gate/up [E,I,H], down [E,H,I] (uint8 or float8_e4m3fn) and their scales. From bf16 weights
-    (moe_quantize_fp8_block_weights), or, with ``stored``, a checkpoint's own
-    (codes, scales) pairs as they are."""
+    (moe_quantize_fp8_block_weights, on ``stream``, which the results then belong
+    to), or, with ``stored``, a checkpoint's own (codes, scales) pairs as they are."""
 
     def __init__(self, w_gate=None, w_up=None, w_down=None, stream=None, stored=None):
         def quant(w):
             if w.dtype != torch.bfloat16 or w.device.type != "cuda" or not w.is_contiguous():
                 raise ValueError("weights have to be bf16, contiguous, on the GPU")
             E, N, K = w.shape
-            q = torch.empty(E, N, K, dtype=torch.uint8, device=w.device)
-            scale = torch.empty(E, -(-N // 128), -(-K // 128), dtype=torch.float32, device=w.device)
-            with torch.cuda.device(w.device):
-                moe_quantize_fp8_block_weights(E, N, K, w, q, scale, stream=stream)
+            with torch.cuda.device(w.device), torch.cuda.stream(stream):  # the results' memory is that stream's
+                q = torch.empty(E, N, K, dtype=torch.uint8, device=w.device)
+                scale = torch.empty(E, -(-N // 128), -(-K // 128), dtype=torch.float32, device=w.device)
+                moe_quantize_fp8_block_weights(E, N, K, w, q, scale)
+            if stream is not None:
+                w.record_stream(stream)
             return q, scale
 
         self.gate, self.up, self.down = stored if stored is not None else (quant(w_gate), quant(w_up), quant(w_down))
@@ -895,6 +897,8 @@ class ServingStage:
         if T == 0:
             return y
         s = shape(T, self.H, self.E, self.k, self.I, torch.bfloat16)
+        if stream is not None:
+            x.record_stream(stream)  # the caller may drop it
         with torch.cuda.device(x.device):
             if T <= self.few_T:
                 fn = moe_forward_few_fp8_block if self.block else moe_forward_few

@@ -210,3 +210,53 @@ def test_layer_past_2_to_31_weights():
             tol = 2**0.5 * U if n <= 64 else 2**0.5 * 2.0**-4 + 2 * U
             assert (y[t] - want).norm() <= tol * want.norm()
     assert whole[stage.ws.numel():].eq(0xA5).all()
+
+
+def _busy(stream):
+    """About 50 ms of waiting on the stream, so that what follows there runs late."""
+    with torch.cuda.stream(stream):
+        torch.cuda._sleep(100_000_000)
+
+
+def test_quantising_on_another_stream_keeps_off_freed_memory():
+    """The codes made on a side stream lie in no block that the current stream still reads."""
+    E, N, K = 16, 1024, 1024  # codes of 16 MiB: blocks of their own in torch's allocator
+    side, here = torch.cuda.Stream(), torch.cuda.current_stream()
+    w = [torch.randn(E, N, K, device="cuda").to(BF) for _ in range(3)]
+    side.wait_stream(here)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    freed = [torch.full((E, N, K), 7, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    _busy(here)
+    kept = [f + 1 for f in freed]
+    del freed
+    w8 = B.FP8BlockWeights(*w, stream=side)
+    torch.cuda.synchronize()
+    assert all(t.eq(8).all() for t in kept)
+    assert all(torch.equal(q, p) and torch.equal(s, r) for (q, s), (p, r) in
+               zip((w8.gate, w8.up, w8.down), ((lambda v: (v.gate, v.up, v.down))(B.FP8BlockWeights(*w)))))
+
+
+def test_inputs_of_another_stream_outlive_the_call():
+    """Weights and x handed to a call on a side stream and dropped by the caller: their memory
+    is not given out again before that stream has read them."""
+    E, I, H, k, T = 4, 1024, 1024, 2, 70
+    g = torch.Generator("cuda").manual_seed(6)
+    w = [torch.randn(E, I, H, generator=g, device="cuda").to(BF) for _ in range(3)]
+    x, wr = torch.randn(T, H, generator=g, device="cuda").to(BF), torch.randn(E, H, generator=g, device="cuda").to(BF)
+    want8 = B.FP8BlockWeights(*w)
+    stage = B.ServingStage(T, k, wr, want8)
+    want = stage.forward(x).clone()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    ws, xs = [t.clone() for t in w], x.clone()
+    torch.cuda.synchronize()
+    _busy(side)
+    got8 = B.FP8BlockWeights(*ws, stream=side)
+    y = stage.forward(xs, stream=side)
+    del ws, xs
+    again = [torch.zeros(E, I, H, dtype=BF, device="cuda") for _ in range(3)] + [torch.zeros(T, H, dtype=BF, device="cuda")]
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and len(again) == 4
+    for a, b in ((got8.gate, want8.gate), (got8.up, want8.up), (got8.down, want8.down)):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
