@@ -26,7 +26,7 @@
 // are read (see there). A row's 128 bytes are eight 16-byte chunks,
 // XOR-swizzled by row so that a 16-lane read touches every bank once. Which
 // weight row sits at which LDS row is chosen so that a lane ends with 8
-// consecutive output columns. Measured: 8192 x 4096 x 4096 in 135 us, 2.0
+// consecutive output columns. Measured: 8192 x 4096 x 4096 in 139 us, 2.0
 // PFLOP/s (2.2 to 2.5 in the steady state of a longer reduction; without the
 // loads it would be 112 us, so the way from L2 to LDS costs the rest); 65536
 // rows over 128 experts, 2048 x 768, 178 us, of which the 520 MB are 101 us.
