@@ -837,6 +837,8 @@ class ServingStage:
     topk_w in ``buf``. Calls of one stage share its workspaces: enqueue them
     on one stream, or order the streams. They run on the weights' device,
     whichever is current; ``stream`` (its current one by default) belongs to it.
+    The buffers are tensors of the stream current at construction: wait for it
+    before a first call on another stream, and for that one before the stage goes.
     """
 
     def __init__(self, max_T: int, k: int, w_router, weights, logit_bias=None):
