@@ -108,6 +108,12 @@ _SIGS = {
     "moe_gemm_gate_up_fp8_block": ([moe_shape] + [_P] * 11, ctypes.c_int),
     "moe_experts_fp8_block": ([moe_shape] + [_P] * 22 + [ctypes.c_size_t, _P], ctypes.c_int),
     "moe_forward_fused_fp8_block": ([moe_shape] + [_P] * 25 + [ctypes.c_size_t, _P], ctypes.c_int),
+    "moe_quantize_i8_rows": ([ctypes.c_int32, ctypes.c_int32] + [_P] * 4, ctypes.c_int),
+    "moe_gemm_i8": ([ctypes.c_int32] * 4 + [_P] * 8, ctypes.c_int),
+    "moe_i8_workspace_bytes": ([moe_shape], ctypes.c_size_t),
+    "moe_gemm_gate_up_i8": ([moe_shape] + [_P] * 11 + [ctypes.c_size_t, _P], ctypes.c_int),
+    "moe_experts_i8": ([moe_shape] + [_P] * 22 + [ctypes.c_size_t, _P], ctypes.c_int),
+    "moe_forward_fused_i8": ([moe_shape] + [_P] * 25 + [ctypes.c_size_t, _P], ctypes.c_int),
     "moe_few_workspace_bytes": ([moe_shape], ctypes.c_size_t),
     "moe_forward_few": ([moe_shape] + [_P] * 11 + [ctypes.c_size_t, _P], ctypes.c_int),
     "moe_forward_few_fp8_block": ([moe_shape] + [_P] * 14 + [ctypes.c_size_t, _P], ctypes.c_int),
@@ -783,6 +789,46 @@ def moe_forward_fused_fp8_block(s, x, w_router, logit_bias, wq_gate, w_gate_scal
 def fp8_block_workspace_bytes(s: moe_shape) -> int:
     """MOE_FP8_BLOCK_WORKSPACE_BYTES of include/moe_serve.h."""
     return ((s.T * s.k + 1023) // 1024 * s.E * 4 + 255) // 256 * 256
+
+
+def moe_quantize_i8_rows(rows, K, x, q, scale, stream=None):
+    _check("moe_quantize_i8_rows", lib.moe_quantize_i8_rows(int(rows), int(K), _ptr(x), _ptr(q), _ptr(scale),
+                                                            _stream(stream)))
+
+
+def moe_gemm_i8(M, E, N, K, aq, a_scale, offsets, wq, w_scale, row_weight, out, stream=None):
+    """offsets None: one expert (E == 1), every row; row_weight None: 1."""
+    _check("moe_gemm_i8", lib.moe_gemm_i8(int(M), int(E), int(N), int(K), _ptr(aq), _ptr(a_scale), _ptr(offsets),
+                                          _ptr(wq), _ptr(w_scale), _ptr(row_weight), _ptr(out), _stream(stream)))
+
+
+def moe_i8_workspace_bytes(s: moe_shape) -> int:
+    return int(lib.moe_i8_workspace_bytes(s))
+
+
+def moe_gemm_gate_up_i8(s, xq, x_scale, row_token, offsets, wq_gate, w_gate_scale, wq_up, w_up_scale, aq, a_scale, ws,
+                        ws_bytes=None, stream=None):
+    args = (xq, x_scale, row_token, offsets, wq_gate, w_gate_scale, wq_up, w_up_scale, aq, a_scale, ws)
+    _check("moe_gemm_gate_up_i8", lib.moe_gemm_gate_up_i8(s, *[_ptr(t) for t in args], _nbytes(ws, ws_bytes),
+                                                          _stream(stream)))
+
+
+def moe_experts_i8(s, x, topk_idx, topk_w, wq_gate, w_gate_scale, wq_up, w_up_scale, wq_down, w_down_scale, counts,
+                   offsets, sorted_to_flat, flat_to_sorted, row_token, row_weight, xq, x_scale, aq, a_scale, o_perm, y,
+                   ws, ws_bytes=None, stream=None):
+    args = (x, topk_idx, topk_w, wq_gate, w_gate_scale, wq_up, w_up_scale, wq_down, w_down_scale, counts, offsets,
+            sorted_to_flat, flat_to_sorted, row_token, row_weight, xq, x_scale, aq, a_scale, o_perm, y, ws)
+    _check("moe_experts_i8", lib.moe_experts_i8(s, *[_ptr(t) for t in args], _nbytes(ws, ws_bytes), _stream(stream)))
+
+
+def moe_forward_fused_i8(s, x, w_router, logit_bias, wq_gate, w_gate_scale, wq_up, w_up_scale, wq_down, w_down_scale,
+                         logits, topk_idx, topk_w, counts, offsets, sorted_to_flat, flat_to_sorted, row_token,
+                         row_weight, xq, x_scale, aq, a_scale, o_perm, y, ws, ws_bytes=None, stream=None):
+    args = (x, w_router, logit_bias, wq_gate, w_gate_scale, wq_up, w_up_scale, wq_down, w_down_scale, logits, topk_idx,
+            topk_w, counts, offsets, sorted_to_flat, flat_to_sorted, row_token, row_weight, xq, x_scale, aq, a_scale,
+            o_perm, y, ws)
+    _check("moe_forward_fused_i8", lib.moe_forward_fused_i8(s, *[_ptr(t) for t in args], _nbytes(ws, ws_bytes),
+                                                            _stream(stream)))
 
 
 def moe_few_workspace_bytes(s: moe_shape) -> int:

@@ -1,0 +1,214 @@
+"""GPU tests of the 8-bit integer operators (include/moe_serve.h) against their
+64-bit definitions (oracle/i8.py).
+
+Tolerances. The codes of bf16 inputs are exact. A product's sums are exact; the
+conversion to fp32, two products of scales and one with the sum are off by 2^-24
+each, the rounding to bf16 by at most 2^-8 of the value. In the expert stage a
+code may fall on the other side of a border that silu(g) u is within 0.01 steps
+of: the 16-bit form in between is off by 2^-16 of its block's maximum (127 / 2^16
+= 0.002 steps), its fp32 arithmetic (scales, exponential, reciprocal: less than 16
+roundings of 2^-24, and the products of codes are exact) by less than 2^-20 of the
+value (127 / 2^20 steps). The oracle says which those are and what each may move."""
+import pytest
+import torch
+
+from mixture_experts_expert_amd import binding as B
+from oracle import i8 as Q
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.bfloat16
+U = 2.0**-8
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def dev(*ts):
+    out = [t.cuda() if t is not None else None for t in ts]
+    return out if len(out) > 1 else out[0]
+
+
+def _same_scale(got, want):
+    """fp32 quotients: half a step, and half the smallest subnormal."""
+    got = got.cpu().double().reshape(want.shape)
+    assert torch.equal(got.isnan(), want.isnan())
+    assert (got - want)[~want.isnan()].abs().le(want[~want.isnan()] * 2.0**-24 + 2.0**-150).all()
+
+
+# ---- quantisers ---------------------------------------------------------------
+
+
+def _rows(R, K, seed):
+    x = torch.randn(R, K, generator=gen(seed)) * torch.exp2(torch.randint(-20, 20, (R, 1), generator=gen(seed + 1)).float())
+    if R > 5:
+        x[0] = 0.0
+        x[1] = 0.0
+        x[1, K // 2] = -2.0**-130  # subnormal
+        x[2] = 3.0e38
+        x[3, : K // 2] = 1.0e-30
+        x[4, K - 1] = float("nan")
+        x[5, 0] = float("-inf")
+    return x.to(BF)
+
+
+@pytest.mark.parametrize("R,K", [(0, 64), (1, 8), (7, 120), (37, 128), (6, 136), (33, 512), (300, 520), (9, 2048),
+                                 (7, 2056), (6, 8192), (6, 8200), (7, 20000)])
+def test_quantize_rows(R, K):
+    x = _rows(R, K, 1)
+    q = torch.full((R + 1, K), 7, dtype=torch.int8, device="cuda")
+    s = torch.full((R + 1,), -1.0, device="cuda")
+    B.moe_quantize_i8_rows(R, K, dev(x) if R else None, q, s)
+    assert (q[R] == 7).all() and s[R] == -1
+    if R:
+        want, scale = Q.codes(x)
+        assert torch.equal(q[:R].cpu(), want)
+        _same_scale(s[:R], scale)
+
+
+def test_quantize_every_quotient():
+    """Every pair of bf16 significands (value, largest): the codes are those of exact division."""
+    m = torch.arange(128) / 128 + 1
+    v = torch.stack([m[:, None].expand(128, 128), m[None].expand(128, 128)], 2).reshape(-1, 2)  # amax, value
+    for shift in range(9):  # the value below the largest
+        for lift in (0, -126):
+            x = torch.zeros(v.shape[0], 64)
+            x[:, 0] = v[:, 0] * 2.0 * 2.0**lift
+            x[:, 5] = -v[:, 1] * 2.0**(lift - shift) if lift == 0 or shift < 1 else 0.0
+            x = x.to(BF)
+            want, scale = Q.codes(x)
+            q = torch.empty(x.shape, dtype=torch.int8, device="cuda")
+            s = torch.empty(x.shape[0], device="cuda")
+            B.moe_quantize_i8_rows(x.shape[0], 64, dev(x), q, s)
+            assert torch.equal(q.cpu(), want)
+            _same_scale(s, scale)
+
+
+# ---- the grouped product --------------------------------------------------------
+
+OFFSETS = {  # name -> rows per expert, rows before and behind
+    "one row": ([1], 0, 0),
+    "stream": ([2, 0, 3, 1, 4], 0, 0),
+    "stream, one long": ([0, 50, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 1], 2, 3),
+    "short tiles": ([7, 0, 64, 65, 1], 3, 5),
+    "long tiles": ([128, 129, 0, 1, 257, 255], 0, 1),
+    "nothing": ([0, 0, 0], 4, 0),
+    "several tiles a workgroup": ([700, 3, 900], 0, 0),
+}
+
+
+@pytest.mark.parametrize("N,K", [(8, 16), (264, 272), (1000, 720), (136, 1040)])
+@pytest.mark.parametrize("rows", list(OFFSETS))
+@pytest.mark.parametrize("weighted", [False, True])
+def test_gemm(rows, N, K, weighted):
+    counts, before, behind = OFFSETS[rows]
+    off = torch.tensor([before] + counts).cumsum(0).to(torch.int32)
+    E, M = len(counts), before + sum(counts) + behind
+    g = gen(3)
+    aq = torch.randint(-128, 128, (M, K), generator=g).to(torch.int8)
+    wq = torch.randint(-128, 128, (E, N, K), generator=g).to(torch.int8)
+    sa, sw = torch.rand(M, generator=g) + 0.01, torch.rand(E, N, generator=g) + 0.01
+    rw = torch.rand(M, generator=g) if weighted else None
+    out = torch.full((M, N), -3.0, dtype=BF, device="cuda")
+    B.moe_gemm_i8(M, E, N, K, *dev(aq, sa, off, wq, sw, rw), out)
+    got = out.cpu().double()
+    r = slice(before, before + sum(counts))
+    assert (got[:before] == -3).all() and (got[r.stop:] == -3).all()
+    want = Q.product(aq, sa, off, wq, sw, rw)[r]
+    assert (got[r] - want).abs().le(want.abs() * (U + 2.0**-21)).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 2048, 2048), (33, 136, 4096), (192, 264, 512), (300, 520, 640), (2000, 512, 256)])
+def test_gemm_dense(M, N, K):
+    """One expert without offsets; the codes' extremes, whose sums are the largest."""
+    aq = torch.full((M, K), -128, dtype=torch.int8)
+    wq = torch.full((1, N, K), -128, dtype=torch.int8)
+    aq[:, ::3], wq[:, :, ::5] = 127, 127
+    aq[M // 2] = torch.randint(-128, 128, (K,), generator=gen(1)).to(torch.int8)
+    sa, sw = torch.rand(M, generator=gen(4)), torch.rand(1, N, generator=gen(5))
+    out = torch.empty(M, N, dtype=BF, device="cuda")
+    aqd, sad, wqd, swd = dev(aq, sa, wq, sw)
+    B.moe_gemm_i8(M, 1, N, K, aqd, sad, None, wqd, swd, None, out)
+    want = Q.product(aq, sa, [0, M], wq, sw)
+    assert (out.cpu().double() - want).abs().le(want.abs() * (U + 2.0**-21)).all()
+
+
+def test_gemm_largest_sums():
+    K = 2**17 - 16
+    for M in (1, 130):
+        aq, wq = torch.full((M, K), -128, dtype=torch.int8), torch.full((1, 8, K), -128, dtype=torch.int8)
+        out = torch.empty(M, 8, dtype=BF, device="cuda")
+        one = torch.ones(M), torch.ones(1, 8)
+        B.moe_gemm_i8(M, 1, 8, K, *dev(aq, one[0]), None, *dev(wq, one[1]), None, out)
+        assert (out.float() == torch.tensor(float(K * 2**14)).to(BF).float().item()).all()
+
+
+def test_gemm_scale_nan_stays_in_its_row():
+    M, N, K = 70, 64, 128
+    aq = torch.randint(-127, 128, (M, K), generator=gen(1)).to(torch.int8)
+    wq = torch.randint(-127, 128, (1, N, K), generator=gen(2)).to(torch.int8)
+    sa, sw = torch.ones(M), torch.ones(1, N)
+    sa[5], sw[0, 9] = float("nan"), float("nan")
+    out = torch.empty(M, N, dtype=BF, device="cuda")
+    B.moe_gemm_i8(M, 1, N, K, *dev(aq, sa), None, *dev(wq, sw), None, out)
+    nan = out.cpu().isnan()
+    want = torch.zeros(M, N, dtype=torch.bool)
+    want[5], want[:, 9] = True, True
+    assert torch.equal(nan, want)
+
+
+# ---- the expert stage -------------------------------------------------------------
+
+
+def stage(T, H, E, k, I, seed, skew=0.0, empty=()):
+    g = gen(seed)
+    x = (torch.randn(T, H, generator=g) * torch.exp(0.5 * torch.randn(T, 1, generator=g))).to(BF)
+    w = [Q.weights((torch.randn(E, N, K, generator=g) * K**-0.5).to(BF)) for N, K in ((I, H), (I, H), (H, I))]
+    w = [(q, s.float()) for q, s in w]
+    score = torch.randn(T, E, generator=g) - skew * torch.arange(E)
+    score[:, list(empty)] = -1e9
+    p, idx = torch.softmax(score, 1).topk(k, dim=1)
+    return x, idx.to(torch.int32), (p / p.sum(1, keepdim=True)).float(), w
+
+
+def run_experts(x, idx, tw, w, stream=None):
+    T, H = x.shape
+    E, I, _ = w[0][0].shape
+    k = idx.shape[1]
+    M = T * k
+    s = B.shape(T, H, E, k, I, BF)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    nb = B.moe_i8_workspace_bytes(s)
+    ws = torch.full((nb + 16,), 0x5a, dtype=torch.uint8, device="cuda")
+    y = torch.empty(T, H, dtype=BF, device="cuda")
+    B.moe_experts_i8(s, *dev(x, idx, tw), *[t for m in w for t in dev(*m)], torch.empty(E, **i32), torch.empty(E + 1, **i32),
+                     torch.empty(M, **i32), torch.empty(M, **i32), torch.empty(M, **i32), torch.empty(M, device="cuda"),
+                     torch.empty(T, H, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda"),
+                     torch.empty(M, I, dtype=torch.int8, device="cuda"), torch.empty(M, device="cuda"),
+                     torch.empty(M, H, dtype=BF, device="cuda"), y, ws, ws_bytes=nb, stream=stream)
+    torch.cuda.synchronize()
+    assert (ws[nb:] == 0x5a).all()
+    return y
+
+
+@pytest.mark.parametrize("T,H,E,k,I,skew,empty", [
+    (1, 64, 1, 1, 64, 0.0, ()), (3, 128, 4, 2, 64, 0.0, (1,)), (70, 192, 4, 2, 320, 0.0, ()),
+    (130, 256, 8, 3, 192, 0.5, (0, 7)), (600, 512, 4, 2, 128, 1.0, ()), (257, 320, 16, 16, 64, 0.0, ())])
+def test_experts(T, H, E, k, I, skew, empty):
+    x, idx, tw, w = stage(T, H, E, k, I, 7, skew, empty)
+    got = run_experts(x, idx, tw, w).cpu().double()
+    y, slack, size = Q.experts(x, idx, tw, *w, near=0.01)
+    # y's rounding; each of the k rows' 16-byte form: 2^-8 of itself; fp32
+    assert (got - y).abs().le(U * y.abs() + (U + 2.0**-20) * size + slack + 1e-30).all()
+    rel = (got - y).norm() / y.norm()
+    assert rel < 2.0**-8, rel
+
+
+def test_experts_rows_without_numbers():
+    """A token with a NaN is NaN, its neighbours are not; a token of zeros is zero."""
+    x, idx, tw, w = stage(70, 128, 4, 2, 128, 9)
+    x[3, 5], x[9] = float("nan"), 0.0
+    got = run_experts(x, idx, tw, w).cpu()
+    assert got[3].isnan().all() and (got[9] == 0).all()
+    assert not torch.cat([got[:3], got[4:]]).isnan().any()
