@@ -1,4 +1,5 @@
-"""Python binding of libmoe's C ABI (include/moe.h, include/moe_serve.h), by ctypes.
+"""Python binding of libmoe's C ABI (include/moe.h, include/moe_serve.h,
+include/moe_i8.h), by ctypes.
 
 Argument marshalling only: every function here has the name of a C entry
 point, checks nothing the library does not check itself, passes torch CUDA
@@ -117,6 +118,7 @@ _SIGS = {
     "moe_few_workspace_bytes": ([moe_shape], ctypes.c_size_t),
     "moe_forward_few": ([moe_shape] + [_P] * 11 + [ctypes.c_size_t, _P], ctypes.c_int),
     "moe_forward_few_fp8_block": ([moe_shape] + [_P] * 14 + [ctypes.c_size_t, _P], ctypes.c_int),
+    "moe_forward_few_i8": ([moe_shape] + [_P] * 14 + [ctypes.c_size_t, _P], ctypes.c_int),
 }
 for _name, (_args, _ret) in _SIGS.items():
     _fn = getattr(lib, _name)
@@ -847,6 +849,14 @@ def moe_forward_few_fp8_block(s, x, w_router, logit_bias, wq_gate, w_gate_scale,
             topk_w, y, ws)
     _check("moe_forward_few_fp8_block", lib.moe_forward_few_fp8_block(
         s, *[_ptr(t) for t in args], _nbytes(ws, ws_bytes), _stream(stream)))
+
+
+def moe_forward_few_i8(s, x, w_router, logit_bias, wq_gate, w_gate_scale, wq_up, w_up_scale, wq_down, w_down_scale, logits,
+                       topk_idx, topk_w, y, ws, ws_bytes=None, stream=None):
+    args = (x, w_router, logit_bias, wq_gate, w_gate_scale, wq_up, w_up_scale, wq_down, w_down_scale, logits, topk_idx,
+            topk_w, y, ws)
+    _check("moe_forward_few_i8", lib.moe_forward_few_i8(s, *[_ptr(t) for t in args], _nbytes(ws, ws_bytes),
+                                                        _stream(stream)))
 
 
 class FP8BlockWeights:

@@ -1,4 +1,4 @@
-// C ABI of the serving operators (moe_serve.h): argument checks on the host,
+// C ABI of the serving operators (moe_serve.h, moe_i8.h): argument checks on the host,
 // then kernel launches. Every check runs before any HIP call, so a rejected
 // call enqueues nothing.
 #include "moe_internal.h"
@@ -384,6 +384,35 @@ moe_status moe_forward_few_fp8_block(moe_shape s, const void* x, const void* w_r
   a.gate_scale = w_gate_scale;
   a.up_scale = w_up_scale;
   a.down_scale = w_down_scale;
+  a.logits = logits;
+  a.topk_idx = topk_idx;
+  a.topk_w = topk_w;
+  a.y = y;
+  return from_hip(moe::launch_few(s, a, ws, stream));
+}
+
+moe_status moe_forward_few_i8(moe_shape s, const void* x, const void* w_router, const float* logit_bias,
+                              const int8_t* wq_gate, const float* w_gate_scale, const int8_t* wq_up,
+                              const float* w_up_scale, const int8_t* wq_down, const float* w_down_scale, float* logits,
+                              int32_t* topk_idx, float* topk_w, void* y, void* ws, size_t ws_bytes, hipStream_t stream) {
+  const moe_status st = check_few(s);
+  if (st != MOE_OK) return st;
+  if (any_null(x, w_router, wq_gate, w_gate_scale, wq_up, w_up_scale, wq_down, w_down_scale, logits, topk_idx, topk_w, y,
+               ws))
+    return MOE_EINVAL;
+  if (misaligned(x, w_router, wq_gate, w_gate_scale, wq_up, w_up_scale, wq_down, w_down_scale, y, ws)) return MOE_EINVAL;
+  if (ws_bytes < moe::few_layout(s).total) return MOE_EWORKSPACE;
+  moe::FewArgs a{};
+  a.x = x;
+  a.w_router = w_router;
+  a.bias = logit_bias;
+  a.w_gate = wq_gate;
+  a.w_up = wq_up;
+  a.w_down = wq_down;
+  a.gate_scale = w_gate_scale;
+  a.up_scale = w_up_scale;
+  a.down_scale = w_down_scale;
+  a.i8 = true;
   a.logits = logits;
   a.topk_idx = topk_idx;
   a.topk_w = topk_w;

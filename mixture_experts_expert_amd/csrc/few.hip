@@ -52,14 +52,15 @@
 //
 // Tile: v_mfma_f32_16x16x32_bf16 with the weights as A (16 rows) and up to 16
 // token rows as B, so a lane's four results are four consecutive columns of
-// one row. A step is 128 bytes of each weight row: 64 bf16 or 128 E4M3 codes
+// one row. A step is 128 bytes of each weight row: 64 bf16 or 128 8-bit codes
 // (one scale block; a last half block reads zeros). Loads take a row's 128
 // bytes with eight neighbouring lanes (a load in the product's own layout,
 // neighbouring lanes in different rows, costs the address unit 64 cycles
 // instead of 16), and the steps change layout through LDS of the wavefront's
 // own, weights and token rows alike: no barrier, and the registers stay the
 // prefetch buffer. E4M3 weights are widened to bf16 (exact) and each step's
-// product is multiplied by its block's scale in fp32.
+// product is multiplied by its block's scale in fp32. Whole numbers of 8 bits are
+// widened likewise (exact), and a row's scale multiplies its finished sum.
 #include "moe_internal.h"
 #include "select.h"
 
@@ -73,7 +74,7 @@ typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kBf16 = 0, kFp8 = 1;  // weight formats
+constexpr int kBf16 = 0, kFp8 = 1, kI8 = 2;  // weight formats
 constexpr int kNW = 8;              // wavefronts per workgroup
 constexpr int kThreads = kNW * kWave;
 constexpr int kGC = 8, kDC = 16;   // columns per gate/up and per down unit
@@ -88,8 +89,8 @@ constexpr uint32_t kNoRow = 0x80000000u;  // an offset past every row, whatever 
 struct FewParams {
   int T, H, E, k, I;
   const bf16_t* x;
-  const void *w0, *w1, *w2;     // gate, up, down: bf16 or E4M3 codes
-  const float *s0, *s1, *s2;    // block scales (E4M3)
+  const void *w0, *w1, *w2;     // gate, up, down: bf16 or 8-bit codes
+  const float *s0, *s1, *s2;    // scales: per block (E4M3) or per row (whole numbers)
   const float* logits;
   int32_t* topk_idx;
   float* topk_w;
@@ -211,6 +212,16 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t a, uint32_t b) {  // eight E4M
   return bf16x8{r0.x, r0.y, r1.x, r1.y, r2.x, r2.y, r3.x, r3.y};
 }
 
+__device__ __forceinline__ bf16x8 whole8(uint32_t a, uint32_t b) {  // eight whole numbers
+  bf16x8 o;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[i] = static_cast<__bf16>(static_cast<float>(static_cast<int8_t>(a >> (8 * i))));
+    o[4 + i] = static_cast<__bf16>(static_cast<float>(static_cast<int8_t>(b >> (8 * i))));
+  }
+  return o;
+}
+
 __device__ __forceinline__ void put_w(char* lds, const u32x4 (&w)[2]) {
   const int lane = threadIdx.x % kWave, row = lane / 8, chunk = lane % 8;
 #pragma unroll
@@ -234,6 +245,14 @@ __device__ __forceinline__ void multiply(f32x4& acc, const char* lds, float scal
       const u32x4 w = at(w_slot(row, 4 * h + g)), x = at(x_slot<FMT>(row, 4 * h + g));
       acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), __builtin_bit_cast(bf16x8, x), acc,
                                                     0, 0, 0);
+    }
+  } else if constexpr (FMT == kI8) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const u32x4 w = at(w_slot(row, 4 * h + g));
+      const u32x4 x0 = at(x_slot<FMT>(row, 2 * (4 * h + g))), x1 = at(x_slot<FMT>(row, 2 * (4 * h + g) + 1));
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(whole8(w.x, w.y), __builtin_bit_cast(bf16x8, x0), acc, 0, 0, 0);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(whole8(w.z, w.w), __builtin_bit_cast(bf16x8, x1), acc, 0, 0, 0);
     }
   } else {
     f32x4 p = f32x4{};
@@ -613,6 +632,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
   const rsrc_t xs = make_rsrc(P.x, static_cast<int64_t>(T) * H * 2);
   Step<FMT, XR> st[2][NB];
   float sa[2] = {1.0f, 1.0f}, sb[2] = {1.0f, 1.0f};  // E4M3: lane d, the scales of the batch's step d
+  float2 ra[2], rb[2];  // whole numbers: the scales of the batch's unit, of the columns that this lane sums (finish)
   f32x4 acc[TILES];
   auto clear = [&]() __attribute__((always_inline)) {
 #pragma unroll
@@ -668,6 +688,11 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
       sa[B] = P.s0[sc];
       sb[B] = P.s1[sc];
     }
+    if constexpr (FMT == kI8) {
+      const int64_t sc = static_cast<int64_t>(e) * I + c * GC + part * kGC + 2 * (lane % 4);
+      ra[B] = *reinterpret_cast<const float2*>(P.s0 + sc);
+      rb[B] = *reinterpret_cast<const float2*>(P.s1 + sc);
+    }
   };
   // The products of batch j of unit u, in set B.
   auto use = [&](auto setc, int u, int j) __attribute__((always_inline)) {
@@ -708,7 +733,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
   // in wavefront order, two columns of a row per lane.
   uint32_t* pending = nullptr;  // counter of a tile whose stores may still be under way
   int turn = 0;
-  auto finish = [&](int u) __attribute__((always_inline)) {
+  auto finish = [&](auto setc, int u) __attribute__((always_inline)) {
+    constexpr int B = decltype(setc)::value;  // the unit's last batch
     const int a = u / gpe, c = u - a * gpe, first = L.start[a], rows = L.start[a + 1] - first, tiles = (rows + 15) / 16;
     if (pending != nullptr) {  // older than the last batch's loads
       asm volatile("" ::: "memory");
@@ -732,6 +758,12 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
         vg.y += x.y;
         vu.x += y.x;
         vu.y += y.y;
+      }
+      if constexpr (FMT == kI8) {
+        vg.x *= ra[B].x;
+        vg.y *= ra[B].y;
+        vu.x *= rb[B].x;
+        vu.y *= rb[B].y;
       }
       if (16 * t + row < rows) {
         const int pair = L.list[first + 16 * t + row];
@@ -769,7 +801,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
       auto turn_over = [&](auto setc) __attribute__((always_inline)) {
         use(setc, u, j);
         if (++j == batches) {
-          finish(u);
+          finish(setc, u);
           u = un;
           un = after(u);
           j = 0;
@@ -811,6 +843,10 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
     };
     rsrc_t rw = cw.q < d1 ? weights_of(cw.a) : make_rsrc(P.w2, 0);
     float sc[2][NB];  // E4M3: the steps' scales
+    f32x4 rs{};       // whole numbers: lane 4 i + j, the scales of columns 4 j .. 4 j + 3 of the group's expert i
+    if constexpr (FMT == kI8)
+      rs = *reinterpret_cast<const f32x4*>(P.s2 + static_cast<int64_t>(L.expert[min(a0 + lane / 4, a_end - 1)]) * H +
+                                           c * kDC + 4 * (lane % 4));
     auto fetch_w = [&](auto setc) __attribute__((always_inline)) {
       constexpr int B = decltype(setc)::value;
 #pragma unroll
@@ -885,13 +921,17 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
           multiply_tile(t, f);
           ++cu.q;
           if (++cu.s == spe || cu.q == d1) {  // this expert's products into the tile, row by row
+            f32x4 rc{1.0f, 1.0f, 1.0f, 1.0f};
+            if constexpr (FMT == kI8)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) rc[i] = __shfl(rs[i], 4 * (cu.a - a0) + g, kWave);
 #pragma unroll
             for (int t = 0; t < TILES; ++t) {
               if (16 * t + col < rows) {
                 f32x4* to = reinterpret_cast<f32x4*>(tile + L.token[first + 16 * t + col] * TS + 4 * g);
                 f32x4 v = *to;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] += acc[t][i];
+                for (int i = 0; i < 4; ++i) v[i] = FMT == kI8 ? fmaf(rc[i], acc[t][i], v[i]) : v[i] + acc[t][i];
                 *to = v;
               }
             }
@@ -1044,7 +1084,11 @@ hipError_t launch_few(const moe_shape& s, const FewArgs& a, void* ws, hipStream_
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   const unsigned grid = static_cast<unsigned>(gemm_grid());
-  if (a.gate_scale != nullptr) {
+  if (a.i8) {
+    if (s.E <= 128) launch_layer<kI8, 8>(P, grid, st);
+    else if (s.E <= 256) launch_layer<kI8, 16>(P, grid, st);
+    else launch_layer<kI8, 64>(P, grid, st);
+  } else if (a.gate_scale != nullptr) {
     if (s.E <= 128) launch_layer<kFp8, 8>(P, grid, st);
     else if (s.E <= 256) launch_layer<kFp8, 16>(P, grid, st);
     else launch_layer<kFp8, 64>(P, grid, st);

@@ -7,6 +7,7 @@
 
 #include "moe.h"
 #include "moe_serve.h"
+#include "moe_i8.h"
 
 namespace moe {
 
@@ -325,8 +326,9 @@ FewLayout few_layout(const moe_shape& s);
 struct FewArgs {
   const void *x, *w_router;
   const float* bias;
-  const void *w_gate, *w_up, *w_down;  // bf16, or E4M3 codes with the scales
+  const void *w_gate, *w_up, *w_down;  // bf16, or codes with the scales
   const float *gate_scale, *up_scale, *down_scale;
+  bool i8;                             // the codes are whole numbers with a scale per row, not E4M3 blocks
   float* logits;
   int32_t* topk_idx;
   float* topk_w;

@@ -14,6 +14,7 @@ import torch
 
 from mixture_experts_expert_amd import binding as B
 from oracle import i8 as Q
+from oracle import serve as S
 
 pytestmark = pytest.mark.gpu
 
@@ -212,3 +213,54 @@ def test_experts_rows_without_numbers():
     got = run_experts(x, idx, tw, w).cpu()
     assert got[3].isnan().all() and (got[9] == 0).all()
     assert not torch.cat([got[:3], got[4:]]).isnan().any()
+
+
+# ---- the few-token layer --------------------------------------------------------
+
+
+def few_stage(T, H, E, k, I, seed):
+    g = gen(seed)
+    x = torch.randn(T, H, generator=g).to(BF)
+    wr = (0.1 * torch.randn(E, H, generator=g)).to(BF)
+    bias = 0.1 * torch.randn(E, generator=g)
+    w = [Q.weights((torch.randn(E, N, K, generator=g) * K**-0.5).to(BF)) for N, K in ((I, H), (I, H), (H, I))]
+    return x, wr, bias, [(q, s.float()) for q, s in w]
+
+
+def run_few(x, wr, bias, w, k, ws=None, stream=None):
+    T, H = x.shape
+    E, I, _ = w[0][0].shape
+    s = B.shape(T, H, E, k, I, BF)
+    if ws is None:
+        ws = torch.full((B.moe_few_workspace_bytes(s),), 0xFF, dtype=torch.uint8, device="cuda")
+    out = (torch.empty(T, E, device="cuda"), torch.empty(T, k, dtype=torch.int32, device="cuda"),
+           torch.empty(T, k, device="cuda"), torch.empty(T, H, dtype=BF, device="cuda"))
+    B.moe_forward_few_i8(s, *dev(x, wr, bias), *[t for m in w for t in dev(*m)], *out, ws, stream=stream)
+    torch.cuda.synchronize()
+    return [t.cpu() for t in out]
+
+
+@pytest.mark.parametrize("T,H,E,k,I", [(1, 64, 1, 1, 64), (1, 2048, 32, 8, 768), (2, 192, 4, 2, 320), (16, 128, 8, 3, 64),
+                                       (17, 256, 8, 2, 192), (33, 512, 32, 8, 128), (64, 320, 4, 2, 64), (64, 128, 64, 16, 64),
+                                       (64, 64, 300, 9, 64)])
+def test_few(T, H, E, k, I):
+    x, wr, bias, w = few_stage(T, H, E, k, I, 11)
+    logits, idx, tw, y = run_few(x, wr, bias, w, k)
+    deq = [Q.weight_values(*m) for m in w]
+    lg, _, want_w, want, size = S.few(x, wr, bias, k, *deq, idx=idx.long())
+    assert (logits.double() - lg).abs().le(lg.abs() * 2.0**-24 + 1e-30).all()
+    assert torch.equal(idx.long(), S.route(logits, k)[0])
+    assert torch.allclose(tw.double(), want_w, rtol=2e-6)
+    # a rounded to bf16, y rounded to bf16, fp32 sums
+    assert (y.double() - want).abs().le(U * want.abs() + (U + 2.0**-18) * size).all()
+    assert (y.double() - want).norm() < 2.0**0.5 * U * want.norm()
+
+
+def test_few_tokens_that_are_not_finite_stay_apart():
+    x, wr, bias, w = few_stage(40, 192, 8, 2, 192, 5)
+    good = run_few(x, wr, bias, w, 2)[3]
+    x[7, 3], x[20, 100] = float("nan"), float("inf")
+    y = run_few(x, wr, bias, w, 2)[3]
+    keep = torch.ones(40, dtype=torch.bool)
+    keep[[7, 20]] = False
+    assert y[7].isnan().all() and not y[20].isfinite().any() and torch.equal(y[keep], good[keep])
