@@ -50,13 +50,13 @@ moe_status moe_gemm_i8(int32_t M, int32_t E, int32_t N, int32_t K, const int8_t*
                        hipStream_t stream);
 
 /* Bytes of workspace of the three calls below (0 for a shape they reject): the
- * sort's counts, and silu(g) u in 16 bits between product and codes. */
+ * sort's counts, and silu(g) u in 24 bits between product and codes. */
 size_t moe_i8_workspace_bytes(moe_shape s);
 
 /* Gathered gate/up GEMM with the SwiGLU epilogue, its result quantised per row:
  *   v = silu(g) * u,  g = deq(xq[row_token[p]]) deq(Wg[e])^T, u likewise,
- *   aq [T*k,I], a_scale [T*k]: v's codes. In between v is held in 16 bits of its
- *   largest magnitude in 128 columns, a 500th of a code's step.
+ *   aq [T*k,I], a_scale [T*k]: v's codes. In between v is held in 24 bits of its
+ *   largest magnitude in 128 columns.
  * xq [T,H], x_scale [T]; wq_gate, wq_up [E,I,H] with scales [E,I]. The shape
  * limits of moe_gemm_gate_up_fp8_block, and H and I below 2^17, T k I below 2^35
  * - 2048 (MOE_EUNSUPPORTED otherwise). ws of ws_bytes >= moe_i8_workspace_bytes(s),

@@ -42,17 +42,18 @@ size_t fp8_block_workspace_bytes(const moe_shape& s) {
   return MOE_FP8_BLOCK_WORKSPACE_BYTES(s.T, s.k, s.E);
 }
 
-// The integer stage's workspace: the sort's counts, then silu(g) u in 16 bits
-// and its maxima per 128 columns.
+// The integer stage's workspace: the sort's counts, then silu(g) u in 16 and 8
+// bits and its maxima per 128 columns.
 struct I8Layout {
-  size_t v16, amax, total;
+  size_t v16, v8, amax, total;
 };
 I8Layout i8_layout(const moe_shape& s) {
   auto up = [](size_t v) { return (v + 255) & ~static_cast<size_t>(255); };
   const size_t M = static_cast<size_t>(s.T) * s.k;
   I8Layout l;
   l.v16 = fp8_block_workspace_bytes(s);
-  l.amax = up(l.v16 + M * s.I * 2);
+  l.v8 = up(l.v16 + M * s.I * 2);
+  l.amax = up(l.v8 + M * s.I);
   l.total = up(l.amax + M * moe::ceil_div(s.I, 128) * 4);
   return l;
 }
@@ -271,10 +272,11 @@ moe_status moe_gemm_gate_up_i8(moe_shape s, const int8_t* xq, const float* x_sca
   g.w1 = wq_up;
   g.w1_scale = w_up_scale;
   g.v16 = reinterpret_cast<int16_t*>(static_cast<char*>(ws) + l.v16);
+  g.v8 = static_cast<uint8_t*>(ws) + l.v8;
   g.amax = reinterpret_cast<float*>(static_cast<char*>(ws) + l.amax);
   const moe_status done = from_hip(moe::launch_gemm_i8(g, stream));
   if (done != MOE_OK) return done;
-  return from_hip(moe::launch_requantize_i8_rows(g.M, s.I, g.v16, g.amax, aq, a_scale, stream));
+  return from_hip(moe::launch_requantize_i8_rows(g.M, s.I, g.v16, g.v8, g.amax, aq, a_scale, stream));
 }
 
 moe_status moe_experts_i8(moe_shape s, const void* x, const int32_t* topk_idx, const float* topk_w,

@@ -24,10 +24,12 @@
 //
 // The gate/up forms end with v = silu(g) u, which the down product takes as
 // 8-bit codes with one scale per row. A workgroup holds 128 columns of a row,
-// not all of them: it writes v in 16 bits, scaled by those 128 columns' largest
-// magnitude, and launch_requantize_i8_rows (i8.hip) makes the codes once all
-// maxima are there. bf16 in between would be as many bytes and would move a
-// tenth of the codes (half a step near the row's maximum is 2^-8 of it).
+// not all of them: it writes v in 24 bits (16 and 8 apart), scaled by those 128
+// columns' largest magnitude, and launch_requantize_i8_rows (i8.hip) makes the
+// codes once all maxima are there. With 16 bits one code in 500 falls on the
+// other side of its border, and since a code's step is large beside most of a
+// row's values (silu(g) u has long tails) that is y's error 0.0026 instead of
+// 0.0019 (192 tokens, 30B shape); bf16 in between would move a tenth of them.
 #include <type_traits>
 
 #include "shared8.h"
@@ -56,7 +58,8 @@ struct Params {
   const float* row_weight;
   bf16_t* out;
   bool shared8;             // out in shared8.h's form
-  int16_t* v16;
+  int16_t* v16;             // the upper 16 bits of silu(g) u, the lower 8, the maxima
+  uint8_t* v8;
   float* amax;
 };
 
@@ -75,19 +78,28 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(g * -1.4426950408889634f)) * u;
 }
 
-// The 16-bit form of values whose largest magnitude is m: 32767 v / m. A block
+// The 24-bit form of values whose largest magnitude is m: kFull24 v / m. A block
 // with a NaN has m NaN, and with it the row's scale.
-struct Factor16 {
-  float up, r;  // up lifts blocks below 2^-64 by 2^64 (exact), so that 32767 / m stays finite
-  __device__ __forceinline__ explicit Factor16(float m) {
+struct Factor24 {
+  float up, r;  // up lifts blocks below 2^-64 by 2^64 (exact), so that 2^23 / m stays finite
+  __device__ __forceinline__ explicit Factor24(float m) {
     up = m < 0x1p-64f ? 0x1p64f : 1.0f;
-    r = m > 0.0f ? 32767.0f / (m * up) : 0.0f;
+    r = m > 0.0f ? kFull24 / (m * up) : 0.0f;
   }
 };
-__device__ __forceinline__ uint32_t pack16(float a, float b, const Factor16& f) {
-  const int x = static_cast<int>(__builtin_rintf(a * f.up * f.r)), y = static_cast<int>(__builtin_rintf(b * f.up * f.r));
-  return __builtin_amdgcn_perm(static_cast<uint32_t>(y), static_cast<uint32_t>(x), 0x05040100u);
-}
+// Four values: the upper 16 bits of each, and the lower 8.
+struct Packed24 {
+  uint32_t hi[2], lo;
+  __device__ __forceinline__ Packed24(const f32x4& v, const Factor24& f) {
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = static_cast<uint32_t>(static_cast<int>(__builtin_rintf(v[i] * f.up * f.r)));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) hi[i] = __builtin_amdgcn_perm(c[2 * i + 1], c[2 * i], 0x06050201u);
+    lo = __builtin_amdgcn_perm(__builtin_amdgcn_perm(c[3], c[2], 0x0c0c0400u), __builtin_amdgcn_perm(c[1], c[0], 0x0c0c0400u),
+                               0x05040100u);
+  }
+};
 
 __device__ __forceinline__ float max4(float m, const f32x4& v) {  // NaN if one is
 #pragma unroll
@@ -120,7 +132,7 @@ __global__ __launch_bounds__(kThreads, 2) void i8_tile_kernel(const Params P) {
   constexpr int HA = BM / 128;              // load instructions of half a's rows per wavefront
   constexpr int OS = BM / 2 * KS;
   constexpr int TN = GU ? BN / 2 : BN;
-  constexpr int G1 = HA, G2 = 4 + HA, STORES = 2 * FM;
+  constexpr int G1 = HA, G2 = 4 + HA, STORES = (GU ? 3 : 2) * FM;
   // A stage, in three arrays, so that the compiler sees which reads follow
   // which loads: the weights' rows, the first and the second half's rows of a.
   __shared__ __attribute__((aligned(1024))) uint8_t w0[BN * KS];
@@ -382,6 +394,7 @@ __global__ __launch_bounds__(kThreads, 2) void i8_tile_kernel(const Params P) {
     if constexpr (GU) {
       const int NT = (A->N + 127) / 128;
       const rsrc_t rv = make_rsrc(A->v16 + static_cast<int64_t>(row0) * A->N, static_cast<int64_t>(valid) * A->N * 2);
+      const rsrc_t rl = make_rsrc(A->v8 + static_cast<int64_t>(row0) * A->N, static_cast<int64_t>(valid) * A->N);
       const rsrc_t rm = make_rsrc(A->amax + static_cast<int64_t>(row0) * NT, static_cast<int64_t>(valid) * NT * 4);
       f32x4 cs[4];
 #pragma unroll
@@ -411,17 +424,20 @@ __global__ __launch_bounds__(kThreads, 2) void i8_tile_kernel(const Params P) {
       for (int i = 0; i < FM; ++i) {
         const int r = row_of(i, q);
         u32x4 o{};
+        u32x2 lo{};
         float m = 0.0f;
         if (i < NI) {
           m = max4(0.0f, *reinterpret_cast<const f32x4*>(amax[r]));
-          const Factor16 f(m);
-          const f32x4 v0 = __builtin_bit_cast(f32x4, acc[i][0]), v1 = __builtin_bit_cast(f32x4, acc[i][1]);
-          o = u32x4{pack16(v0[0], v0[1], f), pack16(v0[2], v0[3], f), pack16(v1[0], v1[1], f), pack16(v1[2], v1[3], f)};
+          const Factor24 f(m);
+          const Packed24 p0(__builtin_bit_cast(f32x4, acc[i][0]), f), p1(__builtin_bit_cast(f32x4, acc[i][1]), f);
+          o = u32x4{p0.hi[0], p0.hi[1], p1.hi[0], p1.hi[1]};
+          lo = u32x2{p0.lo, p1.lo};
         }
         const int n = n0 + wn * 32 + 8 * g;
         const bool row = i < NI && r < valid;
-        __builtin_amdgcn_raw_buffer_store_b128(
-            o, rv, row && n < A->N ? (static_cast<uint32_t>(r) * A->N + n) * 2 : kOutside, 0, 0);
+        const uint32_t to = row && n < A->N ? static_cast<uint32_t>(r) * A->N + n : kOutside;
+        __builtin_amdgcn_raw_buffer_store_b128(o, rv, to == kOutside ? to : 2 * to, 0, 0);
+        __builtin_amdgcn_raw_buffer_store_b64(lo, rl, to, 0, 0);
         __builtin_amdgcn_raw_buffer_store_b32(
             __float_as_uint(m), rm, row && wn == 0 && g == 0 ? (static_cast<uint32_t>(r) * NT + n0 / 128) * 4 : kOutside, 0,
             0);
@@ -632,10 +648,12 @@ __global__ __launch_bounds__(kThreads, 2) void i8_stream_kernel(const Params P, 
         __syncthreads();
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) m = __builtin_elementwise_maximum(m, __int_as_float(red[w][q][0]));
-        const Factor16 f(m);
         if (r < rows) {
-          if (n < N)
-            *reinterpret_cast<uint2*>(P.v16 + p * N + n) = make_uint2(pack16(v[0], v[1], f), pack16(v[2], v[3], f));
+          if (n < N) {
+            const Packed24 o(v, Factor24(m));
+            *reinterpret_cast<uint2*>(P.v16 + p * N + n) = make_uint2(o.hi[0], o.hi[1]);
+            *reinterpret_cast<uint32_t*>(P.v8 + p * N + n) = o.lo;
+          }
           if (wave == 0 && g == 0) P.amax[p * ((N + 127) / 128) + grp] = m;
         }
       } else {
@@ -684,6 +702,7 @@ hipError_t launch(const I8GemmArgs& a, hipStream_t st) {
   P.out = static_cast<bf16_t*>(a.out);
   P.shared8 = a.shared8;
   P.v16 = a.v16;
+  P.v8 = a.v8;
   P.amax = a.amax;
   const unsigned grid = static_cast<unsigned>(gemm_grid());
   const int KB = ceil_div(a.K, KS);

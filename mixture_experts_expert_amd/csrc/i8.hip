@@ -3,7 +3,7 @@
 // backward pass) and back; and the second half of the gate/up product's
 // quantisation. See i8.h for the codes.
 //
-// All are bound by memory (3 bytes per element, 2 + 1 in the last): every value
+// All are bound by memory (3 bytes per element, 4 in the last): every value
 // is read once and stays in registers between its row's maximum and its code.
 #include "i8.h"
 
@@ -98,11 +98,11 @@ __global__ __launch_bounds__(kThreads) void dequantize_ckpt8_kernel(uint32_t blo
   out[at] = o;
 }
 
-// Rows of 16-bit codes with a maximum per 128 columns (amax, NT per row) -> 8-bit
-// codes with a scale per row: the product v of a row is known to 2^-16 of its
-// block's maximum, a 500th of a code's step at most.
+// Rows of 24-bit codes with a maximum per 128 columns (amax, NT per row) -> 8-bit
+// codes with a scale per row.
 __global__ __launch_bounds__(kThreads) void requantize_rows_kernel(uint32_t total, uint32_t chunks, int NT,
                                                                    const uint4* __restrict__ v16,
+                                                                   const uint2* __restrict__ v8,
                                                                    const float* __restrict__ amax,
                                                                    uint2* __restrict__ q, float* __restrict__ scale) {
   const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
@@ -110,16 +110,20 @@ __global__ __launch_bounds__(kThreads) void requantize_rows_kernel(uint32_t tota
   const uint32_t row = i / chunks, c = i - row * chunks;
   const float* a = amax + static_cast<int64_t>(row) * NT;
   const uint4 v = v16[i];
+  const uint2 lo = v8[i];
   float m = 0.0f;
   for (int t = 0; t < NT; ++t) m = __builtin_elementwise_maximum(m, a[t]);  // NaN if one is
   const bool finite = m < __builtin_inff();
-  const float f = finite && m > 0.0f ? a[c / 16] / m * (127.0f / 32767.0f) : 0.0f;
+  const float f = finite && m > 0.0f ? a[c / 16] / m * (127.0f / kFull24) : 0.0f;
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   uint32_t k[8];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    k[2 * j] = code_bits(static_cast<float>(static_cast<int16_t>(w[j])) * f);
-    k[2 * j + 1] = code_bits(static_cast<float>(static_cast<int32_t>(w[j]) >> 16) * f);
+    const uint32_t l = (j < 2 ? lo.x : lo.y) >> 16 * (j & 1);
+    const int even = static_cast<int>(static_cast<int16_t>(w[j])) * 256 + static_cast<int>(l & 0xff);
+    const int odd = (static_cast<int>(w[j]) >> 16) * 256 + static_cast<int>(l >> 8 & 0xff);
+    k[2 * j] = code_bits(static_cast<float>(even) * f);
+    k[2 * j + 1] = code_bits(static_cast<float>(odd) * f);
   }
   q[i] = make_uint2(bytes4(k[0], k[1], k[2], k[3]), bytes4(k[4], k[5], k[6], k[7]));
   if (c == 0) scale[row] = finite ? m / 127.0f : __builtin_nanf("");
@@ -157,11 +161,11 @@ hipError_t launch_dequantize_ckpt8(int rows, int K, const int8_t* q, const float
   return hipGetLastError();
 }
 
-hipError_t launch_requantize_i8_rows(int rows, int K, const void* v16, const float* amax, int8_t* q, float* scale,
-                                     hipStream_t st) {
+hipError_t launch_requantize_i8_rows(int rows, int K, const void* v16, const void* v8, const float* amax, int8_t* q,
+                                     float* scale, hipStream_t st) {
   const uint32_t chunks = static_cast<uint32_t>(K / 8), total = static_cast<uint32_t>(rows) * chunks;
   requantize_rows_kernel<<<(total + kThreads - 1) / kThreads, kThreads, 0, st>>>(
-      total, chunks, ceil_div(K, 128), static_cast<const uint4*>(v16), amax, reinterpret_cast<uint2*>(q), scale);
+      total, chunks, ceil_div(K, 128), static_cast<const uint4*>(v16), static_cast<const uint2*>(v8), amax, reinterpret_cast<uint2*>(q), scale);
   return hipGetLastError();
 }
 
