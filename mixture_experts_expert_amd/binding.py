@@ -881,14 +881,37 @@ class FP8BlockWeights:
         self.gate, self.up, self.down = stored if stored is not None else (quant(w_gate), quant(w_up), quant(w_down))
 
 
+class I8Weights:
+    """Expert weights in 8-bit whole numbers with a float32 scale per output channel: codes
+    gate/up [E,I,H], down [E,H,I] (int8) and scales [E,I], [E,I], [E,H]. From bf16 weights
+    (moe_quantize_i8_rows, on ``stream``, which the results then belong to), or, with
+    ``stored``, a checkpoint's own (codes, scales) pairs as they are."""
+
+    def __init__(self, w_gate=None, w_up=None, w_down=None, stream=None, stored=None):
+        def quant(w):
+            if w.dtype != torch.bfloat16 or w.device.type != "cuda" or not w.is_contiguous():
+                raise ValueError("weights have to be bf16, contiguous, on the GPU")
+            E, N, K = w.shape
+            with torch.cuda.device(w.device), torch.cuda.stream(stream):  # the results' memory is that stream's
+                q = torch.empty(E, N, K, dtype=torch.int8, device=w.device)
+                scale = torch.empty(E, N, dtype=torch.float32, device=w.device)
+                moe_quantize_i8_rows(E * N, K, w, q, scale)
+            if stream is not None:
+                w.record_stream(stream)
+            return q, scale
+
+        self.gate, self.up, self.down = stored if stored is not None else (quant(w_gate), quant(w_up), quant(w_down))
+
+
 class ServingStage:
     """Buffers and call choice of one MoE layer's inference forward.
 
-    ``weights``: (w_gate, w_up, w_down) in bf16, or FP8BlockWeights. Holds the
+    ``weights``: (w_gate, w_up, w_down) in bf16, FP8BlockWeights or I8Weights. Holds the
     buffers for up to ``max_T`` tokens on the weights' device. ``forward(x)``
-    runs the few-token layer (moe_forward_few, moe_forward_few_fp8_block) for
-    batches it takes (at most 64 tokens, k <= 16), and moe_forward_fused or
-    moe_forward_fused_fp8_block for the others; it returns y [T,H], a view of
+    runs the few-token layer (moe_forward_few, moe_forward_few_fp8_block,
+    moe_forward_few_i8) for batches it takes (at most 64 tokens, k <= 16), and
+    moe_forward_fused, moe_forward_fused_fp8_block or moe_forward_fused_i8 for
+    the others; it returns y [T,H], a view of
     a held buffer (overwritten by the next call), and leaves topk_idx and
     topk_w in ``buf``. Calls of one stage share its workspaces: enqueue them
     on one stream, or order the streams. They run on the weights' device,
@@ -899,25 +922,29 @@ class ServingStage:
 
     def __init__(self, max_T: int, k: int, w_router, weights, logit_bias=None):
         self.w_router, self.logit_bias, self.k, self.max_T = w_router, logit_bias, k, max_T
-        self.block = isinstance(weights, FP8BlockWeights)
-        self.w = (*weights.gate, *weights.up, *weights.down) if self.block else tuple(weights)
+        self.block, self.i8 = isinstance(weights, FP8BlockWeights), isinstance(weights, I8Weights)
+        coded = self.block or self.i8
+        self.w = (*weights.gate, *weights.up, *weights.down) if coded else tuple(weights)
         self.E, self.I, self.H = self.w[0].shape
         E, I, H, T, M, dev = self.E, self.I, self.H, max_T, max_T * k, self.w[0].device
         want = [(E, I, H), (E, I, H), (E, H, I)]
         if self.block:
             want = [d for E, N, K in want for d in ((E, N, K), (E, -(-N // 128), -(-K // 128)))]
+        if self.i8:
+            want = [d for E, N, K in want for d in ((E, N, K), (E, N))]
         if [tuple(w.shape) for w in self.w] != want or tuple(w_router.shape) != (E, H):
             raise ValueError(f"weights have to be {want}, the router's {(E, H)}")
         if any(w.device != dev for w in (*self.w, w_router) + (() if logit_bias is None else (logit_bias,))):
             raise ValueError(f"weights, scales, router and bias have to be on one device, {dev}")
         if not all(w.is_contiguous() for w in (*self.w, w_router)):
             raise ValueError("weights have to be contiguous")
-        bf = (w_router,) if self.block else (*self.w, w_router)
-        f32 = (self.w[1::2] if self.block else ()) + (() if logit_bias is None else (logit_bias,))
+        bf = (w_router,) if coded else (*self.w, w_router)
+        f32 = (self.w[1::2] if coded else ()) + (() if logit_bias is None else (logit_bias,))
+        codes = (torch.int8,) if self.i8 else (torch.uint8, torch.float8_e4m3fn)
         if any(w.dtype != torch.bfloat16 for w in bf) or any(w.dtype != torch.float32 for w in f32) or (
-                self.block and any(w.dtype not in (torch.uint8, torch.float8_e4m3fn) for w in self.w[::2])):
-            raise ValueError("bf16 weights, or E4M3 codes (uint8, float8_e4m3fn) with float32 scales; a bf16 router, "
-                             "a float32 bias")
+                coded and any(w.dtype not in codes for w in self.w[::2])):
+            raise ValueError("bf16 weights, or E4M3 codes (uint8, float8_e4m3fn) or int8 ones with float32 scales; a bf16 "
+                             "router, a float32 bias")
         if logit_bias is not None and (tuple(logit_bias.shape) != (E,) or not logit_bias.is_contiguous()):
             raise ValueError(f"logit_bias has to be ({E},), contiguous")
         i32, u8, bf16 = torch.int32, torch.uint8, torch.bfloat16
@@ -929,7 +956,7 @@ class ServingStage:
         self.few_ws = e(few, dt=u8) if few else None
         if self.few_T < T:
             s = shape(T, H, E, k, I, bf16)
-            ws = fp8_block_workspace_bytes(s) if self.block else moe_workspace_bytes(s)
+            ws = fp8_block_workspace_bytes(s) if self.block else (moe_i8_workspace_bytes if self.i8 else moe_workspace_bytes)(s)
             if ws <= 0 or (self.block and moe_few_workspace_bytes(shape(1, H, E, min(k, 16), I, bf16)) == 0):
                 raise MoEError("ServingStage", 2, "shape rejected")
             self.ws = e(ws, dt=u8)
@@ -938,6 +965,9 @@ class ServingStage:
             if self.block:
                 self.buf.update({"xq": e(T, H, dt=u8), "x_scale": e(T, -(-H // 128)), "aq": e(M, I, dt=u8),
                                  "a_scale": e(M, -(-I // 128))})
+            elif self.i8:
+                self.buf.update({"xq": e(T, H, dt=torch.int8), "x_scale": e(T), "aq": e(M, I, dt=torch.int8),
+                                 "a_scale": e(M)})
             else:
                 self.buf["a"] = e(M, I, dt=bf16)
             self.buf["o_perm"] = e(M, H, dt=bf16)
@@ -959,11 +989,11 @@ class ServingStage:
             x.record_stream(stream)  # the caller may drop it
         with torch.cuda.device(x.device):
             if T <= self.few_T:
-                fn = moe_forward_few_fp8_block if self.block else moe_forward_few
+                fn = moe_forward_few_i8 if self.i8 else moe_forward_few_fp8_block if self.block else moe_forward_few
                 fn(s, x, self.w_router, self.logit_bias, *self.w, b["logits"], b["topk_idx"], b["topk_w"], y, self.few_ws,
                    stream=stream)
             else:
-                fn = moe_forward_fused_fp8_block if self.block else moe_forward_fused
+                fn = moe_forward_fused_i8 if self.i8 else moe_forward_fused_fp8_block if self.block else moe_forward_fused
                 fn(s, x, self.w_router, self.logit_bias, *self.w, *[t for n, t in b.items() if n != "y"], y, self.ws,
                    stream=stream)
         return y

@@ -264,3 +264,61 @@ def test_few_tokens_that_are_not_finite_stay_apart():
     keep = torch.ones(40, dtype=torch.bool)
     keep[[7, 20]] = False
     assert y[7].isnan().all() and not y[20].isfinite().any() and torch.equal(y[keep], good[keep])
+
+
+# ---- ServingStage: quantised weights, both paths, streams, graphs ------------------
+
+
+def _serving(E=8, I=192, H=256, k=3, seed=2):
+    g = gen(seed)
+    w = [(torch.randn(E, N, K, generator=g) * K**-0.5).to(BF).cuda() for N, K in ((I, H), (I, H), (H, I))]
+    wr, bias = (0.2 * torch.randn(E, H, generator=g)).to(BF), 0.1 * torch.randn(E, generator=g)
+    return w, wr, bias, B.ServingStage(300, k, wr.cuda(), B.I8Weights(*w), bias.cuda())
+
+
+def test_stage_both_paths():
+    w, wr, bias, stage = _serving()
+    deq = [Q.weight_values(*(t.cpu() for t in m)) for m in (stage.w[0:2], stage.w[2:4], stage.w[4:6])]
+    for n, m in enumerate(w):  # the weights themselves: half a step amax / 127, and 127 times the scale's own rounding of 2^-24
+        amax = m.cpu().double().abs().amax(2, keepdim=True)
+        off = (deq[n] - m.cpu().double()).abs() - amax * (1 / 254 + 2.0**-23)
+        assert off.max() <= 0, off.max()
+    for T in (1, 64, 65, 300):
+        x = torch.randn(T, 256, generator=gen(T)).to(BF)
+        y = stage.forward(x.cuda()).cpu().double()
+        idx, tw = stage.buf["topk_idx"].view(-1)[:T * 3].view(T, 3).cpu(), stage.buf["topk_w"].view(-1)[:T * 3].view(T, 3).cpu()
+        if T <= 64:
+            _, _, _, want, size = S.few(x, wr, bias, 3, *deq, idx=idx.long())
+            assert (y - want).abs().le(U * want.abs() + (U + 2.0**-18) * size).all()
+        else:
+            stored = [tuple(t.cpu() for t in m) for m in (stage.w[0:2], stage.w[2:4], stage.w[4:6])]
+            want, slack, size = Q.experts(x, idx, tw, *stored, near=0.01)
+            assert (y - want).abs().le(U * want.abs() + (U + 2.0**-20) * size + slack).all()
+    assert stage.forward(torch.empty(0, 256, dtype=BF, device="cuda")).shape == (0, 256)
+
+
+def test_stage_on_another_stream_and_in_a_graph():
+    _, _, _, stage = _serving()
+    for T in (40, 200):
+        xs = [torch.randn(T, 256, generator=gen(T + i)).to(BF).cuda() for i in range(3)]
+        want = [stage.forward(x).clone() for x in xs]
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        for x, y in zip(xs, want):
+            got = stage.forward(x, stream=side)
+            side.synchronize()
+            assert torch.equal(got, y)
+        x = xs[0].clone()
+        with torch.cuda.stream(side):
+            stage.forward(x)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            y = stage.forward(x)
+        for i in (1, 2, 0, 1):
+            x.copy_(xs[i])
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, want[i])
+            stage.forward(xs[(i + 1) % 3])  # eager work between replays, in the same buffers
+            torch.cuda.synchronize()

@@ -106,3 +106,34 @@ def test_definition():
     assert q.tolist() == [[127, 0, 2, -127], [0, 0, 0, 0]] and s.tolist() == [[2.0], [0.0]]  # halves to even
     q, s = Q.codes(torch.tensor([[1.0] * 64 + [0.5, float("inf")]]), 64)
     assert q[0, :64].eq(127).all() and q[0, 64:].eq(0).all() and s[0, 1].isnan()
+
+
+# ---- ServingStage on I8Weights ---------------------------------------------------
+
+E, I, H, K = 4, 64, 128, 2
+
+
+def _z(*d, dt=torch.bfloat16, dev="cpu"):
+    return torch.zeros(*d, dtype=dt, device=dev)
+
+
+def _stored(dt=torch.int8, dev="cpu", scale=torch.float32):
+    f = lambda *d: _z(*d, dt=scale, dev=dev)
+    return [(_z(E, I, H, dt=dt, dev=dev), f(E, I)), (_z(E, I, H, dt=dt, dev=dev), f(E, I)), (_z(E, H, I, dt=dt, dev=dev), f(E, H))]
+
+
+def test_stage_refusals(B):
+    good = _stored()
+    for max_T in (8, 200):
+        B.ServingStage(max_T, K, _z(E, H), B.I8Weights(stored=good))
+    bad = [_stored(torch.uint8), _stored(torch.float8_e4m3fn), _stored(scale=torch.float64), _stored()[:2] + _stored(dev="meta")[2:],
+           good[:2] + [(good[2][0], _z(E, I, dt=torch.float32))],                         # one scale per row of [E,H,I]
+           good[:2] + [(good[2][0], _z(E, 1, 1, dt=torch.float32))],                      # block scales
+           good[:2] + [(_z(E, I, H, dt=torch.int8).transpose(1, 2), good[2][1])]]
+    for stored in bad:
+        with pytest.raises(ValueError):
+            B.ServingStage(200, K, _z(E, H), B.I8Weights(stored=stored))
+    with pytest.raises(ValueError):
+        B.I8Weights(_z(E, I, H), _z(E, I, H), _z(E, H, I))  # host tensors
+    with pytest.raises(ValueError):
+        B.ServingStage(8, K, _z(E, H), B.I8Weights(stored=good)).forward(_z(3, H))
