@@ -1,5 +1,5 @@
 """Python binding of libmoe's C ABI (include/moe.h, include/moe_serve.h,
-include/moe_i8.h), by ctypes.
+include/moe_i8.h, include/moe_ckpt8.h), by ctypes.
 
 Argument marshalling only: every function here has the name of a C entry
 point, checks nothing the library does not check itself, passes torch CUDA
@@ -115,6 +115,12 @@ _SIGS = {
     "moe_gemm_gate_up_i8": ([moe_shape] + [_P] * 11 + [ctypes.c_size_t, _P], ctypes.c_int),
     "moe_experts_i8": ([moe_shape] + [_P] * 22 + [ctypes.c_size_t, _P], ctypes.c_int),
     "moe_forward_fused_i8": ([moe_shape] + [_P] * 25 + [ctypes.c_size_t, _P], ctypes.c_int),
+    "moe_quantize_ckpt8": ([ctypes.c_int32, ctypes.c_int32] + [_P] * 4, ctypes.c_int),
+    "moe_dequantize_ckpt8": ([ctypes.c_int32, ctypes.c_int32] + [_P] * 4, ctypes.c_int),
+    "moe_gemm_gate_up_ckpt8": ([moe_shape] + [_P] * 11, ctypes.c_int),
+    "moe_ckpt8_workspace_bytes": ([moe_shape], ctypes.c_size_t),
+    "moe_gemm_down_dgrad_ckpt8": ([moe_shape] + [_P] * 14 + [ctypes.c_size_t, _P], ctypes.c_int),
+    "moe_gemm_down_wgrad_dy": ([moe_shape] + [_P] * 5 + [ctypes.c_int, _P, ctypes.c_size_t, _P], ctypes.c_int),
     "moe_few_workspace_bytes": ([moe_shape], ctypes.c_size_t),
     "moe_forward_few": ([moe_shape] + [_P] * 11 + [ctypes.c_size_t, _P], ctypes.c_int),
     "moe_forward_few_fp8_block": ([moe_shape] + [_P] * 14 + [ctypes.c_size_t, _P], ctypes.c_int),
@@ -570,6 +576,39 @@ def moe_gemm_down_dgrad_dy(s, dy, row_token, row_weight, offsets, w_down, g, u, 
     _check("moe_gemm_down_dgrad_dy", lib.moe_gemm_down_dgrad_dy(
         s, _ptr(dy), _ptr(row_token), _ptr(row_weight), _ptr(offsets), _ptr(w_down), _ptr(g), _ptr(u), _ptr(dgu),
         _stream(stream)))
+
+
+def moe_quantize_ckpt8(rows, K, x, q, scale, stream=None):
+    _check("moe_quantize_ckpt8", lib.moe_quantize_ckpt8(int(rows), int(K), _ptr(x), _ptr(q), _ptr(scale),
+                                                        _stream(stream)))
+
+
+def moe_dequantize_ckpt8(rows, K, q, scale, out, stream=None):
+    _check("moe_dequantize_ckpt8", lib.moe_dequantize_ckpt8(int(rows), int(K), _ptr(q), _ptr(scale), _ptr(out),
+                                                            _stream(stream)))
+
+
+def moe_gemm_gate_up_ckpt8(s, x_rows, row_token, offsets, w_gate, w_up, gq, g_scale, uq, u_scale, a, stream=None):
+    """row_token None: x_rows is x_perm; else x [T,H] read through row_token."""
+    args = (x_rows, row_token, offsets, w_gate, w_up, gq, g_scale, uq, u_scale, a)
+    _check("moe_gemm_gate_up_ckpt8", lib.moe_gemm_gate_up_ckpt8(s, *[_ptr(t) for t in args], _stream(stream)))
+
+
+def moe_ckpt8_workspace_bytes(s: moe_shape) -> int:
+    return int(lib.moe_ckpt8_workspace_bytes(s))
+
+
+def moe_gemm_down_dgrad_ckpt8(s, dy, row_token, row_weight, sorted_to_flat, offsets, w_down, gq, g_scale, uq, u_scale, dgu,
+                              a_w, d_topk_w, ws, ws_bytes=None, stream=None):
+    args = (dy, row_token, row_weight, sorted_to_flat, offsets, w_down, gq, g_scale, uq, u_scale, dgu, a_w, d_topk_w, ws)
+    _check("moe_gemm_down_dgrad_ckpt8", lib.moe_gemm_down_dgrad_ckpt8(
+        s, *[_ptr(t) for t in args], _nbytes(ws, ws_bytes), _stream(stream)))
+
+
+def moe_gemm_down_wgrad_dy(s, dy, row_token, a_w, offsets, dw_down, accumulate_dw, ws, ws_bytes=None, stream=None):
+    _check("moe_gemm_down_wgrad_dy", lib.moe_gemm_down_wgrad_dy(
+        s, _ptr(dy), _ptr(row_token), _ptr(a_w), _ptr(offsets), _ptr(dw_down), int(accumulate_dw), _ptr(ws),
+        _nbytes(ws, ws_bytes), _stream(stream)))
 
 
 class MoEStage:

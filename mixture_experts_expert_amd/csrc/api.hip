@@ -30,6 +30,12 @@ bool any_null(P... p) {
   return ((p == nullptr) || ...);
 }
 
+// The kernels move 16 bytes at a time.
+template <class... P>
+bool misaligned(P... p) {
+  return (((reinterpret_cast<uintptr_t>(p) & 15) != 0) || ...);
+}
+
 moe_status from_hip(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_EHIP; }
 
 // x read through row tokens is addressed with 32-bit byte offsets.
@@ -538,6 +544,119 @@ moe_status moe_gemm_down_bwd_dy(moe_shape s, const void* dy, const int32_t* row_
   gw.dw0 = dw_down;
   gw.accumulate = accumulate_dw;
   return from_hip(moe::launch_gemm_pair(moe::GEMM_DGRAD_DOWN, moe::GEMM_WGRAD_DOWN, s, gd, gw, stream));
+}
+
+// ---- activations kept in 8 bits (moe_ckpt8.h)
+
+namespace {
+constexpr int64_t k2G = static_cast<int64_t>(1) << 31;
+
+moe_status check_ckpt8_rows(int32_t rows, int32_t K) {
+  if (rows < 0 || K <= 0 || K % 8 != 0) return MOE_EINVAL;
+  // 8 threads per block of 64 columns, in workgroups of 256
+  if (rows * moe::ceil_div64(K, moe::kCkptBlock) >= (static_cast<int64_t>(1) << 29) - 32) return MOE_EUNSUPPORTED;
+  return MOE_OK;
+}
+
+size_t ckpt8_dots_bytes(const moe_shape& s) {
+  return static_cast<size_t>(s.T) * s.k * moe::ceil_div(s.I, 128) * sizeof(float);
+}
+
+moe_status check_ckpt8_shape(const moe_shape& s) {
+  const moe_status st = check_shape(s);
+  if (st != MOE_OK) return st;
+  return s.dtype != MOE_BF16 || !gathered_x_fits(s) ? MOE_EUNSUPPORTED : MOE_OK;
+}
+}  // namespace
+
+moe_status moe_quantize_ckpt8(int32_t rows, int32_t K, const void* in, int8_t* q, float* scale, hipStream_t stream) {
+  const moe_status st = check_ckpt8_rows(rows, K);
+  if (st != MOE_OK || rows == 0) return st;
+  if (any_null(in, q, scale) || misaligned(in, q)) return MOE_EINVAL;
+  return from_hip(moe::launch_quantize_ckpt8(rows, K, in, q, scale, stream));
+}
+
+moe_status moe_dequantize_ckpt8(int32_t rows, int32_t K, const int8_t* q, const float* scale, void* out,
+                                hipStream_t stream) {
+  const moe_status st = check_ckpt8_rows(rows, K);
+  if (st != MOE_OK || rows == 0) return st;
+  if (any_null(q, scale, out) || misaligned(q, out)) return MOE_EINVAL;
+  return from_hip(moe::launch_dequantize_ckpt8(rows, K, q, scale, out, stream));
+}
+
+moe_status moe_gemm_gate_up_ckpt8(moe_shape s, const void* x_rows, const int32_t* row_token, const int32_t* offsets,
+                                  const void* w_gate, const void* w_up, int8_t* gq, float* g_scale, int8_t* uq,
+                                  float* u_scale, void* a, hipStream_t stream) {
+  moe_status st = check_shape(s);
+  if (st != MOE_OK) return st;
+  if (any_null(x_rows, offsets, w_gate, w_up, gq, g_scale, uq, u_scale, a)) return MOE_EINVAL;
+  if (misaligned(x_rows, w_gate, w_up, gq, uq, a)) return MOE_EINVAL;
+  if (s.dtype != MOE_BF16 || (row_token != nullptr && !gathered_x_fits(s))) return MOE_EUNSUPPORTED;
+  moe::GemmArgs g{};
+  g.offsets = offsets;
+  g.a = x_rows;
+  g.row_token = row_token;
+  g.b0 = w_gate;
+  g.b1 = w_up;
+  g.gq = gq;
+  g.gs = g_scale;
+  g.uq = uq;
+  g.us = u_scale;
+  g.out2 = a;
+  return from_hip(moe::launch_gemm(moe::GEMM_GATEUP, s, g, stream));
+}
+
+size_t moe_ckpt8_workspace_bytes(moe_shape s) { return check_ckpt8_shape(s) != MOE_OK ? 0 : ckpt8_dots_bytes(s); }
+
+moe_status moe_gemm_down_dgrad_ckpt8(moe_shape s, const void* dy, const int32_t* row_token, const float* row_weight,
+                                     const int32_t* sorted_to_flat, const int32_t* offsets, const void* w_down,
+                                     const int8_t* gq, const float* g_scale, const int8_t* uq, const float* u_scale,
+                                     void* dgu, void* a_w, float* d_topk_w, void* ws, size_t ws_bytes,
+                                     hipStream_t stream) {
+  moe_status st = check_ckpt8_shape(s);
+  if (st != MOE_OK) return st;
+  if (any_null(dy, row_token, row_weight, sorted_to_flat, offsets, w_down, gq, g_scale, uq, u_scale, dgu, a_w, d_topk_w,
+               ws))
+    return MOE_EINVAL;
+  if (misaligned(dy, w_down, gq, uq, dgu, a_w, ws)) return MOE_EINVAL;
+  if (ws_bytes < ckpt8_dots_bytes(s)) return MOE_EWORKSPACE;
+  moe::GemmArgs g{};
+  g.offsets = offsets;
+  g.a = dy;
+  g.row_token = row_token;
+  g.row_weight = row_weight;
+  g.b0 = w_down;
+  g.gq = const_cast<int8_t*>(gq);
+  g.gs = const_cast<float*>(g_scale);
+  g.uq = const_cast<int8_t*>(uq);
+  g.us = const_cast<float*>(u_scale);
+  g.out0 = dgu;
+  g.out1 = a_w;
+  g.dot = static_cast<float*>(ws);
+  if ((st = from_hip(moe::launch_gemm(moe::GEMM_DGRAD_DOWN, s, g, stream))) != MOE_OK) return st;
+  return from_hip(moe::launch_ckpt8_dots(s.T * s.k, moe::ceil_div(s.I, 128), g.dot, sorted_to_flat, d_topk_w, stream));
+}
+
+moe_status moe_gemm_down_wgrad_dy(moe_shape s, const void* dy, const int32_t* row_token, const void* a_w,
+                                  const int32_t* offsets, float* dw_down, int accumulate_dw, void* ws, size_t ws_bytes,
+                                  hipStream_t stream) {
+  const moe_status st = check_ckpt8_shape(s);
+  if (st != MOE_OK) return st;
+  if (any_null(dy, row_token, a_w, offsets, dw_down, ws)) return MOE_EINVAL;
+  if (misaligned(dy, a_w, dw_down, ws)) return MOE_EINVAL;
+  if (accumulate_dw != 0 && accumulate_dw != 1) return MOE_EINVAL;
+  if (4 * (static_cast<int64_t>(s.T) * s.k + 256) >= k2G) return MOE_EUNSUPPORTED;
+  const WsLayout l = moe::ws_layout(s);
+  if (ws_bytes < l.total) return MOE_EWORKSPACE;
+  moe::GemmArgs g{};
+  g.part = reinterpret_cast<float*>(static_cast<char*>(ws) + l.part_off);
+  g.offsets = offsets;
+  g.a = dy;
+  g.row_token = row_token;
+  g.b0 = a_w;
+  g.dw0 = dw_down;
+  g.accumulate = accumulate_dw;
+  return from_hip(moe::launch_gemm(moe::GEMM_WGRAD_DOWN, s, g, stream));
 }
 
 moe_status moe_grouped_gemm_bwd(moe_shape s, const void* do_perm, const void* x_perm, const void* g, const void* u,

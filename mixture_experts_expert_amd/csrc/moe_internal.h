@@ -8,6 +8,7 @@
 #include "moe.h"
 #include "moe_serve.h"
 #include "moe_i8.h"
+#include "moe_ckpt8.h"
 
 namespace moe {
 
@@ -171,6 +172,14 @@ struct GemmArgs {
   const void* bx0;
   const void* bx1;
   int kx, kxr, kxp;
+  // G and U in 8 bits (gq set; bf16 GATEUP, and DGRAD_DOWN with row_token):
+  // codes [T*k][I] and a scale per kCkptBlock columns, written by GATEUP in the
+  // place of out0 and out1, read by DGRAD_DOWN in that of g_in and u_in.
+  // DGRAD_DOWN then also writes a_w (out1) and dot [T*k][ceil(I/128)]: each
+  // row's <dA, a> over 128 columns, before its weight.
+  int8_t *gq, *uq;
+  float *gs, *us;
+  float* dot;
 };
 
 hipError_t launch_gemm_bf16(GemmMode mode, const moe_shape& s, const GemmArgs& a, hipStream_t st);
@@ -316,6 +325,8 @@ struct I8GemmArgs {
   float* amax;
 };
 hipError_t launch_gemm_i8(const I8GemmArgs& a, hipStream_t st);
+// out[sorted_to_flat[p]] = the sum of dot [M][n]'s row p (gemm_bf16.hip).
+hipError_t launch_ckpt8_dots(int M, int n, const float* dot, const int32_t* sorted_to_flat, float* out, hipStream_t st);
 
 // The whole layer for a few tokens (few.hip).
 constexpr int kFewMaxT = 64, kFewMaxK = 16;
