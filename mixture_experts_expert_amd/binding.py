@@ -10,7 +10,8 @@ machine without the built library raises ImportError.
 
 ``MoEStage`` chains the calls of one forward and one backward pass, holding
 the buffers (torch is used for device memory only); ``ServingStage`` holds
-those of the inference forward and picks the call for a batch's size.
+those of the inference forward and picks the call for a batch's size. ``Ckpt8Stage``
+is the training step with its activations kept in 8 bits.
 """
 from __future__ import annotations
 
@@ -781,7 +782,116 @@ class MoEStage:
         return b["dx"]
 
 
-# ---- Serving (include/moe_serve.h) -------------------------------------------
+class Ckpt8Stage:
+    """The training step of one layer's expert stage (bf16) that keeps its activations
+    in 8 bits (include/moe_ckpt8.h): the calls of ``MoEStage``, with neither x_perm nor do_perm.
+
+    Between forward and backward it holds the routing, the sort and the codes of g
+    and u; ``x8`` also keeps x as codes (otherwise the caller's x, which then has to
+    stay as it is until the backward). ``kept_bytes()`` counts them. y is the
+    same, bit for bit, as MoEStage(gather_fused=True, dy_fused=True)'s; the
+    gradients are those at the kept values.
+
+    ``scratch``: a dict for what lives within one call (a, o_perm, dgu, a_w, dx_perm,
+    the restored x, the workspace). Stages of the same sizes on one device that are
+    given the same dict share it; their calls then have to be on one stream, or
+    ordered. ``forward`` and ``backward`` return views of held buffers (y and dx,
+    overwritten by the stage's next call).
+    """
+
+    def __init__(self, T: int, H: int, E: int, k: int, I: int, device="cuda", x8: bool = False,
+                 scratch: Optional[Dict[str, torch.Tensor]] = None):
+        self.T, self.H, self.E, self.k, self.I, self.x8 = T, H, E, k, I, x8
+        self.s = shape(T, H, E, k, I, torch.bfloat16)
+        ws_bytes = moe_workspace_bytes(self.s)
+        if ws_bytes == 0 or moe_ckpt8_workspace_bytes(self.s) == 0:
+            raise MoEError("Ckpt8Stage", 2, "shape rejected")
+        M, dev = T * k, torch.device(device)
+        f32, i32, i8, bf16 = torch.float32, torch.int32, torch.int8, torch.bfloat16
+        e = lambda *sz, dt=f32: torch.empty(*sz, dtype=dt, device=dev)  # noqa: E731
+        self.kept: Dict[str, torch.Tensor] = {
+            "topk_idx": e(T, k, dt=i32), "topk_w": e(T, k), "offsets": e(E + 1, dt=i32), "sorted_to_flat": e(M, dt=i32),
+            "flat_to_sorted": e(M, dt=i32), "row_token": e(M, dt=i32), "row_weight": e(M),
+            "gq": e(M, I, dt=i8), "g_scale": e(M, I // 64), "uq": e(M, I, dt=i8), "u_scale": e(M, I // 64)}
+        if x8:
+            self.kept.update({"xq": e(T, H, dt=i8), "x_scale": e(T, H // 64)})
+        self.buf: Dict[str, torch.Tensor] = {**self.kept, "logits": e(T, E), "counts": e(E, dt=i32), "y": e(T, H, dt=bf16)}
+        self.scratch = {} if scratch is None else scratch
+        sizes = {"a": (M, I), "o_perm": (M, H), "dgu": (M, 2 * I), "a_w": (M, I), "dx_perm": (M, H)}
+        if x8:
+            sizes["x"] = (T, H)
+        for n, sz in sizes.items():
+            if n not in self.scratch:
+                self.scratch[n] = e(*sz, dt=bf16)
+            elif tuple(self.scratch[n].shape) != sz or self.scratch[n].device != self.buf["y"].device:
+                raise ValueError(f"scratch {n} is {tuple(self.scratch[n].shape)} on {self.scratch[n].device}: "
+                                 f"stages that share it have the same sizes, here {sz}, and device")
+        if "ws" not in self.scratch:
+            self.scratch["ws"] = e(ws_bytes, dt=torch.uint8)
+        elif self.scratch["ws"].numel() < ws_bytes or self.scratch["ws"].device != self.buf["y"].device:
+            raise ValueError("scratch ws is of another shape's size or on another device")
+        self.x = None
+
+    def kept_bytes(self) -> int:
+        """Bytes held between forward and backward (x itself not among them)."""
+        return sum(t.numel() * t.element_size() for t in self.kept.values())
+
+    def _activations(self, t, name):
+        if tuple(t.shape) != (self.T, self.H) or t.dtype != torch.bfloat16 or not t.is_contiguous():
+            raise ValueError(f"{name} has to be [{self.T}, {self.H}] in bf16, contiguous")
+        if t.device != self.buf["y"].device or t.device.type != "cuda":
+            raise ValueError(f"{name} is on {t.device}, the stage on {self.buf['y'].device}; both have to be on one GPU")
+
+    def forward(self, x, w_router, w_gate, w_up, w_down, logit_bias=None, stream=None):
+        self._activations(x, "x")
+        b, c, s = self.buf, self.scratch, self.s
+        with torch.cuda.device(x.device):
+            moe_route(s, x, w_router, logit_bias, b["logits"], b["topk_idx"], b["topk_w"], stream)
+            moe_permute_fused(s, b["topk_idx"], b["topk_w"], b["counts"], b["offsets"], b["sorted_to_flat"],
+                              b["flat_to_sorted"], b["row_token"], b["row_weight"], c["ws"], stream=stream)
+            moe_gemm_gate_up_ckpt8(s, x, b["row_token"], b["offsets"], w_gate, w_up, b["gq"], b["g_scale"], b["uq"],
+                                   b["u_scale"], c["a"], stream)
+            moe_gemm_down(s, c["a"], b["offsets"], w_down, c["o_perm"], stream)
+            moe_combine(s, c["o_perm"], b["topk_w"], b["flat_to_sorted"], b["y"], stream)
+            if self.x8:
+                moe_quantize_ckpt8(self.T, self.H, x, b["xq"], b["x_scale"], stream)
+        if self.x8 and stream is not None:
+            x.record_stream(stream)  # the caller may drop it
+        self.x, self.w = (None if self.x8 else x), (w_gate, w_up, w_down)
+        return b["y"]
+
+    def backward(self, dy, accumulate_dw: bool = False, stream=None):
+        """Of the last forward: returns dx; dw_gate, dw_up, dw_down (float32, added to with
+        ``accumulate_dw``), d_topk_w and d_logits are in ``buf``."""
+        self._activations(dy, "dy")
+        if not hasattr(self, "w"):
+            raise ValueError("backward before forward")
+        b, c, s, acc = self.buf, self.scratch, self.s, int(accumulate_dw)
+        w_gate, w_up, w_down = self.w
+        if "dx" not in b:
+            if acc:
+                raise ValueError("accumulate_dw before a first backward: there is nothing to add to")
+            z = lambda *sz, dt=torch.float32: torch.empty(*sz, dtype=dt, device=dy.device)  # noqa: E731
+            T, H, E, k, I = self.T, self.H, self.E, self.k, self.I
+            b.update({"dx": z(T, H, dt=torch.bfloat16), "d_topk_w": z(T, k), "d_logits": z(T, E), "dw_gate": z(E, I, H),
+                      "dw_up": z(E, I, H), "dw_down": z(E, H, I)})
+        with torch.cuda.device(dy.device):
+            moe_gemm_down_dgrad_ckpt8(s, dy, b["row_token"], b["row_weight"], b["sorted_to_flat"], b["offsets"], w_down,
+                                      b["gq"], b["g_scale"], b["uq"], b["u_scale"], c["dgu"], c["a_w"], b["d_topk_w"],
+                                      c["ws"], stream=stream)
+            moe_gemm_down_wgrad_dy(s, dy, b["row_token"], c["a_w"], b["offsets"], b["dw_down"], acc, c["ws"], stream=stream)
+            x = self.x
+            if self.x8:
+                x = c["x"]
+                moe_dequantize_ckpt8(self.T, self.H, b["xq"], b["x_scale"], x, stream)
+            moe_gemm_gate_up_bwd(s, c["dgu"], x, b["row_token"], b["offsets"], w_gate, w_up, c["dx_perm"], b["dw_gate"],
+                                 b["dw_up"], acc, c["ws"], stream=stream)
+            moe_unpermute_sum(s, c["dx_perm"], b["flat_to_sorted"], b["dx"], stream)
+            moe_route_bwd(s, b["d_topk_w"], b["topk_w"], b["topk_idx"], b["d_logits"], stream)
+        return b["dx"]
+
+
+# ---- Serving (include/moe_serve.h, include/moe_i8.h) -------------------------
 
 
 def moe_quantize_fp8_block_rows(rows, K, x, q, scale, stream=None):

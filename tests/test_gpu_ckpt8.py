@@ -144,3 +144,138 @@ def test_down_dgrad(T, H, E, k, I, skew, empty):
     mag = (dA * (gv * sg * uv).abs()).sum(1)
     got = dt[:T].cpu().double().reshape(-1)[order.long()]
     assert (got - want_dot).abs().le(mag * (H + I + 20) * f + 1e-30).all()
+
+
+# ---- the training step -------------------------------------------------------------
+
+
+def layer(T, H, E, k, I, seed, zipf=0.0):
+    g = gen(seed)
+    x, dy = torch.randn(T, H, generator=g).to(BF), torch.randn(T, H, generator=g).to(BF)
+    wr = (0.1 * torch.randn(E, H, generator=g)).to(BF)
+    w = [(torch.randn(E, N, K, generator=g) * K**-0.5).to(BF) for N, K in ((I, H), (I, H), (H, I))]
+    bias = (-zipf * torch.log(torch.arange(1, E + 1).float()))
+    return x, dy, wr, w, bias
+
+
+def reference(b, x, dy, w, gv, uv):
+    """Gradients in 64 bits at the kept values gv, uv (and x), for the stage's own routing."""
+    T, H = x.shape
+    tok, off, rw = b["row_token"].cpu().long(), b["offsets"].cpu(), b["row_weight"].cpu()
+    order, idx, tw = b["sorted_to_flat"].cpu().long(), b["topk_idx"].cpu().long(), b["topk_w"].cpu().double()
+    E, I, _ = w[0].shape
+    dgu, a_w, dot = Q.down_backward(dy, tok, rw, off, w[2], gv, uv)
+    out = {"dx": torch.zeros(T, H, dtype=torch.float64)}
+    dw = [torch.zeros(m.shape, dtype=torch.float64) for m in w]
+    for e in range(E):
+        r = slice(int(off[e]), int(off[e + 1]))
+        xe, dye, dg, du = x[tok[r]].double(), dy[tok[r]].double(), dgu[r, :I], dgu[r, I:]
+        out["dx"].index_add_(0, tok[r], dg @ w[0][e].double() + du @ w[1][e].double())
+        dw[0][e], dw[1][e], dw[2][e] = dg.T @ xe, du.T @ xe, dye.T @ a_w[r]
+    out.update(dw_gate=dw[0], dw_up=dw[1], dw_down=dw[2])
+    d = torch.zeros(T * idx.shape[1], dtype=torch.float64)
+    d[order] = dot
+    d = d.view_as(tw)
+    out["d_logits"] = torch.zeros(T, E, dtype=torch.float64).scatter_(1, idx, tw * (d - (tw * d).sum(1, keepdim=True)))
+    return out
+
+
+def off_by(got, want):
+    return ((got.cpu().double() - want).norm() / want.norm().clamp(min=1e-30)).item()
+
+
+@pytest.mark.parametrize("x8", [False, True])
+@pytest.mark.parametrize("T,H,E,k,I,zipf", [(1, 64, 2, 1, 64, 0.0), (70, 192, 4, 2, 320, 0.0), (300, 256, 16, 3, 128, 1.2),
+                                            (600, 128, 4, 2, 192, 0.0)])
+def test_training_step(T, H, E, k, I, zipf, x8):
+    x, dy, wr, w, bias = layer(T, H, E, k, I, 21, zipf)
+    xd, dyd, wrd, biasd, *wd = dev(x, dy, wr, bias, *w)
+    st = B.Ckpt8Stage(T, H, E, k, I, x8=x8)
+    plain = B.MoEStage(T, H, E, k, I, BF, gather_fused=True, dy_fused=True)
+    y = st.forward(xd, wrd, *wd, biasd)
+    assert torch.equal(y, plain.forward(xd, wrd, *wd, biasd))
+    given = xd.clone()
+    if x8:
+        xd.zero_()  # the stage has its own
+    dx = st.backward(dyd)
+    b = st.buf
+    kept = Q.values(b["xq"].cpu(), b["x_scale"].cpu()) if x8 and H > 64 else (
+        b["xq"].cpu().double() * b["x_scale"].cpu().double() if x8 else x)
+    kept = kept.to(BF) if x8 else x
+    val = lambda q, s: q.cpu().double() * s.cpu().double().repeat_interleave(64, 1)
+    want = reference(b, kept, dy, w, val(b["gq"], b["g_scale"]), val(b["uq"], b["u_scale"]))
+    got = {"dx": dx, **{n: b[n] for n in ("dw_gate", "dw_up", "dw_down", "d_logits")}}
+    # Rounded to bf16 on the way: dgu, dx_perm and dx (dx); dgu (dw_gate, dw_up); a_w (dw_down). 2^-8 each at most.
+    for n, lim in (("dx", 3 * U), ("dw_gate", U), ("dw_up", U), ("dw_down", U), ("d_logits", 2.0**-14)):
+        assert off_by(got[n], want[n]) <= lim, n
+    # Beside the step without codes: a value of g or u is off by at most half a step, 1/254 of its block's
+    # largest, which for 64 normal values is at most 5 of their deviations: 2% of one deviation, and each
+    # gradient is linear in those errors with factors of at most 1.1 (silu') and 0.5 (silu'') beside values of
+    # about one deviation: within 5%.
+    plain.forward(given, wrd, *wd, biasd)
+    plain.backward(dyd)
+    for n in ("dx", "dw_gate", "dw_up", "dw_down"):
+        assert off_by(got[n], plain.buf[n].cpu().double()) < 0.05, n
+    # Added to, and again the same bits.
+    first = {n: t.clone() for n, t in got.items()}
+    if x8:
+        xd.copy_(given)
+    st.forward(xd, wrd, *wd, biasd)
+    st.backward(dyd, accumulate_dw=True)
+    assert torch.equal(b["dx"], first["dx"]) and torch.equal(b["d_logits"], first["d_logits"])
+    for n in ("dw_gate", "dw_up", "dw_down"):
+        assert off_by(b[n], 2 * first[n].cpu().double()) < 2.0**-20, n
+
+
+def test_stages_that_share_scratch():
+    """Two layers: forward, forward, backward, backward; the first's codes are still its own."""
+    dims = (130, 128, 4, 2, 192)
+    ls = [layer(*dims, seed) for seed in (1, 2)]
+    scratch = {}
+    pair = [B.Ckpt8Stage(*dims, x8=True, scratch=scratch) for _ in ls]
+    alone = [B.Ckpt8Stage(*dims, x8=True) for _ in ls]
+    for st, (x, dy, wr, w, bias) in list(zip(alone, ls)):
+        st.forward(*dev(x, wr, *w, bias))
+        st.backward(dev(dy))
+    for st, (x, dy, wr, w, bias) in zip(pair, ls):
+        st.forward(*dev(x, wr, *w, bias))
+    for st, (x, dy, wr, w, bias) in reversed(list(zip(pair, ls))):
+        st.backward(dev(dy))
+    for a, b in zip(pair, alone):
+        for n in ("y", "dx", "dw_gate", "dw_up", "dw_down", "d_logits"):
+            assert torch.equal(a.buf[n], b.buf[n]), n
+    with pytest.raises(ValueError):
+        B.Ckpt8Stage(131, *dims[1:], scratch=scratch)
+
+
+def test_step_in_a_graph_and_on_another_stream():
+    dims = (200, 128, 4, 2, 192)
+    x, dy, wr, w, bias = layer(*dims, 3)
+    xd, dyd, wrd, biasd, *wd = dev(x, dy, wr, bias, *w)
+    st = B.Ckpt8Stage(*dims, x8=True)
+    names = ("y", "dx", "dw_gate", "dw_up", "dw_down", "d_logits")
+    xs = [xd.clone(), (xd * 0.5).contiguous(), -xd]
+    want = []
+    for v in xs:
+        st.forward(v, wrd, *wd, biasd)
+        st.backward(dyd)
+        want.append({n: st.buf[n].clone() for n in names})
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    st.forward(xs[1], wrd, *wd, biasd, stream=side)
+    st.backward(dyd, stream=side)
+    side.synchronize()
+    assert all(torch.equal(st.buf[n], want[1][n]) for n in names)
+    buf = xs[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        st.forward(buf, wrd, *wd, biasd)
+        st.backward(dyd)
+    for i in (2, 0, 1, 2):
+        buf.copy_(xs[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(st.buf[n], want[i][n]) for n in names), i
+        st.forward(xs[(i + 1) % 3], wrd, *wd, biasd)  # eager work in between
+        torch.cuda.synchronize()
