@@ -414,12 +414,11 @@ moe_status moe_forward_few_i8(moe_shape s, const void* x, const void* w_router, 
   a.gate_scale = w_gate_scale;
   a.up_scale = w_up_scale;
   a.down_scale = w_down_scale;
-  a.i8 = true;
   a.logits = logits;
   a.topk_idx = topk_idx;
   a.topk_w = topk_w;
   a.y = y;
-  return from_hip(moe::launch_few(s, a, ws, stream));
+  return from_hip(moe::launch_few_i8(s, a, ws, stream));
 }
 
 }  // extern "C"

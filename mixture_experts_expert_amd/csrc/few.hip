@@ -1040,6 +1040,13 @@ int few_max_groups(const moe_shape& s) {  // the most over the active counts: gr
   return na <= 64 ? ceil_div(na, 8) : (ceil_div(na, 16) > 8 ? ceil_div(na, 16) : 8);
 }
 
+template <int FMT>
+void launch_format(const FewParams& P, unsigned grid, hipStream_t st) {
+  if (P.E <= 128) launch_layer<FMT, 8>(P, grid, st);
+  else if (P.E <= 256) launch_layer<FMT, 16>(P, grid, st);
+  else launch_layer<FMT, 64>(P, grid, st);
+}
+
 }  // namespace
 
 FewLayout few_layout(const moe_shape& s) {
@@ -1053,7 +1060,8 @@ FewLayout few_layout(const moe_shape& s) {
   return l;
 }
 
-hipError_t launch_few(const moe_shape& s, const FewArgs& a, void* ws, hipStream_t st) {
+namespace {
+hipError_t launch(const moe_shape& s, const FewArgs& a, void* ws, hipStream_t st, int fmt) {
   const FewLayout l = few_layout(s);
   char* base = static_cast<char*>(ws);
   FewParams P{};
@@ -1084,20 +1092,16 @@ hipError_t launch_few(const moe_shape& s, const FewArgs& a, void* ws, hipStream_
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   const unsigned grid = static_cast<unsigned>(gemm_grid());
-  if (a.i8) {
-    if (s.E <= 128) launch_layer<kI8, 8>(P, grid, st);
-    else if (s.E <= 256) launch_layer<kI8, 16>(P, grid, st);
-    else launch_layer<kI8, 64>(P, grid, st);
-  } else if (a.gate_scale != nullptr) {
-    if (s.E <= 128) launch_layer<kFp8, 8>(P, grid, st);
-    else if (s.E <= 256) launch_layer<kFp8, 16>(P, grid, st);
-    else launch_layer<kFp8, 64>(P, grid, st);
-  } else {
-    if (s.E <= 128) launch_layer<kBf16, 8>(P, grid, st);
-    else if (s.E <= 256) launch_layer<kBf16, 16>(P, grid, st);
-    else launch_layer<kBf16, 64>(P, grid, st);
-  }
+  if (fmt == kI8) launch_format<kI8>(P, grid, st);
+  else if (fmt == kFp8) launch_format<kFp8>(P, grid, st);
+  else launch_format<kBf16>(P, grid, st);
   return hipGetLastError();
 }
+}  // namespace
+
+hipError_t launch_few(const moe_shape& s, const FewArgs& a, void* ws, hipStream_t st) {
+  return launch(s, a, ws, st, a.gate_scale != nullptr ? kFp8 : kBf16);
+}
+hipError_t launch_few_i8(const moe_shape& s, const FewArgs& a, void* ws, hipStream_t st) { return launch(s, a, ws, st, kI8); }
 
 }  // namespace moe

@@ -341,7 +341,6 @@ struct FewArgs {
   const float* bias;
   const void *w_gate, *w_up, *w_down;  // bf16, or codes with the scales
   const float *gate_scale, *up_scale, *down_scale;
-  bool i8;                             // the codes are whole numbers with a scale per row, not E4M3 blocks
   float* logits;
   int32_t* topk_idx;
   float* topk_w;
@@ -349,5 +348,7 @@ struct FewArgs {
   uint32_t polls = kFewPolls;  // before a wait inside the kernel gives up
 };
 hipError_t launch_few(const moe_shape& s, const FewArgs& a, void* ws, hipStream_t st);
+// The same on whole numbers with a scale per row.
+hipError_t launch_few_i8(const moe_shape& s, const FewArgs& a, void* ws, hipStream_t st);
 
 }  // namespace moe
