@@ -116,8 +116,6 @@ __device__ __forceinline__ float across_groups(float m) {  // lanes 16, 32 and 4
 constexpr int BN = 256;
 constexpr int kBand = 8;  // row tiles that run side by side over all columns: what an XCD's workgroups read meets in its L2
 
-// GU: N columns of each of w0 and w1 (128 per tile), else N of w0 (256 per tile).
-//
 // A tile's rows come in two halves; a wavefront has half of each. Step s lives
 // in stage s % 2, and its loads leave a step and a half before they are used:
 // the weights and the first half's rows as soon as every wavefront has taken
@@ -126,13 +124,12 @@ constexpr int kBand = 8;  // row tiles that run side by side over all columns: w
 //   .. | W, A0 of s+1 | A1 of s+1 | W, A0 of s+2 | A1 of s+2 | ..
 //         step s-1, 2nd  step s, 1st   step s, 2nd  step s+1, 1st half
 // so at each barrier all but the last two groups have landed.
-template <bool GU, int BM>
 __global__ __launch_bounds__(kThreads, 2) void i8_tile_kernel(const Params P) {
+  constexpr int BM = 256;
   constexpr int FM = BM / 32, HM = FM / 2;  // 16-row tiles of a per wavefront, and of those per half
   constexpr int HA = BM / 128;              // load instructions of half a's rows per wavefront
   constexpr int OS = BM / 2 * KS;
-  constexpr int TN = GU ? BN / 2 : BN;
-  constexpr int G1 = HA, G2 = 4 + HA, STORES = (GU ? 3 : 2) * FM;
+  constexpr int G1 = HA, G2 = 4 + HA, STORES = 2 * FM;
   // A stage, in three arrays, so that the compiler sees which reads follow
   // which loads: the weights' rows, the first and the second half's rows of a.
   __shared__ __attribute__((aligned(1024))) uint8_t w0[BN * KS];
@@ -144,9 +141,8 @@ __global__ __launch_bounds__(kThreads, 2) void i8_tile_kernel(const Params P) {
   __shared__ int tstart[1025];
   __shared__ int eoff[1025];
   __shared__ int wsum[kWaves];
-  __shared__ float amax[GU ? BM : 1][4];
-  __shared__ __attribute__((aligned(256))) int per_row[kThreads];   // GU: the next tile's tokens, else this one's weights
-  __shared__ __attribute__((aligned(256))) float scale[kThreads];   // this tile's scales: 256 rows, 256 columns
+  __shared__ __attribute__((aligned(256))) int per_row[kThreads];   // this tile's row weights
+  __shared__ __attribute__((aligned(256))) float scale[kThreads];   // its scales: 256 rows, 256 columns
 
   const int tid = threadIdx.x;
   const int lane_id = tid & 63;
@@ -182,7 +178,7 @@ __global__ __launch_bounds__(kThreads, 2) void i8_tile_kernel(const Params P) {
     if (tid == kThreads - 1) tstart[E] = at + mine;
     __syncthreads();
   }
-  const int ntn = (P.N + TN - 1) / TN;
+  const int ntn = (P.N + BN - 1) / BN;
   const int total = tstart[E] * ntn;
   // Eighths of the tile list per XCD, neighbouring tiles on one XCD.
   const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3, nslots = gridDim.x >> 3;
@@ -217,7 +213,7 @@ __global__ __launch_bounds__(kThreads, 2) void i8_tile_kernel(const Params P) {
     t.e = __builtin_amdgcn_readfirstlane(l);
     t.row0 = __builtin_amdgcn_readfirstlane(eoff[l] + mt * BM);
     t.valid = __builtin_amdgcn_readfirstlane(min(BM, eoff[l + 1] - eoff[l] - mt * BM));
-    t.n0 = __builtin_amdgcn_readfirstlane(nt * TN);
+    t.n0 = __builtin_amdgcn_readfirstlane(nt * BN);
     return t;
   };
   // The loads' state: resources of their tile, and the lane's offsets.
@@ -227,22 +223,20 @@ __global__ __launch_bounds__(kThreads, 2) void i8_tile_kernel(const Params P) {
     const auto* A = args();
     int lane = lane_id;  // opaque: the lane terms are recomputed here, not kept alive
     asm volatile("" : "+v"(lane));
-    const int64_t first = GU ? 0 : t.row0, rows = GU ? A->arows : t.valid;
-    ra = make_rsrc(A->a + first * K, rows * K);
-    rb = make_rsrc((GU && (wave & 1) ? A->w1 : A->w0) + static_cast<int64_t>(t.e) * A->N * K, static_cast<int64_t>(A->N) * K);
+    ra = make_rsrc(A->a + static_cast<int64_t>(t.row0) * K, static_cast<int64_t>(t.valid) * K);
+    rb = make_rsrc(A->w0 + static_cast<int64_t>(t.e) * A->N * K, static_cast<int64_t>(A->N) * K);
 #pragma unroll
     for (int i = 0; i < 2 * HA; ++i) {
       const int r = (i / HA) * (BM / 2) + (wave * HA + i % HA) * 8 + (lane >> 3);
       const int c = (lane & 7) ^ ((r >> 1) & 7);
-      const int row = GU ? (r < t.valid ? per_row[r] : 0) : r;
-      aoff[i] = r < t.valid ? static_cast<uint32_t>(row) * K + c * 16 : kOutside;
+      aoff[i] = r < t.valid ? static_cast<uint32_t>(r) * K + c * 16 : kOutside;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = (wave * 4 + i) * 8 + (lane >> 3);
       const int c = (lane & 7) ^ ((r >> 1) & 7);
       const int j = (r >> 4) & 3, q = r & 15;
-      const int n = t.n0 + (r >> 6) * (GU ? 32 : 64) + (GU ? 0 : (j >> 1) * 32) + 8 * (q >> 2) + 4 * (j & 1) + (q & 3);
+      const int n = t.n0 + (r >> 6) * 64 + (j >> 1) * 32 + 8 * (q >> 2) + 4 * (j & 1) + (q & 3);
       boff[i] = n < A->N ? static_cast<uint32_t>(n) * K + c * 16 : kOutside;
     }
   };
@@ -280,20 +274,18 @@ __global__ __launch_bounds__(kThreads, 2) void i8_tile_kernel(const Params P) {
                                                        valid * 4),
                                              (lds_ptr)(reinterpret_cast<char*>(per_row) + wave * 256), 4, r * 4, 0, 0, 0);
   };
-  // The tile's scales: wavefronts 0 to 3 the rows' (GU: through the tokens, which
-  // are still this tile's), 4 to 7 the columns'. One instruction each.
+  // The tile's scales: wavefronts 0 to 3 the rows', 4 to 7 the columns'. One instruction each.
   auto scale_load = [&](const Tile& t) __attribute__((always_inline)) {
     const auto* A = args();
     const int r = wave * 64 + lane_id;
     rsrc_t rs;
     uint32_t off;
     if (wave < 4) {
-      rs = make_rsrc(A->sa + (GU ? 0 : t.row0), (GU ? A->arows : t.valid) * 4ll);
-      off = r < t.valid ? static_cast<uint32_t>(GU ? per_row[r] : r) * 4 : kOutside;
+      rs = make_rsrc(A->sa + t.row0, t.valid * 4ll);
+      off = static_cast<uint32_t>(r) * 4;
     } else {
-      const int c = r - 256, n = t.n0 + (GU ? c & 127 : c);
-      rs = make_rsrc((GU && wave >= 6 ? A->sw1 : A->sw0) + static_cast<int64_t>(t.e) * A->N, A->N * 4ll);
-      off = n < A->N ? static_cast<uint32_t>(n) * 4 : kOutside;
+      rs = make_rsrc(A->sw0 + static_cast<int64_t>(t.e) * A->N, A->N * 4ll);
+      off = static_cast<uint32_t>(t.n0 + r - 256) * 4;
     }
     __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)(reinterpret_cast<char*>(scale) + wave * 256), 4, off, 0, 0, 0);
   };
@@ -362,18 +354,10 @@ __global__ __launch_bounds__(kThreads, 2) void i8_tile_kernel(const Params P) {
       landed(pending{});
       if constexpr (first) {  // every wavefront has left the previous tile's epilogue
         scale_load(now);
-        if constexpr (GU) {
-          if (more) {
-            nx = find(next);
-            per_row_load(args()->row_token, nx.row0, nx.valid);
-          }
-        } else if (const float* w = args()->row_weight; w != nullptr) {
-          per_row_load(w, now.row0, now.valid);
-        }
+        if (const float* w = args()->row_weight; w != nullptr) per_row_load(w, now.row0, now.valid);
       }
       if (last && more) {
-        if constexpr (!GU) nx = find(next);
-        if (GU && first) landed(none{});  // a reduction of one pair: the tokens were only just sent for
+        nx = find(next);
         aim(nx);
       }
       half(nic, one{}, y0, nullptr, x0, w0, last ? 0 : s + 2, last ? more : s + 2 < steps);
@@ -391,30 +375,316 @@ __global__ __launch_bounds__(kThreads, 2) void i8_tile_kernel(const Params P) {
     const int lane = lane_id, g = lane >> 4, q = lane & 15;
     const int row0 = now.row0, valid = now.valid, n0 = now.n0;
     auto columns = [&](int at) __attribute__((always_inline)) { return *reinterpret_cast<const f32x4*>(&scale[256 + at]); };
+    const rsrc_t ro = make_rsrc(A->out + static_cast<int64_t>(row0) * A->N, static_cast<int64_t>(valid) * A->N * 2);
+    f32x4 cs[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) cs[j] = columns(wn * 64 + (j >> 1) * 32 + 8 * g + 4 * (j & 1));
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int r = row_of(i, q);
+      const float rs = scale[r] * (A->row_weight != nullptr ? __int_as_float(per_row[r]) : 1.0f);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int n = n0 + wn * 64 + 32 * h + 8 * g;
+        u32x4 o{};
+        if (i < NI && row_of(i, 0) < valid) {  // 16 rows past the end are not packed
+          float v[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            v[c] = static_cast<float>(acc[i][2 * h + c / 4][c % 4]) * cs[2 * h + c / 4][c % 4] * rs;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[c] = pack_bf16x2(v[2 * c], v[2 * c + 1]);
+        }
+        __builtin_amdgcn_raw_buffer_store_b128(
+            o, ro, i < NI && r < valid && n < A->N ? (static_cast<uint32_t>(r) * A->N + n) * 2 : kOutside, 0, 0);
+      }
+    }
+    now = nx;
+    L = next;
+  };
+
+  aim(now);
+#pragma unroll
+  for (int v = 0; v < G2; ++v) load(0, v, x0, w0, 0, true);
+#pragma unroll
+  for (int v = 0; v < G1; ++v) load(1, v, y0, nullptr, 0, true);
+#pragma unroll
+  for (int v = 0; v < G2; ++v) load(0, v, x1, w1, 1, steps > 1);
+  landed(none{});
+  while (L < hi) {
+    if (now.valid > BM / 2) tile(std::integral_constant<int, FM>{});
+    else tile(std::integral_constant<int, HM>{});  // the first half holds every row
+  }
+  landed(none{});  // nothing is on its way into LDS when the workgroup ends
+}
+
+// ---- many rows per expert, two workgroups per CU ------------------------------
+
+constexpr int kW4 = 256;   // threads of i8_wide_kernel
+constexpr int KW = 64;     // its k per step
+constexpr int kRing = 3;   // stages of LDS; loads run two steps ahead
+
+template <bool GU, bool S8 = false>
+__global__ __attribute__((amdgpu_flat_work_group_size(kW4, kW4), amdgpu_waves_per_eu(2, 2))) void i8_duo_kernel(
+    const Params P) {
+  constexpr int BM = 128, TN = GU ? BN / 2 : BN;
+  constexpr int FM = 4, FN = 8;       // 16-row tiles of a and of the weights per wavefront
+  constexpr int SA = BM * KW, STAGE = SA + BN * KW;
+  constexpr int LA = 2, LOADS = LA + 4;  // per wavefront and step: 2 of a's rows, 4 of the weights'
+  constexpr int STORES = GU ? 5 * FM : 4 * FM;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds0[STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds1[STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds2[STAGE];
+  __shared__ int tstart[1025];
+  __shared__ int wsum[kW4 / kWave];
+  __shared__ float amax[GU ? BM : 1][2];
+  __shared__ __attribute__((aligned(256))) int per_row[BM];        // GU: the next tile's tokens, else this one's weights
+  __shared__ __attribute__((aligned(256))) float scale[BN + BN];   // this tile's scales: rows, columns
+
+  const int tid = threadIdx.x;
+  const int lane_id = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  const int E = P.E, K = P.K;
+  {  // tstart[e]: row tiles of the experts before e (four experts per thread)
+    int c[4], mine = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = 4 * tid + i;
+      const int b = e < E && P.offsets ? P.offsets[e] : 0;
+      const int t = e < E ? (P.offsets ? P.offsets[e + 1] : P.M) : 0;
+      c[i] = e < E ? (t - b + BM - 1) / BM : 0;
+      mine += c[i];
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+      const int v = __shfl_up(incl, o, kWave);
+      if (lane_id >= o) incl += v;
+    }
+    if (lane_id == kWave - 1) wsum[wave] = incl;
+    __syncthreads();
+    int at = incl - mine;
+    for (int w = 0; w < wave; ++w) at += wsum[w];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (4 * tid + i < E) tstart[4 * tid + i] = at;
+      at += c[i];
+    }
+    if (tid == kW4 - 1) tstart[E] = at;
+    __syncthreads();
+  }
+  const int ntn = (P.N + TN - 1) / TN;
+  const int total = tstart[E] * ntn;
+  const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3, nslots = gridDim.x >> 3;
+  const int lo = static_cast<int>(static_cast<int64_t>(total) * xcd / 8);
+  const int hi = static_cast<int>(static_cast<int64_t>(total) * (xcd + 1) / 8);
+  const int steps = (K + KW - 1) / KW, padded = (steps + kRing - 1) / kRing * kRing;
+  int L = lo + slot;
+  if (L >= hi) return;
+
+  auto args = [&]() __attribute__((always_inline)) {
+    uintptr_t u = reinterpret_cast<uintptr_t>(__builtin_amdgcn_kernarg_segment_ptr());
+    asm volatile("" : "+s"(u));
+    return reinterpret_cast<const __attribute__((address_space(4))) Params*>(u);
+  };
+  struct Tile {
+    int e, row0, valid, n0;
+  };
+  auto find = [&](int at) __attribute__((always_inline)) {
+    int l = 0, h = E - 1;
+    while (l < h) {
+      const int mid = (l + h + 1) >> 1;
+      if (tstart[mid] * ntn <= at) l = mid; else h = mid - 1;
+    }
+    const int rem = at - tstart[l] * ntn, mte = tstart[l + 1] - tstart[l];
+    const int band = rem / (kBand * ntn), bm = min(kBand, mte - band * kBand);
+    const int nt = (rem - band * kBand * ntn) / bm, mt = band * kBand + rem - band * kBand * ntn - nt * bm;
+    Tile t;
+    t.e = __builtin_amdgcn_readfirstlane(l);
+    const int32_t* off = args()->offsets;
+    const int begin = off ? off[t.e] : 0, end = off ? off[t.e + 1] : args()->M;
+    t.row0 = __builtin_amdgcn_readfirstlane(begin + mt * BM);
+    t.valid = __builtin_amdgcn_readfirstlane(min(BM, end - begin - mt * BM));
+    t.n0 = __builtin_amdgcn_readfirstlane(nt * TN);
+    return t;
+  };
+  // LDS row r of a stage is 64 bytes, chunk c at (c ^ (r >> 2 & 3)): 16 rows of one
+  // chunk touch every bank once. Row r of a: the tile's row r. Row r of the
+  // weights: columns in such an order that a lane's results are 8 neighbours.
+  rsrc_t ra, rb;
+  uint32_t aoff[LA], boff[4];
+  auto aim = [&](const Tile& t) __attribute__((always_inline)) {
+    const auto* A = args();
+    int lane = lane_id;
+    asm volatile("" : "+v"(lane));
+    const int64_t first = GU ? 0 : t.row0, rows = GU ? A->arows : t.valid;
+    ra = make_rsrc(A->a + first * K, rows * K);
+    rb = make_rsrc((GU && (wave & 1) ? A->w1 : A->w0) + static_cast<int64_t>(t.e) * A->N * K, static_cast<int64_t>(A->N) * K);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = (wave * 4 + i) * 16 + (lane >> 2);
+      const int c = (lane & 3) ^ ((r >> 2) & 3);
+      if (i < LA) {
+        const int ar = (wave * LA + i) * 16 + (lane >> 2);
+        const int row = GU ? (ar < t.valid ? per_row[ar] : 0) : ar;
+        aoff[i] = ar < t.valid ? static_cast<uint32_t>(row) * K + c * 16 : kOutside;
+      }
+      const int j = (r >> 4) & (GU ? 3 : 7), q = r & 15;
+      const int n = t.n0 + (r >> 7) * (GU ? 64 : 128) + (j >> 1) * 32 + 8 * (q >> 2) + 4 * (j & 1) + (q & 3);
+      boff[i] = n < A->N ? static_cast<uint32_t>(n) * K + c * 16 : kOutside;
+    }
+  };
+  typedef __attribute__((address_space(3))) void* lds_ptr;
+  auto load = [&](int v, uint8_t* S, int s, int k) __attribute__((always_inline)) {
+    const bool weights = v < 4;
+    const int i = weights ? v : v - 4, blk = weights ? wave * 4 + i : wave * LA + i;
+    const int c = (lane_id & 3) ^ ((lane_id >> 4) & 3);  // of the lane's row: (r >> 2 & 3) = lane >> 4
+    const uint32_t to = weights ? boff[i & 3] : aoff[i % LA];
+    const uint32_t off = c * 16 < k ? to : kOutside;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(weights ? rb : ra, (lds_ptr)(S + (weights ? SA : 0) + blk * 1024), 16, off,
+                                             s * KW, 0, 0);
+  };
+  auto landed = [&](auto pending) __attribute__((always_inline)) {
+    constexpr int n = decltype(pending)::value;
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070 | (n & 15) | (n >> 4) << 14);  // vmcnt(n) lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  };
+  using none = std::integral_constant<int, 0>;
+  auto per_row_load = [&](const void* base, int row0, int valid) __attribute__((always_inline)) {
+    if (wave >= BM / 64) return;
+    const int r = wave * 64 + lane_id;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(static_cast<const char*>(base) + static_cast<int64_t>(row0) * 4,
+                                                       valid * 4),
+                                             (lds_ptr)(reinterpret_cast<char*>(per_row) + wave * 256), 4, r * 4, 0, 0, 0);
+  };
+  auto scale_load = [&](const Tile& t) __attribute__((always_inline)) {
+    const auto* A = args();
+    const int r = wave * 64 + lane_id;
+    const rsrc_t rr = make_rsrc(A->sa + (GU ? 0 : t.row0), (GU ? A->arows : t.valid) * 4ll);
+    const uint32_t off = r < t.valid ? static_cast<uint32_t>(GU ? per_row[r & (BM - 1)] : r) * 4 : kOutside;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rr, (lds_ptr)(reinterpret_cast<char*>(scale) + wave * 256), 4, off, 0, 0, 0);
+    const int n = t.n0 + (GU ? r & 127 : r);
+    const rsrc_t rc = make_rsrc((GU && wave >= 2 ? A->sw1 : A->sw0) + static_cast<int64_t>(t.e) * A->N, A->N * 4ll);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rc, (lds_ptr)(reinterpret_cast<char*>(scale + BN) + wave * 256), 4,
+                                             n < A->N ? static_cast<uint32_t>(n) * 4 : kOutside, 0, 0, 0);
+  };
+
+  i32x4 acc[FM][FN];
+  u32x4 fa[2], fb[FN];
+  int fo;  // the lane's byte in a 16-row tile
+  {
+    const int q = lane_id & 15, g = lane_id >> 4;
+    fo = q * KW + ((g ^ ((q >> 2) & 3)) << 4);
+  }
+  // The wavefront's 16-row tile i is the tile's 2 i + wm: both halves of a short tile have rows.
+  auto read_a = [&](u32x4& to, const uint8_t* S, int i) __attribute__((always_inline)) {
+    to = *reinterpret_cast<const u32x4*>(S + (2 * i + wm) * (16 * KW) + fo);
+  };
+  auto read_b = [&](u32x4& to, const uint8_t* S, int j) __attribute__((always_inline)) {
+    to = *reinterpret_cast<const u32x4*>(S + SA + (wn * 8 + j) * (16 * KW) + fo);
+  };
+  // Step s on stage C, while the loads of step sn go out into stage D.
+  auto kstep = [&](auto nic, auto firstc, bool stores, const uint8_t* C, uint8_t* D, int sn, bool live,
+                   auto&& after) __attribute__((always_inline)) {
+    constexpr int NI = decltype(nic)::value;
+    constexpr bool first = decltype(firstc)::value != 0;
+    asm volatile("" ::: "memory");
+    if (stores) __builtin_amdgcn_s_waitcnt(0x0070 | ((LOADS + STORES) & 15) | ((LOADS + STORES) >> 4) << 14);
+    else __builtin_amdgcn_s_waitcnt(0x0070 | (LOADS & 15) | (LOADS >> 4) << 14);
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    after();
+    int k = min(K - sn * KW, live ? KW : 0);
+    asm volatile("" : "+s"(k));  // a select, not a branch
+    read_a(fa[0], C, 0);
+#pragma unroll
+    for (int j = 0; j < FN; ++j) read_b(fb[j], C, j);
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_setprio(1);  // products before the other workgroup's loads and results
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      if (i + 1 < NI) read_a(fa[(i + 1) & 1], C, i + 1);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < FN; ++j) acc[i][j] = product64(fb[j], fa[i & 1], first ? i32x4{} : acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int v = i * LOADS / NI; v < (i + 1) * LOADS / NI; ++v) load(v, D, sn, k);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    __builtin_amdgcn_s_setprio(0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  Tile now = find(L), nx = now;
+  using zero = std::integral_constant<int, 0>;
+  using one = std::integral_constant<int, 1>;
+  auto tile = [&](auto nic) __attribute__((always_inline)) {
+    constexpr int NI = decltype(nic)::value;
+    const int next = L + nslots;
+    const bool more = next < hi;
+    auto nothing = [] {};
+    // Step s is read after its own barrier, at which all but step s + 1's loads
+    // (and the stores, if they are newer) have landed; step s + 2's go out then.
+    auto turn = [&]() __attribute__((always_inline)) {
+      if (more) {
+        if constexpr (!GU) nx = find(next);
+        if (GU && padded == kRing) landed(none{});  // the tokens were only just sent for
+        aim(nx);
+      }
+    };
+    kstep(nic, one{}, true, lds0, lds2, 2, 2 < steps, [&]() __attribute__((always_inline)) {
+      scale_load(now);
+      if constexpr (GU) {
+        if (more) {
+          nx = find(next);
+          per_row_load(args()->row_token, nx.row0, nx.valid);
+        }
+      } else if (const float* w = args()->row_weight; w != nullptr) {
+        per_row_load(w, now.row0, now.valid);
+      }
+    });
+    for (int s = kRing; s < padded; s += kRing) {  // steps s - 2 .. s
+      kstep(nic, zero{}, s == kRing, lds1, lds0, s, s < steps, nothing);
+      kstep(nic, zero{}, false, lds2, lds1, s + 1, s + 1 < steps, nothing);
+      kstep(nic, zero{}, false, lds0, lds2, s + 2, s + 2 < steps, nothing);
+    }
+    kstep(nic, zero{}, padded == kRing, lds1, lds0, 0, more, turn);
+    kstep(nic, zero{}, false, lds2, lds1, 1, more && steps > 1, nothing);
+    // ---- epilogue; stores of rows and columns outside go out of range, so
+    // that their count is fixed: they run on under the next tile's first steps.
+    const auto* A = args();
+    const int lane = lane_id, g = lane >> 4, q = lane & 15;
+    const int row0 = now.row0, valid = now.valid, n0 = now.n0;
+    auto columns = [&](int at) __attribute__((always_inline)) { return *reinterpret_cast<const f32x4*>(&scale[BN + at]); };
     if constexpr (GU) {
       const int NT = (A->N + 127) / 128;
       const rsrc_t rv = make_rsrc(A->v16 + static_cast<int64_t>(row0) * A->N, static_cast<int64_t>(valid) * A->N * 2);
       const rsrc_t rl = make_rsrc(A->v8 + static_cast<int64_t>(row0) * A->N, static_cast<int64_t>(valid) * A->N);
       const rsrc_t rm = make_rsrc(A->amax + static_cast<int64_t>(row0) * NT, static_cast<int64_t>(valid) * NT * 4);
-      f32x4 cs[4];
+      f32x4 cs[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) cs[j] = columns((j >> 1) * 128 + wn * 32 + 8 * g + 4 * (j & 1));
+      for (int j = 0; j < 8; ++j) cs[j] = columns((j >> 2) * 128 + wn * 64 + ((j >> 1) & 1) * 32 + 8 * g + 4 * (j & 1));
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const float rs = scale[row_of(i, q)];
+        const int r = (2 * i + wm) * 16 + q;
+        const float rs = scale[r];
         float m = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 4; ++j) {
           f32x4 v;
 #pragma unroll
           for (int x = 0; x < 4; ++x)
             v[x] = silu_mul(static_cast<float>(acc[i][j][x]) * (rs * cs[j][x]),
-                            static_cast<float>(acc[i][j + 2][x]) * (rs * cs[j + 2][x]));
+                            static_cast<float>(acc[i][j + 4][x]) * (rs * cs[j + 4][x]));
           m = max4(m, v);
           acc[i][j] = __builtin_bit_cast(i32x4, v);
         }
         m = across_groups(m);
-        if (g == 0) amax[row_of(i, q)][wn] = m;
+        if (g == 0) amax[r][wn] = m;
       }
       asm volatile("" ::: "memory");
       __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
@@ -422,51 +692,57 @@ __global__ __launch_bounds__(kThreads, 2) void i8_tile_kernel(const Params P) {
       asm volatile("" ::: "memory");
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
-        const int r = row_of(i, q);
-        u32x4 o{};
-        u32x2 lo{};
-        float m = 0.0f;
-        if (i < NI) {
-          m = max4(0.0f, *reinterpret_cast<const f32x4*>(amax[r]));
-          const Factor24 f(m);
-          const Packed24 p0(__builtin_bit_cast(f32x4, acc[i][0]), f), p1(__builtin_bit_cast(f32x4, acc[i][1]), f);
-          o = u32x4{p0.hi[0], p0.hi[1], p1.hi[0], p1.hi[1]};
-          lo = u32x2{p0.lo, p1.lo};
-        }
-        const int n = n0 + wn * 32 + 8 * g;
+        const int r = (2 * i + wm) * 16 + q;
         const bool row = i < NI && r < valid;
-        const uint32_t to = row && n < A->N ? static_cast<uint32_t>(r) * A->N + n : kOutside;
-        __builtin_amdgcn_raw_buffer_store_b128(o, rv, to == kOutside ? to : 2 * to, 0, 0);
-        __builtin_amdgcn_raw_buffer_store_b64(lo, rl, to, 0, 0);
+        float m = 0.0f;
+        if (i < NI) m = __builtin_elementwise_maximum(amax[r][0], amax[r][1]);
+        const Factor24 f(m);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          u32x4 o{};
+          u32x2 low{};
+          if (i < NI) {
+            const Packed24 p0(__builtin_bit_cast(f32x4, acc[i][2 * h]), f), p1(__builtin_bit_cast(f32x4, acc[i][2 * h + 1]), f);
+            o = u32x4{p0.hi[0], p0.hi[1], p1.hi[0], p1.hi[1]};
+            low = u32x2{p0.lo, p1.lo};
+          }
+          const int n = n0 + wn * 64 + 32 * h + 8 * g;
+          const uint32_t to = row && n < A->N ? static_cast<uint32_t>(r) * A->N + n : kOutside;
+          __builtin_amdgcn_raw_buffer_store_b128(o, rv, to == kOutside ? to : 2 * to, 0, 0);
+          __builtin_amdgcn_raw_buffer_store_b64(low, rl, to, 0, 0);
+        }
         __builtin_amdgcn_raw_buffer_store_b32(
             __float_as_uint(m), rm, row && wn == 0 && g == 0 ? (static_cast<uint32_t>(r) * NT + n0 / 128) * 4 : kOutside, 0,
             0);
       }
     } else {
       const rsrc_t ro = make_rsrc(A->out + static_cast<int64_t>(row0) * A->N, static_cast<int64_t>(valid) * A->N * 2);
-      f32x4 cs[4];
+      f32x4 cs[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) cs[j] = columns(wn * 64 + (j >> 1) * 32 + 8 * g + 4 * (j & 1));
+      for (int j = 0; j < 8; ++j) cs[j] = columns(wn * 128 + (j >> 1) * 32 + 8 * g + 4 * (j & 1));
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
-        const int r = row_of(i, q);
-        const float rs = scale[r] * (A->row_weight != nullptr ? __int_as_float(per_row[r]) : 1.0f);
+        const int r = (2 * i + wm) * 16 + q;
+        const float rs = i < NI ? scale[r] * (A->row_weight != nullptr ? __int_as_float(per_row[r]) : 1.0f) : 0.0f;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int n = n0 + wn * 64 + 32 * h + 8 * g;
+        for (int h = 0; h < 4; ++h) {
+          const int n = n0 + wn * 128 + 32 * h + 8 * g;
           u32x4 o{};
-          if (i < NI && row_of(i, 0) < valid) {  // 16 rows past the end are not packed
+          if (i < NI) {
             float v[8], m = 0.0f;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
-              v[c] = static_cast<float>(acc[i][2 * h + c / 4][c % 4]) * (rs * cs[2 * h + c / 4][c % 4]);
-              m = __builtin_elementwise_maximum(m, fabsf(v[c]));  // NaN if one is
+              v[c] = static_cast<float>(acc[i][2 * h + c / 4][c % 4]) * cs[2 * h + c / 4][c % 4] * rs;
+              if constexpr (S8) m = __builtin_elementwise_maximum(m, fabsf(v[c]));  // NaN if one is
             }
             float f = 0.0f;
-            const uint32_t s = A->shared8 ? shared8_exponent(m, f) : 0;
+            uint32_t s = 0;
+            if constexpr (S8) s = shared8_exponent(m, f);
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              o[c] = A->shared8 ? shared8_word(v[2 * c], v[2 * c + 1], s, f, c) : pack_bf16x2(v[2 * c], v[2 * c + 1]);
+            for (int c = 0; c < 4; ++c) {
+              if constexpr (S8) o[c] = shared8_word(v[2 * c], v[2 * c + 1], s, f, c);
+              else o[c] = pack_bf16x2(v[2 * c], v[2 * c + 1]);
+            }
           }
           __builtin_amdgcn_raw_buffer_store_b128(
               o, ro, i < NI && r < valid && n < A->N ? (static_cast<uint32_t>(r) * A->N + n) * 2 : kOutside, 0, 0);
@@ -483,16 +759,16 @@ __global__ __launch_bounds__(kThreads, 2) void i8_tile_kernel(const Params P) {
   }
   aim(now);
 #pragma unroll
-  for (int v = 0; v < G2; ++v) load(0, v, x0, w0, 0, true);
+  for (int v = 0; v < LOADS; ++v) load(v, lds0, 0, min(K, KW));
 #pragma unroll
-  for (int v = 0; v < G1; ++v) load(1, v, y0, nullptr, 0, true);
-#pragma unroll
-  for (int v = 0; v < G2; ++v) load(0, v, x1, w1, 1, steps > 1);
+  for (int v = 0; v < LOADS; ++v) load(v, lds1, 1, min(K - KW, KW));
   landed(none{});
   while (L < hi) {
-    if (now.valid > BM / 2) tile(std::integral_constant<int, FM>{});
-    else tile(std::integral_constant<int, HM>{});  // the first half holds every row
+    if (now.valid > 64) tile(std::integral_constant<int, 4>{});
+    else if (now.valid > 32) tile(std::integral_constant<int, 2>{});
+    else tile(std::integral_constant<int, 1>{});
   }
+  landed(none{});  // nothing is on its way into LDS when the workgroup ends
 }
 
 // ---- few rows per expert ----------------------------------------------------
@@ -717,10 +993,12 @@ hipError_t launch(const I8GemmArgs& a, hipStream_t st) {
       while (ks < kWaves && static_cast<int64_t>(a.E) * ceil_div(a.N, 16 * kWaves / ks) < 2 * grid && ks < KB) ks *= 2;
     const int groups = ceil_div(a.N, 16 * kWaves / ks);
     i8_stream_kernel<GU><<<static_cast<unsigned>(a.E) * groups, kThreads, 0, st>>>(P, ks, groups);
-  } else if (avg <= 96) {
-    i8_tile_kernel<GU, 128><<<grid, kThreads, 0, st>>>(P);
+  } else if (!GU && !a.shared8 && avg >= 512 && (a.M / 256) * static_cast<int64_t>(ceil_div(a.N, BN)) >= grid) {
+    i8_tile_kernel<<<grid, kThreads, 0, st>>>(P);
+  } else if (!GU && a.shared8) {
+    i8_duo_kernel<GU, !GU><<<2 * grid, kW4, 0, st>>>(P);
   } else {
-    i8_tile_kernel<GU, 256><<<grid, kThreads, 0, st>>>(P);
+    i8_duo_kernel<GU><<<2 * grid, kW4, 0, st>>>(P);
   }
   return hipGetLastError();
 }

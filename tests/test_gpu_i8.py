@@ -135,6 +135,25 @@ def test_gemm_dense(M, N, K):
     assert (out.cpu().double() - want).abs().le(want.abs() * (U + 2.0**-21)).all()
 
 
+@pytest.mark.parametrize("K", [16, 144, 400, 1040])
+@pytest.mark.parametrize("counts,weighted", [([4200], False), ([2000, 0, 37, 2500, 128], True)])
+def test_gemm_large_tiles(counts, weighted, K):
+    """Enough rows and columns for 256 x 256 tiles on every CU, several a workgroup."""
+    N, M, E = 4200, sum(counts), len(counts)
+    off = torch.tensor([0] + counts).cumsum(0).to(torch.int32)
+    g = gen(K)
+    aq = torch.randint(-128, 128, (M, K), generator=g).to(torch.int8)
+    wq = torch.randint(-128, 128, (E, N, K), generator=g).to(torch.int8)
+    sa, sw = torch.rand(M, generator=g) + 0.01, torch.rand(E, N, generator=g) + 0.01
+    rw = torch.rand(M, generator=g) if weighted else None
+    out = torch.full((M + 1, N), -3.0, dtype=BF, device="cuda")
+    for _ in range(2):  # again over its own results
+        B.moe_gemm_i8(M, E, N, K, *dev(aq, sa, off if E > 1 else None, wq, sw, rw), out)
+        got = out.cpu().double()
+        want = Q.product(aq, sa, off, wq, sw, rw)
+        assert (got[M] == -3).all() and (got[:M] - want).abs().le(want.abs() * (U + 2.0**-21)).all()
+
+
 def test_gemm_largest_sums():
     K = 2**17 - 16
     for M in (1, 130):
