@@ -292,10 +292,10 @@ moe_status moe_experts_i8(moe_shape s, const void* x, const int32_t* topk_idx, c
     return MOE_EINVAL;
   if (misaligned(x, wq_gate, wq_up, wq_down, xq, aq, o_perm, y, ws)) return MOE_EINVAL;
   if (ws_bytes < i8_layout(s).total) return MOE_EWORKSPACE;
-  if ((st = from_hip(moe::launch_permute_fused(s, topk_idx, topk_w, counts, offsets, sorted_to_flat, flat_to_sorted,
-                                               row_token, row_weight, ws, stream))) != MOE_OK)
+  if ((st = from_hip(moe::launch_permute_quantize_i8(s, topk_idx, topk_w, x, counts, offsets, sorted_to_flat,
+                                                     flat_to_sorted, row_token, row_weight, xq, x_scale, ws,
+                                                     stream))) != MOE_OK)
     return st;
-  if ((st = moe_quantize_i8_rows(s.T, s.H, x, xq, x_scale, stream)) != MOE_OK) return st;
   if ((st = moe_gemm_gate_up_i8(s, xq, x_scale, row_token, offsets, wq_gate, w_gate_scale, wq_up, w_up_scale, aq, a_scale,
                                 ws, ws_bytes, stream)) != MOE_OK)
     return st;

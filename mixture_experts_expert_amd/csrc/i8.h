@@ -66,6 +66,31 @@ __device__ __forceinline__ float code_value(uint32_t w, int i) {
   return static_cast<float>(static_cast<int8_t>(w >> (8 * i)));
 }
 
+// One row [K] of bf16 by a wavefront: codes and scale. The first 4096 columns
+// stay in registers between the maximum and the codes.
+template <int LANES>
+__device__ __forceinline__ uint32_t group_max(uint32_t v);
+__device__ __forceinline__ void quantize_row(int K, const uint4* __restrict__ in, uint2* __restrict__ q,
+                                             float* __restrict__ scale) {
+  constexpr int CPL = 8;
+  const int lane = threadIdx.x % kWave, chunks = K / 8;
+  uint4 v[CPL];
+  u16x2 m{0, 0};
+#pragma unroll
+  for (int i = 0; i < CPL; ++i) v[i] = lane + i * kWave < chunks ? in[lane + i * kWave] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+  for (int i = 0; i < CPL; ++i) m = amax_bits(m, v[i]);
+  for (int c = lane + CPL * kWave; c < chunks; c += kWave) m = amax_bits(m, in[c]);
+  const uint32_t r = group_max<16>(amax_bits(m));
+  const CodeFactor f(max(max(__builtin_amdgcn_readlane(r, 0), __builtin_amdgcn_readlane(r, 16)),
+                         max(__builtin_amdgcn_readlane(r, 32), __builtin_amdgcn_readlane(r, 48))));
+#pragma unroll
+  for (int i = 0; i < CPL; ++i)
+    if (lane + i * kWave < chunks) q[lane + i * kWave] = codes8(v[i], f);
+  for (int c = lane + CPL * kWave; c < chunks; c += kWave) q[c] = codes8(in[c], f);
+  if (lane == 0) *scale = f.scale;
+}
+
 // Maximum over the 8 or 16 neighbouring lanes of a group, in every lane of it.
 template <int LANES>
 __device__ __forceinline__ uint32_t group_max(uint32_t v) {

@@ -104,6 +104,11 @@ hipError_t launch_permute_rows(const moe_shape& s, const int32_t* idx, const flo
 hipError_t launch_permute_fused(const moe_shape& s, const int32_t* idx, const float* w, int32_t* counts,
                                 int32_t* offsets, int32_t* s2f, int32_t* f2s, int32_t* row_token, float* row_weight,
                                 void* ws, hipStream_t st);
+// launch_permute_fused and launch_quantize_i8_rows of x (xq, x_scale), sharing
+// their launches.
+hipError_t launch_permute_quantize_i8(const moe_shape& s, const int32_t* idx, const float* w, const void* x,
+                                      int32_t* counts, int32_t* offsets, int32_t* s2f, int32_t* f2s, int32_t* row_token,
+                                      float* row_weight, int8_t* xq, float* x_scale, void* ws, hipStream_t st);
 // The allocation-free sort: the per-block histograms in the library's static
 // scratch (kScratchBytes per device) instead of a workspace; the caller checks
 // sort_hist_bytes(s) <= kScratchBytes first.

@@ -16,7 +16,7 @@
 // blocks) + (rank inside its block): the definition of the stable order.
 #include <mutex>
 
-#include "moe_internal.h"
+#include "i8.h"
 
 // Device memory of the allocation-free sort (moe_forward_fused_noalloc): the
 // per-block histograms live in this array instead of a caller's workspace.
@@ -95,6 +95,118 @@ __global__ __launch_bounds__(kScanThreads) void scan_kernel(int nb, int E, int32
 }
 
 constexpr int kWavesPerBlock = kThreads / kWave;
+
+// Workgroups from `sorting` on quantise rows of x [T][H] (i8.h) beside the sort's
+// first pass: they have nothing to do with each other, and the launch between
+// them is as long as either.
+__global__ __launch_bounds__(kThreads) void hist_quantize_kernel(int sorting, int n, int E, const int32_t* __restrict__ idx,
+                                                                 int32_t* __restrict__ hist, int T, int H,
+                                                                 const uint4* __restrict__ x, uint2* __restrict__ xq,
+                                                                 float* __restrict__ x_scale) {
+  __shared__ int32_t h[1024];
+  if (static_cast<int>(blockIdx.x) >= sorting) {
+    const int t = (static_cast<int>(blockIdx.x) - sorting) * kWavesPerBlock +
+                  __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / kWave);
+    const int64_t at = static_cast<int64_t>(t) * (H / 8);
+    if (t < T) quantize_row(H, x + at, xq + at, x_scale + t);
+    return;
+  }
+  for (int e = threadIdx.x; e < E; e += kThreads) h[e] = 0;
+  __syncthreads();
+  const int64_t f0 = static_cast<int64_t>(blockIdx.x) * kPermBlock;
+  for (int i = threadIdx.x; i < kPermBlock; i += kThreads) {
+    const int64_t f = f0 + i;
+    if (f < n) atomicAdd(&h[clamp_expert(idx[f], E)], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += kThreads) hist[static_cast<int64_t>(blockIdx.x) * E + e] = h[e];
+}
+
+// The whole sort of up to kSmallSort pairs by workgroup 0, beside the others'
+// rows of x. A wavefront ranks a run of pairs of its own, 64 at a time in
+// order (peers by one ballot per bit of the expert, its own counters in LDS);
+// the wavefronts' counts, in order, and the experts' totals then place them.
+constexpr int kSmallThreads = 1024, kSmallWaves = kSmallThreads / kWave, kSmallSort = 4096;
+constexpr int kSmallRun = kSmallSort / kSmallWaves;  // pairs of a wavefront at most
+__global__ __launch_bounds__(kSmallThreads) void sort_quantize_kernel(
+    int n, int E, int nbits, const int32_t* __restrict__ idx, const float* __restrict__ w, int k,
+    int32_t* __restrict__ counts, int32_t* __restrict__ offsets, int32_t* __restrict__ s2f, int32_t* __restrict__ f2s,
+    int32_t* __restrict__ row_token, float* __restrict__ row_weight, int T, int H, const uint4* __restrict__ x,
+    uint2* __restrict__ xq, float* __restrict__ x_scale) {
+  __shared__ uint16_t cnt[kSmallWaves][1024];
+  __shared__ int32_t start[1024];
+  __shared__ int32_t part[kSmallWaves];
+  const int tid = threadIdx.x, lane = tid % kWave, wv = __builtin_amdgcn_readfirstlane(tid / kWave);
+  if (blockIdx.x > 0) {
+    const int t = (static_cast<int>(blockIdx.x) - 1) * kSmallWaves + wv;
+    const int64_t at = static_cast<int64_t>(t) * (H / 8);
+    if (t < T) quantize_row(H, x + at, xq + at, x_scale + t);
+    return;
+  }
+  const int run = (n + kSmallThreads - 1) / kSmallThreads * kWave;  // of a wavefront: whole 64s, at most kSmallRun
+  constexpr int kSteps = kSmallRun / kWave;
+  int e[kSteps], rank[kSteps];
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    const int f = wv * run + s * kWave + lane;
+    e[s] = s * kWave < run && f < n ? clamp_expert(idx[f], E) : -1;
+  }
+  for (int i = lane; i < E; i += kWave) cnt[wv][i] = 0;
+  const uint64_t below = (lane == 0) ? 0ull : (~0ull >> (64 - lane));
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    const bool valid = e[s] >= 0;
+    uint64_t peers = __ballot(valid);
+    for (int b = 0; b < nbits; ++b) {
+      const bool bit = (e[s] >> b) & 1;
+      const uint64_t ones = __ballot(valid && bit);
+      peers &= bit ? ones : ~ones;
+    }
+    const int r = __popcll(peers & below);
+    rank[s] = 0;
+    if (valid) rank[s] = cnt[wv][e[s]] + r;
+    __builtin_amdgcn_wave_barrier();  // every lane has read its counter: LDS operations of a wavefront are in order
+    if (valid && r == 0) cnt[wv][e[s]] = static_cast<uint16_t>(rank[s] + __popcll(peers));
+    __builtin_amdgcn_wave_barrier();
+  }
+  __syncthreads();
+  // Thread e: its expert's counts in wavefront order, then the experts in order.
+  int total = 0;
+  if (tid < E) {
+#pragma unroll
+    for (int v = 0; v < kSmallWaves; ++v) {
+      const int c = cnt[v][tid];
+      cnt[v][tid] = static_cast<uint16_t>(total);
+      total += c;
+    }
+  }
+  int incl = total;
+#pragma unroll
+  for (int o = 1; o < kWave; o <<= 1) {
+    const int v = __shfl_up(incl, o);
+    incl += lane >= o ? v : 0;
+  }
+  if (lane == kWave - 1) part[wv] = incl;
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < kSmallWaves; ++v) incl += v < wv ? part[v] : 0;
+  if (tid < E) {
+    start[tid] = incl - total;
+    counts[tid] = total;
+    offsets[tid] = incl - total;
+    if (tid == E - 1) offsets[E] = incl;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    if (e[s] < 0) continue;
+    const int f = wv * run + s * kWave + lane, pos = start[e[s]] + cnt[wv][e[s]] + rank[s];
+    s2f[pos] = f;
+    f2s[f] = pos;
+    row_token[pos] = f / k;
+    row_weight[pos] = w[f];
+  }
+}
 
 // The fused inference forward also takes, per sorted row p, its token
 // row_token[p] = s2f[p] / k and its routing weight row_weight[p] = w[s2f[p]]
@@ -293,18 +405,20 @@ WsLayout ws_layout(const moe_shape& s) {
 
 namespace {
 
-// The stable counting sort shared by the permute entry points; hist holds
-// ceil(T*k / kPermBlock) * E int32 (every element is written before it is read).
-hipError_t launch_sort(const moe_shape& s, const int32_t* idx, int32_t* counts, int32_t* offsets, int32_t* s2f,
+int expert_bits(const moe_shape& s) {
+  int nbits = 0;
+  while ((1 << nbits) < s.E) ++nbits;
+  return nbits;
+}
+
+// The sort after its first pass.
+hipError_t launch_rank(const moe_shape& s, const int32_t* idx, int32_t* counts, int32_t* offsets, int32_t* s2f,
                        int32_t* f2s, const float* w, int32_t* row_token, float* row_weight, int32_t* hist,
                        hipStream_t st) {
   const int n = s.T * s.k;
   const int nb = ceil_div(n, kPermBlock);
-  int nbits = 0;
-  while ((1 << nbits) < s.E) ++nbits;
-  block_hist_kernel<<<nb, kThreads, 0, st>>>(n, s.E, idx, hist);
-  hipError_t err = hipGetLastError();
-  if (err != hipSuccess) return err;
+  const int nbits = expert_bits(s);
+  hipError_t err;
   if (nb <= kScanInBlocks) {  // each ranking block scans for itself: one launch fewer
     rank_scatter_kernel<true><<<nb, kThreads, 0, st>>>(n, s.E, nbits, idx, hist, counts, offsets, s2f, f2s, s.k, w,
                                                        row_token, row_weight);
@@ -315,6 +429,17 @@ hipError_t launch_sort(const moe_shape& s, const int32_t* idx, int32_t* counts, 
   rank_scatter_kernel<false><<<nb, kThreads, 0, st>>>(n, s.E, nbits, idx, hist, counts, offsets, s2f, f2s, s.k, w,
                                                       row_token, row_weight);
   return hipGetLastError();
+}
+
+// The stable counting sort shared by the permute entry points; hist holds
+// ceil(T*k / kPermBlock) * E int32 (every element is written before it is read).
+hipError_t launch_sort(const moe_shape& s, const int32_t* idx, int32_t* counts, int32_t* offsets, int32_t* s2f,
+                       int32_t* f2s, const float* w, int32_t* row_token, float* row_weight, int32_t* hist,
+                       hipStream_t st) {
+  const int n = s.T * s.k;
+  block_hist_kernel<<<ceil_div(n, kPermBlock), kThreads, 0, st>>>(n, s.E, idx, hist);
+  const hipError_t err = hipGetLastError();
+  return err != hipSuccess ? err : launch_rank(s, idx, counts, offsets, s2f, f2s, w, row_token, row_weight, hist, st);
 }
 
 int32_t* ws_hist(const moe_shape& s, void* ws) {
@@ -353,6 +478,25 @@ hipError_t launch_permute_fused(const moe_shape& s, const int32_t* idx, const fl
                                 int32_t* offsets, int32_t* s2f, int32_t* f2s, int32_t* row_token, float* row_weight,
                                 void* ws, hipStream_t st) {
   return launch_sort(s, idx, counts, offsets, s2f, f2s, w, row_token, row_weight, ws_hist(s, ws), st);
+}
+
+hipError_t launch_permute_quantize_i8(const moe_shape& s, const int32_t* idx, const float* w, const void* x,
+                                      int32_t* counts, int32_t* offsets, int32_t* s2f, int32_t* f2s, int32_t* row_token,
+                                      float* row_weight, int8_t* xq, float* x_scale, void* ws, hipStream_t st) {
+  const int n = s.T * s.k;
+  const uint4* from = static_cast<const uint4*>(x);
+  uint2* to = reinterpret_cast<uint2*>(xq);
+  if (n <= kSmallSort) {
+    sort_quantize_kernel<<<1 + ceil_div(s.T, kSmallWaves), kSmallThreads, 0, st>>>(
+        n, s.E, expert_bits(s), idx, w, s.k, counts, offsets, s2f, f2s, row_token, row_weight, s.T, s.H, from, to, x_scale);
+    return hipGetLastError();
+  }
+  const int nb = ceil_div(n, kPermBlock);
+  int32_t* hist = ws_hist(s, ws);
+  hist_quantize_kernel<<<nb + ceil_div(s.T, kWavesPerBlock), kThreads, 0, st>>>(nb, n, s.E, idx, hist, s.T, s.H, from, to,
+                                                                               x_scale);
+  const hipError_t err = hipGetLastError();
+  return err != hipSuccess ? err : launch_rank(s, idx, counts, offsets, s2f, f2s, w, row_token, row_weight, hist, st);
 }
 
 size_t sort_hist_bytes(const moe_shape& s) { return ws_layout(s).hist_bytes; }

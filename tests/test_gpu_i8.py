@@ -341,3 +341,48 @@ def test_stage_on_another_stream_and_in_a_graph():
             assert torch.equal(y, want[i])
             stage.forward(xs[(i + 1) % 3])  # eager work between replays, in the same buffers
             torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (5, 3, 2), (192, 128, 8), (255, 1024, 16), (1024, 7, 4), (4096, 300, 1),
+                                   (513, 128, 8), (3000, 16, 5)])
+def test_sort_is_permute_fused(T, E, k):
+    """The expert stage's sort, on both sides of 4096 pairs: the outputs of moe_permute_fused, and x's codes."""
+    H = I = 64
+    g = gen(T)
+    x = torch.randn(T, H, generator=g).to(BF)
+    idx = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).to(torch.int32)
+    if T > 100:
+        idx[: T // 2] = idx[0]  # a few long experts
+    tw = torch.rand(T, k, generator=g)
+    w = [(torch.zeros(E, 64, 64, dtype=torch.int8, device="cuda"), torch.ones(E, 64, device="cuda")) for _ in range(3)]
+    M, s = T * k, B.shape(T, H, E, k, I, BF)
+    xd, idxd, twd = dev(x, idx, tw)
+    new = lambda: [torch.full((n,), -7, dtype=torch.int32, device="cuda") for n in (E, E + 1, M, M, M)] + [torch.zeros(M, device="cuda")]
+    ours, want = new(), new()
+    ws = torch.full((max(B.moe_i8_workspace_bytes(s), B.moe_workspace_bytes(s)),), 0xFF, dtype=torch.uint8, device="cuda")
+    xq, xs = torch.empty(T, H, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    B.moe_experts_i8(s, xd, idxd, twd, *w[0], *w[1], *w[2], *ours, xq, xs, torch.empty(M, I, dtype=torch.int8, device="cuda"),
+                     torch.empty(M, device="cuda"), torch.empty(M, H, dtype=BF, device="cuda"),
+                     torch.empty(T, H, dtype=BF, device="cuda"), ws)
+    B.moe_permute_fused(s, idxd, twd, *want, ws)
+    assert all(torch.equal(a, b) for a, b in zip(ours, want))
+    assert torch.equal(xq.cpu(), Q.codes(x)[0])
+
+
+@pytest.mark.parametrize("H", [64, 512, 576, 4096, 4160, 8192])
+def test_rows_of_x_of_every_length(H):
+    """x's codes inside the expert stage are moe_quantize_i8_rows'."""
+    T, E, k, I = 9, 2, 1, 64
+    x, idx, tw, w = stage(T, H, E, k, I, 3)
+    x[2, H - 1], x[3] = float("inf"), 0.0
+    s = B.shape(T, H, E, k, I, BF)
+    xq, xs = torch.empty(T, H, dtype=torch.int8, device="cuda"), torch.empty(T, device="cuda")
+    i32 = lambda n: torch.empty(n, dtype=torch.int32, device="cuda")
+    B.moe_experts_i8(s, *dev(x, idx, tw), *[t for m in w for t in dev(*m)], i32(E), i32(E + 1), i32(T), i32(T), i32(T),
+                     torch.empty(T, device="cuda"), xq, xs, torch.empty(T, I, dtype=torch.int8, device="cuda"),
+                     torch.empty(T, device="cuda"), torch.empty(T, H, dtype=BF, device="cuda"),
+                     torch.empty(T, H, dtype=BF, device="cuda"),
+                     torch.empty(B.moe_i8_workspace_bytes(s), dtype=torch.uint8, device="cuda"))
+    q, sc = torch.empty_like(xq), torch.empty_like(xs)
+    B.moe_quantize_i8_rows(T, H, dev(x), q, sc)
+    assert torch.equal(q, xq) and torch.equal(sc.nan_to_num(-1), xs.nan_to_num(-1)) and sc[2].isnan()
