@@ -212,14 +212,23 @@ __device__ __forceinline__ bf16x8 widen8(uint32_t a, uint32_t b) {  // eight E4M
   return bf16x8{r0.x, r0.y, r1.x, r1.y, r2.x, r2.y, r3.x, r3.y};
 }
 
+// Byte N of a word, signed, as a number: one instruction (the compiler's own
+// choice for the odd bytes is a shift and a conversion).
+#define MOE_BYTE_VALUE(N)                                                                                          \
+  asm("v_cvt_f32_i32_sdwa %0, sext(%1) dst_sel:DWORD dst_unused:UNUSED_PAD src0_sel:BYTE_" #N : "=v"(v[N]) : "v"(w))
+__device__ __forceinline__ void byte_values(uint32_t w, float (&v)[4]) {
+  MOE_BYTE_VALUE(0);
+  MOE_BYTE_VALUE(1);
+  MOE_BYTE_VALUE(2);
+  MOE_BYTE_VALUE(3);
+}
+#undef MOE_BYTE_VALUE
 __device__ __forceinline__ bf16x8 whole8(uint32_t a, uint32_t b) {  // eight whole numbers
-  bf16x8 o;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    o[i] = static_cast<__bf16>(static_cast<float>(static_cast<int8_t>(a >> (8 * i))));
-    o[4 + i] = static_cast<__bf16>(static_cast<float>(static_cast<int8_t>(b >> (8 * i))));
-  }
-  return o;
+  float u[4], v[4];
+  byte_values(a, u);
+  byte_values(b, v);
+  const u32x4 o{pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  return __builtin_bit_cast(bf16x8, o);
 }
 
 __device__ __forceinline__ void put_w(char* lds, const u32x4 (&w)[2]) {
@@ -543,9 +552,9 @@ struct Claims {
   uint32_t ticket;   // lane 0: its answer
   uint32_t seen;     // lane l: counter l at that time
 
-  static __device__ __forceinline__ uint32_t add(uint32_t* c) {
+  static __device__ __forceinline__ uint32_t add(uint32_t* c, uint32_t n = 1) {
     uint32_t v = 0;
-    if (threadIdx.x % kWave == 0) v = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (threadIdx.x % kWave == 0) v = __hip_atomic_fetch_add(c, n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     return v;
   }
   static __device__ __forceinline__ int size(int n, int list) { return (n - list + kLists - 1) / kLists; }
@@ -594,8 +603,10 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
   // wavefronts. Two share a unit's end and its barrier, at twice the loads of
   // token rows (us, one / two: 64 tokens in bf16 266 / 259, 33 in E4M3 184 / 174
   // at 128 experts, k = 8); not for a few units (1 token, E4M3: 34 / 43), nor
-  // where the token rows are many (64 tokens, 8 experts, k = 2: 58 / 83).
-  constexpr int GW = TILES > 1 && XR == 8 ? 2 : 1, GC = kGC * GW, KW = kNW / GW;
+  // where the token rows are many (64 tokens, 8 experts, k = 2: 58 / 83). Whole
+  // numbers take four (us, two / four: 17 tokens 138 / 136, 33 174 / 169, 64 200 /
+  // 195): half as many steps a unit as bf16, and no scales with each.
+  constexpr int GW = TILES > 1 && XR == 8 ? (FMT == kI8 ? 4 : 2) : 1, GC = kGC * GW, KW = kNW / GW;
   constexpr int kBatchLoads = NB * (2 + XN);
   __shared__ FewLists L;
   __shared__ __attribute__((aligned(16))) FewScratch<TILES> S;
@@ -731,7 +742,8 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
   };
   // A unit's end: the partial sums to LDS; wavefront t then sums row tile t,
   // in wavefront order, two columns of a row per lane.
-  uint32_t* pending = nullptr;  // counter of a tile whose stores may still be under way
+  uint32_t* pending = nullptr;  // counter of tiles whose stores may still be under way, and their number
+  uint32_t pending_tiles = 0;
   int turn = 0;
   auto finish = [&](auto setc, int u) __attribute__((always_inline)) {
     constexpr int B = decltype(setc)::value;  // the unit's last batch
@@ -740,15 +752,15 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
       asm volatile("" ::: "memory");
       __builtin_amdgcn_s_waitcnt(0x0F70 | (kBatchLoads & 15) | (kBatchLoads >> 4) << 14);  // vmcnt(kBatchLoads)
       asm volatile("" ::: "memory");
-      Claims::add(pending);
+      Claims::add(pending, pending_tiles);
       pending = nullptr;
     }
 #pragma unroll
     for (int t = 0; t < TILES; ++t)
       if (t < tiles) *reinterpret_cast<f32x4*>(&S.red[turn][t][wave][col][4 * g]) = acc[t];
     lds_barrier();
-    if (kw < tiles) {
-      const int t = kw < TILES ? kw : 0, row = lane / 4, c0 = 2 * (lane % 4);
+    for (int t = kw; t < tiles && t < TILES; t += KW) {
+      const int row = lane / 4, c0 = 2 * (lane % 4);
       float2 vg = make_float2(0.0f, 0.0f), vu = vg;
 #pragma unroll
       for (int v = 0; v < KW; ++v) {
@@ -772,6 +784,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
                            pack_bf16x2(pw * (vg.x * sigmoidf_dev(vg.x) * vu.x), pw * (vg.y * sigmoidf_dev(vg.y) * vu.y)),
                            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
+      pending_tiles = pending != nullptr ? pending_tiles + 1 : 1;
       pending = P.cnt + (kLists + a / size) * kLine;
     }
     turn ^= 1;
@@ -820,7 +833,7 @@ __global__ __launch_bounds__(kThreads, 2) void few_kernel(const FewParams P) {
     }
     if (pending != nullptr) {  // before this workgroup waits for others
       stores_done();
-      Claims::add(pending);
+      Claims::add(pending, pending_tiles);
     }
   }
 
