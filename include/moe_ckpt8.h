@@ -48,8 +48,9 @@ moe_status moe_dequantize_ckpt8(int32_t rows, int32_t K, const int8_t* q, const 
 /* moe_gemm_gate_up (x_rows = x_perm, row_token NULL) or moe_gemm_gate_up_gathered
  * (x_rows = x [T,H], sorted row p read as row row_token[p]) that keeps g and u in 8
  * bits: gq, uq [T*k,I] and g_scale, u_scale [T*k,I/64], from the fp32 sums; a
- * [T*k,I] as there. bf16 only (MOE_EUNSUPPORTED otherwise); the limits of
- * moe_gemm_gate_up_gathered with row_token. */
+ * [T*k,I] as there. bf16 only, I*H*2 < 2^31, H and I below 2^22
+ * (MOE_EUNSUPPORTED otherwise); the limits of moe_gemm_gate_up_gathered with
+ * row_token. */
 moe_status moe_gemm_gate_up_ckpt8(moe_shape s, const void* x_rows, const int32_t* row_token, const int32_t* offsets,
                                   const void* w_gate, const void* w_up, int8_t* gq, float* g_scale, int8_t* uq,
                                   float* u_scale, void* a, hipStream_t stream);
@@ -62,8 +63,8 @@ moe_status moe_gemm_gate_up_ckpt8(moe_shape s, const void* x_rows, const int32_t
  *   a_w[p] = w a                                         (bf16 [T*k,I], for moe_gemm_down_wgrad_dy)
  *   d_topk_w[sorted_to_flat[p]] = <dA, a>                (f32 [T,k])
  * Workspace: ws of ws_bytes >= moe_ckpt8_workspace_bytes(s) (0 for a shape this
- * call rejects; moe_workspace_bytes(s) covers it). bf16 only and T*H*2 < 2^31
- * (MOE_EUNSUPPORTED otherwise). */
+ * call rejects; moe_workspace_bytes(s) covers it). bf16 only, T*H*2 and I*H*2
+ * below 2^31, H and I below 2^22 (MOE_EUNSUPPORTED otherwise). */
 size_t moe_ckpt8_workspace_bytes(moe_shape s);
 moe_status moe_gemm_down_dgrad_ckpt8(moe_shape s, const void* dy, const int32_t* row_token, const float* row_weight,
                                      const int32_t* sorted_to_flat, const int32_t* offsets, const void* w_down,

@@ -567,6 +567,12 @@ moe_status check_ckpt8_shape(const moe_shape& s) {
   if (st != MOE_OK) return st;
   return s.dtype != MOE_BF16 || !gathered_x_fits(s) ? MOE_EUNSUPPORTED : MOE_OK;
 }
+
+// One expert's weight, and a tile's rows (512 H bytes of x_perm, 512 I of dgu or a),
+// are addressed with 32-bit byte offsets.
+bool ckpt8_tile_fits(const moe_shape& s) {
+  return 2 * static_cast<int64_t>(s.I) * s.H < k2G && 512 * static_cast<int64_t>(std::max(s.I, s.H)) < k2G;
+}
 }  // namespace
 
 moe_status moe_quantize_ckpt8(int32_t rows, int32_t K, const void* in, int8_t* q, float* scale, hipStream_t stream) {
@@ -592,18 +598,19 @@ moe_status moe_gemm_gate_up_ckpt8(moe_shape s, const void* x_rows, const int32_t
   if (any_null(x_rows, offsets, w_gate, w_up, gq, g_scale, uq, u_scale, a)) return MOE_EINVAL;
   if (misaligned(x_rows, w_gate, w_up, gq, uq, a)) return MOE_EINVAL;
   if (s.dtype != MOE_BF16 || (row_token != nullptr && !gathered_x_fits(s))) return MOE_EUNSUPPORTED;
-  moe::GemmArgs g{};
+  if (!ckpt8_tile_fits(s)) return MOE_EUNSUPPORTED;
+  moe::Ckpt8Args g{};
   g.offsets = offsets;
-  g.a = x_rows;
   g.row_token = row_token;
-  g.b0 = w_gate;
-  g.b1 = w_up;
+  g.in = x_rows;
+  g.w0 = w_gate;
+  g.w1 = w_up;
   g.gq = gq;
   g.gs = g_scale;
   g.uq = uq;
   g.us = u_scale;
-  g.out2 = a;
-  return from_hip(moe::launch_gemm(moe::GEMM_GATEUP, s, g, stream));
+  g.a_out = a;
+  return from_hip(moe::launch_gate_up_ckpt8(s, g, stream));
 }
 
 size_t moe_ckpt8_workspace_bytes(moe_shape s) { return check_ckpt8_shape(s) != MOE_OK ? 0 : ckpt8_dots_bytes(s); }
@@ -619,22 +626,24 @@ moe_status moe_gemm_down_dgrad_ckpt8(moe_shape s, const void* dy, const int32_t*
                ws))
     return MOE_EINVAL;
   if (misaligned(dy, w_down, gq, uq, dgu, a_w, ws)) return MOE_EINVAL;
+  if (!ckpt8_tile_fits(s)) return MOE_EUNSUPPORTED;
   if (ws_bytes < ckpt8_dots_bytes(s)) return MOE_EWORKSPACE;
-  moe::GemmArgs g{};
+  moe::Ckpt8Args g{};
   g.offsets = offsets;
-  g.a = dy;
   g.row_token = row_token;
-  g.row_weight = row_weight;
-  g.b0 = w_down;
+  g.in = dy;
+  g.w0 = w_down;
   g.gq = const_cast<int8_t*>(gq);
   g.gs = const_cast<float*>(g_scale);
   g.uq = const_cast<int8_t*>(uq);
   g.us = const_cast<float*>(u_scale);
-  g.out0 = dgu;
-  g.out1 = a_w;
+  g.a_out = a_w;
+  g.row_weight = row_weight;
+  g.sorted_to_flat = sorted_to_flat;
+  g.dgu = dgu;
   g.dot = static_cast<float*>(ws);
-  if ((st = from_hip(moe::launch_gemm(moe::GEMM_DGRAD_DOWN, s, g, stream))) != MOE_OK) return st;
-  return from_hip(moe::launch_ckpt8_dots(s.T * s.k, moe::ceil_div(s.I, 128), g.dot, sorted_to_flat, d_topk_w, stream));
+  g.d_topk_w = d_topk_w;
+  return from_hip(moe::launch_down_dgrad_ckpt8(s, g, stream));
 }
 
 moe_status moe_gemm_down_wgrad_dy(moe_shape s, const void* dy, const int32_t* row_token, const void* a_w,

@@ -130,12 +130,10 @@ struct Params {
   const bf16_t* bx0;
   const bf16_t* bx1;
   int kx, kxr, kxp;
-  // Q8 instances: G and U as 8-bit codes [M][I] with a scale per 64 columns,
-  // written by GATEUP (with out2 = a), read by DGRAD_DOWN, which also writes
-  // a_w (out1) and the rows' <dA, a> over 128 columns (dot [M][ceil(I/128)]).
+  // Q8 instances (GATEUP): G and U as 8-bit codes [M][I] with a scale per 64
+  // columns, beside out2 = a.
   int8_t *gq, *uq;
   float *gs, *us;
-  float* dot;
 };
 
 typedef short v4i16 __attribute__((ext_vector_type(4)));
@@ -310,19 +308,12 @@ __device__ __forceinline__ void pair_cols8(const float (&t0)[4], const float (&t
 }
 
 // Over the eight lanes that hold one row's 64 columns (lane bits 2 to 4), in
-// every one of them.
-template <class OP>
-__device__ __forceinline__ float row8(float v, OP op) {
-  v = op(v, __uint_as_float(swap4(__float_as_uint(v))));
-  v = op(v, __uint_as_float(dpp32<0x128>(__float_as_uint(v))));  // 8 on in each row of 16
+// every one of them; NaN if one is.
+__device__ __forceinline__ float row8_max(float v) {
+  v = __builtin_elementwise_maximum(v, __uint_as_float(swap4(__float_as_uint(v))));
+  v = __builtin_elementwise_maximum(v, __uint_as_float(dpp32<0x128>(__float_as_uint(v))));  // 8 on in each row of 16
   const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-  return op(__uint_as_float(p[0]), __uint_as_float(p[1]));
-}
-__device__ __forceinline__ float row8_max(float v) {  // NaN if one is
-  return row8(v, [](float a, float b) { return __builtin_elementwise_maximum(a, b); });
-}
-__device__ __forceinline__ float row8_sum(float v) {
-  return row8(v, [](float a, float b) { return a + b; });
+  return __builtin_elementwise_maximum(__uint_as_float(p[0]), __uint_as_float(p[1]));
 }
 
 // Eight values of a row as codes, and the scale of its 64 columns: t0 and t1 as
@@ -333,16 +324,13 @@ __device__ __forceinline__ u32x2 codes64(const float (&t0)[4], const float (&t1)
 #pragma unroll
   for (int q = 0; q < 4; ++q)
     m = __builtin_elementwise_maximum(m, __builtin_elementwise_maximum(fabsf(t0[q]), fabsf(t1[q])));
-  m = row8_max(m);
-  const bool finite = m < __builtin_inff();
-  const float up = m < 0x1p-64f ? 0x1p64f : 1.0f;  // 127 / m stays finite
-  const float r = finite && m > 0.0f ? 127.0f * __builtin_amdgcn_rcpf(m * up) : 0.0f;
-  scale = finite ? m * (1.0f / 127.0f) : __builtin_nanf("");
+  const SumFactor f(row8_max(m));
+  scale = f.scale;
   uint32_t c[8];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
-    c[q] = code_bits(t0[q] * up * r);
-    c[4 + q] = code_bits(t1[q] * up * r);
+    c[q] = f.code(t0[q]);
+    c[4 + q] = f.code(t1[q]);
   }
   const uint32_t w0 = bytes4(c[0], c[1], c[2], c[3]), w1 = bytes4(c[4], c[5], c[6], c[7]);
   const bool hi = (lane & 4) != 0;
@@ -433,8 +421,8 @@ __device__ __forceinline__ void gemm_tiles(const Params& P, const int bid, const
   static_assert(!KX || (!F8 && !AW && !grouped_k(MODE) && (!FUSED || MODE == GATEUP || MODE == DGRAD_DOWN)),
                 "extended K: the bf16 forward and data-gradient GEMMs (gate/up and down dgrad also with gathered rows)");
   static_assert(!AW || (MODE == GATEUP && !F8), "a_w: the gate/up GEMM of the training step");
-  static_assert(!Q8 || (!F8 && !AW && !KX && (MODE == GATEUP || (MODE == DGRAD_DOWN && FUSED))),
-                "G and U in 8 bits: gate/up, and the down data gradient that reads dy");
+  static_assert(!Q8 || (!F8 && !AW && !KX && MODE == GATEUP),
+                "G and U in 8 bits: gate/up");
   // Element size in bytes, elements per k-step (64 bytes of a k-major row
   // either way) and per 16-byte chunk.
   constexpr int ESZ = F8 ? 1 : 2;
@@ -1381,8 +1369,8 @@ __device__ __forceinline__ void gemm_tiles(const Params& P, const int bid, const
       // dA -> dG = dA U silu'(G), dU = dA silu(G), with the saved G and U of
       // the same rows; written side by side as [dG | dU] (row length 2I).
       const int64_t base = static_cast<int64_t>(trow0) * I;
-      const rsrc_t rg = make_rsrc(Q8 ? static_cast<const void*>(P.gq + base) : P.g_in + base, (Q8 ? 1 : 2) * tmvalid * I);
-      const rsrc_t ru = make_rsrc(Q8 ? static_cast<const void*>(P.uq + base) : P.u_in + base, (Q8 ? 1 : 2) * tmvalid * I);
+      const rsrc_t rg = make_rsrc(P.g_in + base, 2 * tmvalid * I);
+      const rsrc_t ru = make_rsrc(P.u_in + base, 2 * tmvalid * I);
       const rsrc_t ro = make_rsrc(P.out0 + 2 * base, 4 * tmvalid * I);
       // 16-byte lanes (pair_cols8): lane l handles row 8b + 4(l/32) + l%4 of
       // the row block, columns 32*((l/4)%2) + 8*((l%32)/8) .. + 7 of the
@@ -1394,14 +1382,7 @@ __device__ __forceinline__ void gemm_tiles(const Params& P, const int bid, const
       // FUSED (dy read through row_token): dA row p is scaled by
       // row_weight[p] in fp32 first; the weights travel with G and U.
       const rsrc_t rwr = make_rsrc(P.row_weight + (FUSED ? trow0 : 0), FUSED ? 4 * tmvalid : 0);
-      // Q8: G and U from their codes (a 64-column pair jp is one block), a_w and
-      // the rows' dots as well.
-      const int nblk = I / kCkptBlock, ndot = (I + 127) / 128;
-      const rsrc_t rgs = make_rsrc(Q8 ? P.gs + static_cast<int64_t>(trow0) * nblk : nullptr, Q8 ? 4 * tmvalid * nblk : 0);
-      const rsrc_t rus = make_rsrc(Q8 ? P.us + static_cast<int64_t>(trow0) * nblk : nullptr, Q8 ? 4 * tmvalid * nblk : 0);
-      const rsrc_t raw = make_rsrc(Q8 ? P.out1 + base : nullptr, Q8 ? 2 * tmvalid * I : 0);
-      const rsrc_t rdt = make_rsrc(Q8 ? P.dot + static_cast<int64_t>(trow0) * ndot : nullptr, Q8 ? 4 * tmvalid * ndot : 0);
-      typedef u32x4 GU[FN / 2][4];  // Q8: codes in .xy, the scale in .z
+      typedef u32x4 GU[FN / 2][4];
       float rwb[2][4];
       auto load_gu = [&](int i, GU& gb, GU& ub) __attribute__((always_inline)) {
         if constexpr (FUSED) {
@@ -1416,14 +1397,6 @@ __device__ __forceinline__ void gemm_tiles(const Params& P, const int bid, const
           for (int b = 0; b < 4; ++b) {
             const int r = wm * WTM + i * 32 + 8 * b + hrow;
             const int n = tn0 + wn * WTN + jp * 64 + ncol8;
-            if constexpr (Q8) {
-              const uint32_t off = n < I ? static_cast<uint32_t>(r * I + n) : kNoWrite;
-              const uint32_t so = n < I ? 4u * static_cast<uint32_t>(r * nblk + n / kCkptBlock) : kNoWrite;
-              const u32x2 gw = load_b64(rg, off), uw = load_b64(ru, off);
-              gb[jp][b] = u32x4{gw.x, gw.y, __builtin_amdgcn_raw_buffer_load_b32(rgs, so, 0, 0), 0};
-              ub[jp][b] = u32x4{uw.x, uw.y, __builtin_amdgcn_raw_buffer_load_b32(rus, so, 0, 0), 0};
-              continue;
-            }
             const uint32_t off = n < I ? 2u * static_cast<uint32_t>(r * I + n) : kNoWrite;
             gb[jp][b] = load_b128(rg, off);
             ub[jp][b] = load_b128(ru, off);
@@ -1437,7 +1410,6 @@ __device__ __forceinline__ void gemm_tiles(const Params& P, const int bid, const
         if (i + 1 < FM && i + 1 < nbm) load_gu(i + 1, gb[(i + 1) & 1], ub[(i + 1) & 1]);
         const GU& gc = gb[i & 1];
         const GU& uc = ub[i & 1];
-        float dot[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int jp = 0; jp < FN / 2; ++jp)
 #pragma unroll
@@ -1452,33 +1424,6 @@ __device__ __forceinline__ void gemm_tiles(const Params& P, const int bid, const
               quad_transpose(da[j], lane);
             }
             pair_cols8(da[0], da[1], lane, d8);
-            if constexpr (Q8) {
-              const u32x4 gw = gc[jp][b], uw = uc[jp][b];
-              const float sg = __uint_as_float(gw.z), su = __uint_as_float(uw.z), w = rwb[i & 1][b];
-              float dg[8], du[8], aw[8], sum = 0.0f;
-#pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                const float gv = code_value(q < 4 ? gw.x : gw.y, q & 3) * sg;
-                const float uv = code_value(q < 4 ? uw.x : uw.y, q & 3) * su;
-                const float s = sigmoid_fast(gv), silu = gv * s, a = silu * uv;
-                sum = fmaf(d8[q], a, sum);
-                aw[q] = w * a;
-                const float d = w * d8[q];
-                dg[q] = d * uv * s * (1.0f + gv * (1.0f - s));
-                du[q] = d * silu;
-              }
-              dot[b] += n < I ? sum : 0.0f;  // past the end d8 is another column's
-              const uint32_t to = n < I ? 2u * static_cast<uint32_t>(r * I + n) : kNoWrite;
-              const uint32_t off = n < I ? 2u * static_cast<uint32_t>(r * 2 * I + n) : kNoWrite;
-              auto pack = [](const float (&v)[8]) {
-                return u32x4{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                             pack_bf16x2(v[6], v[7])};
-              };
-              store_b128(pack(dg), ro, off);
-              store_b128(pack(du), ro, off == kNoWrite ? kNoWrite : off + 2u * I);
-              store_b128(pack(aw), raw, to);
-              continue;
-            }
             if constexpr (FUSED) {
 #pragma unroll
               for (int q = 0; q < 8; ++q) d8[q] *= rwb[i & 1][b];
@@ -1504,15 +1449,6 @@ __device__ __forceinline__ void gemm_tiles(const Params& P, const int bid, const
             store_b128(u32x4{dgp[0], dgp[1], dgp[2], dgp[3]}, ro, off);
             store_b128(u32x4{dup[0], dup[1], dup[2], dup[3]}, ro, off == kNoWrite ? kNoWrite : off + 2u * I);
           }
-        if constexpr (Q8) {
-#pragma unroll
-          for (int b = 0; b < 4; ++b) {
-            const int r = wm * WTM + i * 32 + 8 * b + hrow, c = tn0 + wn * WTN;
-            __builtin_amdgcn_raw_buffer_store_b32(
-                __float_as_uint(row8_sum(dot[b])), rdt,
-                c < I && (lane & 28) == 0 ? 4u * static_cast<uint32_t>(r * ndot + c / 128) : kNoWrite, 0, 0);
-          }
-        }
       }
     } else {
       // fp32 weight gradient of expert te, rows m0.., columns n0..; a 32-row
@@ -1846,7 +1782,6 @@ Params make_params(const moe_shape& s, const GemmArgs& g) {
   p.uq = g.uq;
   p.gs = g.gs;
   p.us = g.us;
-  p.dot = g.dot;
   return p;
 }
 
@@ -1885,7 +1820,6 @@ hipError_t launch_gemm_bf16(GemmMode mode, const moe_shape& s, const GemmArgs& g
       if (g.a_scale) return g.row_weight ? run<DOWN, true, true>(p, st) : hipErrorInvalidValue;
       return g.row_weight ? run<DOWN, true>(p, st) : run<DOWN>(p, st);
     case GEMM_DGRAD_DOWN:
-      if (g.gq) return g.row_token ? run<DGRAD_DOWN, true, false, false, false, false, true>(p, st) : hipErrorInvalidValue;
       if (g.kx > 0)
         return g.row_token ? run<DGRAD_DOWN, true, false, false, false, true>(p, st)
                            : run<DGRAD_DOWN, false, false, false, false, true>(p, st);
@@ -1911,29 +1845,6 @@ hipError_t launch_gemm_pair_bf16(GemmMode ma, GemmMode mb, const moe_shape& s, c
     return gb.row_token ? run_pair<DGRAD_GATEUP, WGRAD_GATEUP, false, true>(pa, pb, st)
                         : run_pair<DGRAD_GATEUP, WGRAD_GATEUP>(pa, pb, st);
   return hipErrorInvalidValue;
-}
-
-}  // namespace moe
-
-namespace moe {
-namespace {
-
-// d_topk_w of each (token, slot): its row's dots in column order.
-__global__ __launch_bounds__(256) void ckpt8_dots_kernel(int M, int n, const float* __restrict__ dot,
-                                                         const int32_t* __restrict__ sorted_to_flat,
-                                                         float* __restrict__ out) {
-  const int p = blockIdx.x * 256 + threadIdx.x;
-  if (p >= M) return;
-  float v = 0.0f;
-  for (int i = 0; i < n; ++i) v += dot[static_cast<int64_t>(p) * n + i];
-  out[sorted_to_flat[p]] = v;
-}
-
-}  // namespace
-
-hipError_t launch_ckpt8_dots(int M, int n, const float* dot, const int32_t* sorted_to_flat, float* out, hipStream_t st) {
-  ckpt8_dots_kernel<<<static_cast<unsigned>(ceil_div64(M, 256)), 256, 0, st>>>(M, n, dot, sorted_to_flat, out);
-  return hipGetLastError();
 }
 
 }  // namespace moe

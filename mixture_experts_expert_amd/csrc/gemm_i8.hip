@@ -7,15 +7,18 @@
 // core's int32 accumulators (v_mfma_i32_16x16x64_i8). The scales multiply the
 // finished sums, so nothing but products, LDS reads and loads is in the loop.
 //
-// Two kernels:
+// Three kernels (launch says which):
 //
-// i8_tile_kernel: a persistent workgroup of 8 wavefronts on BM x 256 tiles, 2 x 4
-// wavefronts of BM/2 x 64. Operands go from memory straight into LDS, two
-// stages of one 128-wide k-step in halves that are refilled as soon as they
-// are read (see there). A row's 128 bytes are eight 16-byte chunks,
-// XOR-swizzled by row so that a 16-lane read touches every bank once. Which
-// weight row sits at which LDS row is chosen so that a lane ends with 8
-// consecutive output columns.
+// i8_tile_kernel, the plain product of many rows: a persistent workgroup of 8
+// wavefronts per CU on 256 x 256 tiles, 2 x 4 wavefronts of 128 x 64. Operands go
+// from memory straight into LDS, two stages of one 128-wide k-step in halves that
+// are refilled as soon as they are read (see there). A row's 128 bytes are eight
+// 16-byte chunks, XOR-swizzled by row so that a 16-lane read touches every bank
+// once. Which weight row sits at which LDS row is chosen so that a lane ends with
+// 8 consecutive output columns.
+//
+// i8_duo_kernel, everything between: two workgroups per CU on 128 x 256 tiles
+// (duo.h), gate/up and down.
 //
 // i8_stream_kernel, for a few rows: bound by the weights' bytes or by latency.
 // Weights go from memory into registers steps ahead; with few workgroups of
@@ -32,6 +35,7 @@
 // 0.0019 (192 tokens, 30B shape); bf16 in between would move a tenth of them.
 #include <type_traits>
 
+#include "duo.h"
 #include "shared8.h"
 
 namespace moe {
@@ -252,8 +256,8 @@ __global__ __launch_bounds__(kThreads, 2) void i8_tile_kernel(const Params P) {
     const uint32_t to = weights ? boff[i & 3] : aoff[(h * HA + i) % (2 * HA)];
     const int c = (lane_id & 7) ^ (lane_id >> 4) ^ ((blk & 1) * 4);
     const uint32_t off = c * 16 < (!live ? 0 : s == steps - 1 ? tail : KS) ? to : kOutside;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(weights ? rb : ra, (lds_ptr)((weights ? W : S) + blk * 1024), 16, off, s * KS,
-                                             0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(weights ? rb : ra, (lds_ptr)((weights ? W : S) + blk * 1024), 16, off,
+                                             min(s, steps - 1) * KS, 0, 0);
   };
   // All but the last PENDING memory instructions are done, and every wavefront is here.
   auto landed = [&](auto pending) __attribute__((always_inline)) {
@@ -418,259 +422,66 @@ __global__ __launch_bounds__(kThreads, 2) void i8_tile_kernel(const Params P) {
   landed(none{});  // nothing is on its way into LDS when the workgroup ends
 }
 
-// ---- many rows per expert, two workgroups per CU ------------------------------
+// ---- up to some hundred rows per expert: two workgroups per CU (duo.h) ----------
 
-constexpr int kW4 = 256;   // threads of i8_wide_kernel
-constexpr int KW = 64;     // its k per step
-constexpr int kRing = 3;   // stages of LDS; loads run two steps ahead
+struct DuoParams : duo::Base {
+  const float *sa, *sw0, *sw1;
+  const float* row_weight;
+  bf16_t* out;
+  int16_t* v16;
+  uint8_t* v8;
+  float* amax;
+};
 
-template <bool GU, bool S8 = false>
-__global__ __attribute__((amdgpu_flat_work_group_size(kW4, kW4), amdgpu_waves_per_eu(2, 2))) void i8_duo_kernel(
-    const Params P) {
-  constexpr int BM = 128, TN = GU ? BN / 2 : BN;
-  constexpr int FM = 4, FN = 8;       // 16-row tiles of a and of the weights per wavefront
-  constexpr int SA = BM * KW, STAGE = SA + BN * KW;
-  constexpr int LA = 2, LOADS = LA + 4;  // per wavefront and step: 2 of a's rows, 4 of the weights'
-  constexpr int STORES = GU ? 5 * FM : 4 * FM;
-  __shared__ __attribute__((aligned(1024))) uint8_t lds0[STAGE];
-  __shared__ __attribute__((aligned(1024))) uint8_t lds1[STAGE];
-  __shared__ __attribute__((aligned(1024))) uint8_t lds2[STAGE];
-  __shared__ int tstart[1025];
-  __shared__ int wsum[kW4 / kWave];
-  __shared__ float amax[GU ? BM : 1][2];
-  __shared__ __attribute__((aligned(256))) int per_row[BM];        // GU: the next tile's tokens, else this one's weights
-  __shared__ __attribute__((aligned(256))) float scale[BN + BN];   // this tile's scales: rows, columns
+// GU: gate/up with silu(g) u in 24 bits; else the plain product, S8 in shared8.h's
+// form. The extras: scales of 256 rows and 256 columns, then the rows' weights, or
+// their maxima over each wavefront's columns.
+template <bool GU, bool S8>
+struct I8Op {
+  typedef DuoParams Params;
+  typedef const __attribute__((address_space(4))) Params* args_t;
+  typedef i32x4 Acc;
+  static constexpr bool PAIRED = GU, GATHER = GU, KROWS = false;
+  static constexpr int STORES = (GU ? 5 : 4) * duo::FM;
+  static constexpr int EXTRA = 4 * (2 * duo::BN + (GU ? 2 * duo::BM : duo::BM));
 
-  const int tid = threadIdx.x;
-  const int lane_id = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 1, wn = wave & 1;
-  const int E = P.E, K = P.K;
-  {  // tstart[e]: row tiles of the experts before e (four experts per thread)
-    int c[4], mine = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = 4 * tid + i;
-      const int b = e < E && P.offsets ? P.offsets[e] : 0;
-      const int t = e < E ? (P.offsets ? P.offsets[e + 1] : P.M) : 0;
-      c[i] = e < E ? (t - b + BM - 1) / BM : 0;
-      mine += c[i];
-    }
-    int incl = mine;
-#pragma unroll
-    for (int o = 1; o < kWave; o <<= 1) {
-      const int v = __shfl_up(incl, o, kWave);
-      if (lane_id >= o) incl += v;
-    }
-    if (lane_id == kWave - 1) wsum[wave] = incl;
-    __syncthreads();
-    int at = incl - mine;
-    for (int w = 0; w < wave; ++w) at += wsum[w];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (4 * tid + i < E) tstart[4 * tid + i] = at;
-      at += c[i];
-    }
-    if (tid == kW4 - 1) tstart[E] = at;
-    __syncthreads();
-  }
-  const int ntn = (P.N + TN - 1) / TN;
-  const int total = tstart[E] * ntn;
-  const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3, nslots = gridDim.x >> 3;
-  const int lo = static_cast<int>(static_cast<int64_t>(total) * xcd / 8);
-  const int hi = static_cast<int>(static_cast<int64_t>(total) * (xcd + 1) / 8);
-  const int steps = (K + KW - 1) / KW, padded = (steps + kRing - 1) / kRing * kRing;
-  int L = lo + slot;
-  if (L >= hi) return;
+  static __device__ __forceinline__ Acc product(const u32x4& w, const u32x4& a, const Acc& c) { return product64(w, a, c); }
 
-  auto args = [&]() __attribute__((always_inline)) {
-    uintptr_t u = reinterpret_cast<uintptr_t>(__builtin_amdgcn_kernarg_segment_ptr());
-    asm volatile("" : "+s"(u));
-    return reinterpret_cast<const __attribute__((address_space(4))) Params*>(u);
-  };
-  struct Tile {
-    int e, row0, valid, n0;
-  };
-  auto find = [&](int at) __attribute__((always_inline)) {
-    int l = 0, h = E - 1;
-    while (l < h) {
-      const int mid = (l + h + 1) >> 1;
-      if (tstart[mid] * ntn <= at) l = mid; else h = mid - 1;
-    }
-    const int rem = at - tstart[l] * ntn, mte = tstart[l + 1] - tstart[l];
-    const int band = rem / (kBand * ntn), bm = min(kBand, mte - band * kBand);
-    const int nt = (rem - band * kBand * ntn) / bm, mt = band * kBand + rem - band * kBand * ntn - nt * bm;
-    Tile t;
-    t.e = __builtin_amdgcn_readfirstlane(l);
-    const int32_t* off = args()->offsets;
-    const int begin = off ? off[t.e] : 0, end = off ? off[t.e + 1] : args()->M;
-    t.row0 = __builtin_amdgcn_readfirstlane(begin + mt * BM);
-    t.valid = __builtin_amdgcn_readfirstlane(min(BM, end - begin - mt * BM));
-    t.n0 = __builtin_amdgcn_readfirstlane(nt * TN);
-    return t;
-  };
-  // LDS row r of a stage is 64 bytes, chunk c at (c ^ (r >> 2 & 3)): 16 rows of one
-  // chunk touch every bank once. Row r of a: the tile's row r. Row r of the
-  // weights: columns in such an order that a lane's results are 8 neighbours.
-  rsrc_t ra, rb;
-  uint32_t aoff[LA], boff[4];
-  auto aim = [&](const Tile& t) __attribute__((always_inline)) {
-    const auto* A = args();
-    int lane = lane_id;
-    asm volatile("" : "+v"(lane));
-    const int64_t first = GU ? 0 : t.row0, rows = GU ? A->arows : t.valid;
-    ra = make_rsrc(A->a + first * K, rows * K);
-    rb = make_rsrc((GU && (wave & 1) ? A->w1 : A->w0) + static_cast<int64_t>(t.e) * A->N * K, static_cast<int64_t>(A->N) * K);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = (wave * 4 + i) * 16 + (lane >> 2);
-      const int c = (lane & 3) ^ ((r >> 2) & 3);
-      if (i < LA) {
-        const int ar = (wave * LA + i) * 16 + (lane >> 2);
-        const int row = GU ? (ar < t.valid ? per_row[ar] : 0) : ar;
-        aoff[i] = ar < t.valid ? static_cast<uint32_t>(row) * K + c * 16 : kOutside;
-      }
-      const int j = (r >> 4) & (GU ? 3 : 7), q = r & 15;
-      const int n = t.n0 + (r >> 7) * (GU ? 64 : 128) + (j >> 1) * 32 + 8 * (q >> 2) + 4 * (j & 1) + (q & 3);
-      boff[i] = n < A->N ? static_cast<uint32_t>(n) * K + c * 16 : kOutside;
-    }
-  };
-  typedef __attribute__((address_space(3))) void* lds_ptr;
-  auto load = [&](int v, uint8_t* S, int s, int k) __attribute__((always_inline)) {
-    const bool weights = v < 4;
-    const int i = weights ? v : v - 4, blk = weights ? wave * 4 + i : wave * LA + i;
-    const int c = (lane_id & 3) ^ ((lane_id >> 4) & 3);  // of the lane's row: (r >> 2 & 3) = lane >> 4
-    const uint32_t to = weights ? boff[i & 3] : aoff[i % LA];
-    const uint32_t off = c * 16 < k ? to : kOutside;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(weights ? rb : ra, (lds_ptr)(S + (weights ? SA : 0) + blk * 1024), 16, off,
-                                             s * KW, 0, 0);
-  };
-  auto landed = [&](auto pending) __attribute__((always_inline)) {
-    constexpr int n = decltype(pending)::value;
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0070 | (n & 15) | (n >> 4) << 14);  // vmcnt(n) lgkmcnt(0)
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-  };
-  using none = std::integral_constant<int, 0>;
-  auto per_row_load = [&](const void* base, int row0, int valid) __attribute__((always_inline)) {
-    if (wave >= BM / 64) return;
-    const int r = wave * 64 + lane_id;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(static_cast<const char*>(base) + static_cast<int64_t>(row0) * 4,
-                                                       valid * 4),
-                                             (lds_ptr)(reinterpret_cast<char*>(per_row) + wave * 256), 4, r * 4, 0, 0, 0);
-  };
-  auto scale_load = [&](const Tile& t) __attribute__((always_inline)) {
-    const auto* A = args();
-    const int r = wave * 64 + lane_id;
+  static __device__ __forceinline__ void begin(args_t A, const duo::Tile& t, const int* per_row, char* extra, int wave,
+                                               int lane) {
+    const int r = wave * 64 + lane;
     const rsrc_t rr = make_rsrc(A->sa + (GU ? 0 : t.row0), (GU ? A->arows : t.valid) * 4ll);
-    const uint32_t off = r < t.valid ? static_cast<uint32_t>(GU ? per_row[r & (BM - 1)] : r) * 4 : kOutside;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rr, (lds_ptr)(reinterpret_cast<char*>(scale) + wave * 256), 4, off, 0, 0, 0);
+    duo::words_to_lds(rr, extra + wave * 256,
+                      r < t.valid ? static_cast<uint32_t>(GU ? per_row[r & (duo::BM - 1)] : r) * 4 : kOutside);
     const int n = t.n0 + (GU ? r & 127 : r);
     const rsrc_t rc = make_rsrc((GU && wave >= 2 ? A->sw1 : A->sw0) + static_cast<int64_t>(t.e) * A->N, A->N * 4ll);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rc, (lds_ptr)(reinterpret_cast<char*>(scale + BN) + wave * 256), 4,
-                                             n < A->N ? static_cast<uint32_t>(n) * 4 : kOutside, 0, 0, 0);
-  };
-
-  i32x4 acc[FM][FN];
-  u32x4 fa[2], fb[FN];
-  int fo;  // the lane's byte in a 16-row tile
-  {
-    const int q = lane_id & 15, g = lane_id >> 4;
-    fo = q * KW + ((g ^ ((q >> 2) & 3)) << 4);
+    duo::words_to_lds(rc, extra + 4 * duo::BN + wave * 256, n < A->N ? static_cast<uint32_t>(n) * 4 : kOutside);
+    if constexpr (!GU)
+      if (A->row_weight != nullptr && wave < duo::BM / kWave)
+        duo::words_to_lds(make_rsrc(A->row_weight + t.row0, t.valid * 4ll), extra + 8 * duo::BN + wave * 256, r * 4);
   }
-  // The wavefront's 16-row tile i is the tile's 2 i + wm: both halves of a short tile have rows.
-  auto read_a = [&](u32x4& to, const uint8_t* S, int i) __attribute__((always_inline)) {
-    to = *reinterpret_cast<const u32x4*>(S + (2 * i + wm) * (16 * KW) + fo);
-  };
-  auto read_b = [&](u32x4& to, const uint8_t* S, int j) __attribute__((always_inline)) {
-    to = *reinterpret_cast<const u32x4*>(S + SA + (wn * 8 + j) * (16 * KW) + fo);
-  };
-  // Step s on stage C, while the loads of step sn go out into stage D.
-  auto kstep = [&](auto nic, auto firstc, bool stores, const uint8_t* C, uint8_t* D, int sn, bool live,
-                   auto&& after) __attribute__((always_inline)) {
-    constexpr int NI = decltype(nic)::value;
-    constexpr bool first = decltype(firstc)::value != 0;
-    asm volatile("" ::: "memory");
-    if (stores) __builtin_amdgcn_s_waitcnt(0x0070 | ((LOADS + STORES) & 15) | ((LOADS + STORES) >> 4) << 14);
-    else __builtin_amdgcn_s_waitcnt(0x0070 | (LOADS & 15) | (LOADS >> 4) << 14);
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    after();
-    int k = min(K - sn * KW, live ? KW : 0);
-    asm volatile("" : "+s"(k));  // a select, not a branch
-    read_a(fa[0], C, 0);
-#pragma unroll
-    for (int j = 0; j < FN; ++j) read_b(fb[j], C, j);
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_setprio(1);  // products before the other workgroup's loads and results
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      if (i + 1 < NI) read_a(fa[(i + 1) & 1], C, i + 1);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int j = 0; j < FN; ++j) acc[i][j] = product64(fb[j], fa[i & 1], first ? i32x4{} : acc[i][j]);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int v = i * LOADS / NI; v < (i + 1) * LOADS / NI; ++v) load(v, D, sn, k);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    __builtin_amdgcn_s_setprio(0);
-    __builtin_amdgcn_sched_barrier(0);
-  };
 
-  Tile now = find(L), nx = now;
-  using zero = std::integral_constant<int, 0>;
-  using one = std::integral_constant<int, 1>;
-  auto tile = [&](auto nic) __attribute__((always_inline)) {
-    constexpr int NI = decltype(nic)::value;
-    const int next = L + nslots;
-    const bool more = next < hi;
-    auto nothing = [] {};
-    // Step s is read after its own barrier, at which all but step s + 1's loads
-    // (and the stores, if they are newer) have landed; step s + 2's go out then.
-    auto turn = [&]() __attribute__((always_inline)) {
-      if (more) {
-        if constexpr (!GU) nx = find(next);
-        if (GU && padded == kRing) landed(none{});  // the tokens were only just sent for
-        aim(nx);
-      }
+  template <int NI>
+  static __device__ __forceinline__ void finish(args_t A, Acc (&acc)[duo::FM][duo::FN], const duo::Tile& t, char* extra,
+                                                const duo::Where& w) {
+    constexpr int FM = duo::FM;
+    const int g = w.g, wn = w.wn, n0 = t.n0, valid = t.valid;
+    const float* scale = reinterpret_cast<const float*>(extra);
+    auto columns = [&](int at) __attribute__((always_inline)) {
+      return *reinterpret_cast<const f32x4*>(&scale[duo::BN + at]);
     };
-    kstep(nic, one{}, true, lds0, lds2, 2, 2 < steps, [&]() __attribute__((always_inline)) {
-      scale_load(now);
-      if constexpr (GU) {
-        if (more) {
-          nx = find(next);
-          per_row_load(args()->row_token, nx.row0, nx.valid);
-        }
-      } else if (const float* w = args()->row_weight; w != nullptr) {
-        per_row_load(w, now.row0, now.valid);
-      }
-    });
-    for (int s = kRing; s < padded; s += kRing) {  // steps s - 2 .. s
-      kstep(nic, zero{}, s == kRing, lds1, lds0, s, s < steps, nothing);
-      kstep(nic, zero{}, false, lds2, lds1, s + 1, s + 1 < steps, nothing);
-      kstep(nic, zero{}, false, lds0, lds2, s + 2, s + 2 < steps, nothing);
-    }
-    kstep(nic, zero{}, padded == kRing, lds1, lds0, 0, more, turn);
-    kstep(nic, zero{}, false, lds2, lds1, 1, more && steps > 1, nothing);
-    // ---- epilogue; stores of rows and columns outside go out of range, so
-    // that their count is fixed: they run on under the next tile's first steps.
-    const auto* A = args();
-    const int lane = lane_id, g = lane >> 4, q = lane & 15;
-    const int row0 = now.row0, valid = now.valid, n0 = now.n0;
-    auto columns = [&](int at) __attribute__((always_inline)) { return *reinterpret_cast<const f32x4*>(&scale[BN + at]); };
+    f32x4 cs[8];
     if constexpr (GU) {
+      float(&amax)[duo::BM][2] = *reinterpret_cast<float(*)[duo::BM][2]>(extra + 8 * duo::BN);
       const int NT = (A->N + 127) / 128;
-      const rsrc_t rv = make_rsrc(A->v16 + static_cast<int64_t>(row0) * A->N, static_cast<int64_t>(valid) * A->N * 2);
-      const rsrc_t rl = make_rsrc(A->v8 + static_cast<int64_t>(row0) * A->N, static_cast<int64_t>(valid) * A->N);
-      const rsrc_t rm = make_rsrc(A->amax + static_cast<int64_t>(row0) * NT, static_cast<int64_t>(valid) * NT * 4);
-      f32x4 cs[8];
+      const rsrc_t rv = make_rsrc(A->v16 + static_cast<int64_t>(t.row0) * A->N, static_cast<int64_t>(valid) * A->N * 2);
+      const rsrc_t rl = make_rsrc(A->v8 + static_cast<int64_t>(t.row0) * A->N, static_cast<int64_t>(valid) * A->N);
+      const rsrc_t rm = make_rsrc(A->amax + static_cast<int64_t>(t.row0) * NT, static_cast<int64_t>(valid) * NT * 4);
 #pragma unroll
       for (int j = 0; j < 8; ++j) cs[j] = columns((j >> 2) * 128 + wn * 64 + ((j >> 1) & 1) * 32 + 8 * g + 4 * (j & 1));
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
-        const int r = (2 * i + wm) * 16 + q;
+        const int r = w.row(i);
         const float rs = scale[r];
         float m = 0.0f;
 #pragma unroll
@@ -692,7 +503,7 @@ __global__ __attribute__((amdgpu_flat_work_group_size(kW4, kW4), amdgpu_waves_pe
       asm volatile("" ::: "memory");
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
-        const int r = (2 * i + wm) * 16 + q;
+        const int r = w.row(i);
         const bool row = i < NI && r < valid;
         float m = 0.0f;
         if (i < NI) m = __builtin_elementwise_maximum(amax[r][0], amax[r][1]);
@@ -716,14 +527,13 @@ __global__ __attribute__((amdgpu_flat_work_group_size(kW4, kW4), amdgpu_waves_pe
             0);
       }
     } else {
-      const rsrc_t ro = make_rsrc(A->out + static_cast<int64_t>(row0) * A->N, static_cast<int64_t>(valid) * A->N * 2);
-      f32x4 cs[8];
+      const rsrc_t ro = make_rsrc(A->out + static_cast<int64_t>(t.row0) * A->N, static_cast<int64_t>(valid) * A->N * 2);
 #pragma unroll
       for (int j = 0; j < 8; ++j) cs[j] = columns(wn * 128 + (j >> 1) * 32 + 8 * g + 4 * (j & 1));
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
-        const int r = (2 * i + wm) * 16 + q;
-        const float rs = i < NI ? scale[r] * (A->row_weight != nullptr ? __int_as_float(per_row[r]) : 1.0f) : 0.0f;
+        const int r = w.row(i);
+        const float rs = i < NI ? scale[r] * (A->row_weight != nullptr ? scale[2 * duo::BN + r] : 1.0f) : 0.0f;
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           const int n = n0 + wn * 128 + 32 * h + 8 * g;
@@ -749,26 +559,12 @@ __global__ __attribute__((amdgpu_flat_work_group_size(kW4, kW4), amdgpu_waves_pe
         }
       }
     }
-    now = nx;
-    L = next;
-  };
+  }
+};
 
-  if constexpr (GU) {
-    per_row_load(P.row_token, now.row0, now.valid);
-    landed(none{});
-  }
-  aim(now);
-#pragma unroll
-  for (int v = 0; v < LOADS; ++v) load(v, lds0, 0, min(K, KW));
-#pragma unroll
-  for (int v = 0; v < LOADS; ++v) load(v, lds1, 1, min(K - KW, KW));
-  landed(none{});
-  while (L < hi) {
-    if (now.valid > 64) tile(std::integral_constant<int, 4>{});
-    else if (now.valid > 32) tile(std::integral_constant<int, 2>{});
-    else tile(std::integral_constant<int, 1>{});
-  }
-  landed(none{});  // nothing is on its way into LDS when the workgroup ends
+template <bool GU, bool S8>
+MOE_DUO_KERNEL void i8_duo_kernel(const DuoParams P) {
+  duo::run<I8Op<GU, S8>>(P);
 }
 
 // ---- few rows per expert ----------------------------------------------------
@@ -958,6 +754,22 @@ __global__ __launch_bounds__(kThreads, 2) void i8_stream_kernel(const Params P, 
   }
 }
 
+// Which kernel, in us:
+//   Few rows: the weights are read once whatever the tile, so what counts is how
+//   early their loads leave. stream | duo, one expert with N = K = 4096: 32 rows
+//   9.0 | 27.9, 64 12.7 | 28.7, 128 21.3 | 33.3, 192 29.7 | 33.0, 256 38.0 | 33.2.
+//   Several experts: the stream kernel takes an expert's rows 32 at a time and
+//   reads its weights for each again, so that the longest expert sets the time.
+//   16 of 2048 x 2048 with 4 rows each 14.0 | 17.3; a whole stage of 128 experts
+//   (2048 x 768, top-8) of 65 tokens 125 | 135 evenly spread and 102 | 87 with
+//   their ranks' 1.2th powers, of 128 tokens 129 | 139 and 148 | 98. Four rows per
+//   expert is where the loss from skew passes the gain.
+//   Many rows: 256-row tiles need full ones and enough of them for every CU.
+//   tile | duo, one expert with N = K = 4096: 1024 rows 55 | 36, 4096 64 | 71, 8192
+//   123 | 135; 128 experts of 512 rows, 2048 x 768, 171 | 181. Gate/up and the
+//   shared8 form have longer epilogues, which the second workgroup hides: 8192
+//   tokens of the stage above gate/up 299 | 295, down 204 | 196, 4096 skewed ones
+//   207 | 177 and 136 | 118.
 template <bool GU>
 hipError_t launch(const I8GemmArgs& a, hipStream_t st) {
   Params P{};
@@ -995,10 +807,28 @@ hipError_t launch(const I8GemmArgs& a, hipStream_t st) {
     i8_stream_kernel<GU><<<static_cast<unsigned>(a.E) * groups, kThreads, 0, st>>>(P, ks, groups);
   } else if (!GU && !a.shared8 && avg >= 512 && (a.M / 256) * static_cast<int64_t>(ceil_div(a.N, BN)) >= grid) {
     i8_tile_kernel<<<grid, kThreads, 0, st>>>(P);
-  } else if (!GU && a.shared8) {
-    i8_duo_kernel<GU, !GU><<<2 * grid, kW4, 0, st>>>(P);
   } else {
-    i8_duo_kernel<GU><<<2 * grid, kW4, 0, st>>>(P);
+    DuoParams D{};
+    D.M = a.M;
+    D.E = a.E;
+    D.N = a.N;
+    D.K = a.K;
+    D.arows = a.arows;
+    D.offsets = a.offsets;
+    D.row_token = a.row_token;
+    D.a = reinterpret_cast<const uint8_t*>(a.a);
+    D.w0 = reinterpret_cast<const uint8_t*>(a.w0);
+    D.w1 = reinterpret_cast<const uint8_t*>(a.w1);
+    D.sa = a.a_scale;
+    D.sw0 = a.w0_scale;
+    D.sw1 = a.w1_scale;
+    D.row_weight = a.row_weight;
+    D.out = static_cast<bf16_t*>(a.out);
+    D.v16 = a.v16;
+    D.v8 = a.v8;
+    D.amax = a.amax;
+    if (!GU && a.shared8) i8_duo_kernel<GU, !GU><<<2 * grid, duo::kThreads, 0, st>>>(D);
+    else i8_duo_kernel<GU, false><<<2 * grid, duo::kThreads, 0, st>>>(D);
   }
   return hipGetLastError();
 }

@@ -61,6 +61,20 @@ __device__ __forceinline__ uint2 codes8(const uint4& v, const CodeFactor& f) {
   return make_uint2(bytes4(c[0], c[1], c[2], c[3]), bytes4(c[4], c[5], c[6], c[7]));
 }
 
+// The same for a block of fp32 sums whose largest magnitude is m (NaN if one is).
+// The hardware's reciprocal is off by about 1 ulp, which moves a value's code only
+// if it is that close to a border: the code is off by less than 0.5 + 2^-15 still.
+struct SumFactor {
+  float up, r, scale;
+  __device__ __forceinline__ explicit SumFactor(float m) {
+    const bool finite = m < __builtin_inff();
+    up = m < 0x1p-64f ? 0x1p64f : 1.0f;
+    r = finite && m > 0.0f ? 127.0f * __builtin_amdgcn_rcpf(m * up) : 0.0f;
+    scale = finite ? m * (1.0f / 127.0f) : __builtin_nanf("");
+  }
+  __device__ __forceinline__ uint32_t code(float v) const { return code_bits(v * up * r); }
+};
+
 // Code i (0 to 3) of a word as a number.
 __device__ __forceinline__ float code_value(uint32_t w, int i) {
   return static_cast<float>(static_cast<int8_t>(w >> (8 * i)));

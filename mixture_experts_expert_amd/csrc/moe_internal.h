@@ -177,14 +177,10 @@ struct GemmArgs {
   const void* bx0;
   const void* bx1;
   int kx, kxr, kxp;
-  // G and U in 8 bits (gq set; bf16 GATEUP, and DGRAD_DOWN with row_token):
-  // codes [T*k][I] and a scale per kCkptBlock columns, written by GATEUP in the
-  // place of out0 and out1, read by DGRAD_DOWN in that of g_in and u_in.
-  // DGRAD_DOWN then also writes a_w (out1) and dot [T*k][ceil(I/128)]: each
-  // row's <dA, a> over 128 columns, before its weight.
+  // bf16 GATEUP with gq set: g and u as codes with a scale per kCkptBlock columns
+  // in the place of out0 and out1.
   int8_t *gq, *uq;
   float *gs, *us;
-  float* dot;
 };
 
 hipError_t launch_gemm_bf16(GemmMode mode, const moe_shape& s, const GemmArgs& a, hipStream_t st);
@@ -330,8 +326,26 @@ struct I8GemmArgs {
   float* amax;
 };
 hipError_t launch_gemm_i8(const I8GemmArgs& a, hipStream_t st);
-// out[sorted_to_flat[p]] = the sum of dot [M][n]'s row p (gemm_bf16.hip).
-hipError_t launch_ckpt8_dots(int M, int n, const float* dot, const int32_t* sorted_to_flat, float* out, hipStream_t st);
+
+// The products of a training step that keeps g and u as codes with a scale per
+// kCkptBlock columns, [T*k][I] and [T*k][I/kCkptBlock] (gemm_ckpt8.hip).
+// Gate/up: in = x rows (through row_token, or sorted), w0 and w1 [E][I][H]
+// -> gq, gs, uq, us, a_out. Down dgrad: in = dy, w0 = w_down [E][H][I] and the
+// codes -> dgu, a_out (a times its row's weight), dot [T*k][ceil(I/128)] with each
+// row's <dA, a> over 128 columns, and their sums d_topk_w.
+struct Ckpt8Args {
+  const int32_t *offsets, *row_token;
+  const void *in, *w0, *w1;
+  int8_t *gq, *uq;
+  float *gs, *us;
+  void* a_out;
+  const float* row_weight;
+  const int32_t* sorted_to_flat;
+  void* dgu;
+  float *dot, *d_topk_w;
+};
+hipError_t launch_gate_up_ckpt8(const moe_shape& s, const Ckpt8Args& a, hipStream_t st);
+hipError_t launch_down_dgrad_ckpt8(const moe_shape& s, const Ckpt8Args& a, hipStream_t st);
 
 // The whole layer for a few tokens (few.hip).
 constexpr int kFewMaxT = 64, kFewMaxK = 16;

@@ -55,6 +55,14 @@ SHAPES = [((0, 64, 4, 2, 64, "bf16"), EINVAL), ((8, 64, 4, 5, 64, "bf16"), EINVA
           ((8, 64, 4, 2, 64, "f32"), EUNSUPPORTED), ((1 << 24, 64, 4, 2, 64, "bf16"), EUNSUPPORTED)]
 
 
+@pytest.mark.parametrize("name,n,tail", [("moe_gemm_gate_up_ckpt8", 10, [None]),
+                                         ("moe_gemm_down_dgrad_ckpt8", 14, [1 << 40, None])])
+def test_a_weight_and_a_tiles_rows_have_less_than_2_gib(B, name, n, tail):
+    for H, I, code in ((1 << 15, 1 << 15, EUNSUPPORTED), (64, 1 << 24, EUNSUPPORTED), (64, 1 << 22, EUNSUPPORTED),
+                       (1 << 22, 64, EUNSUPPORTED)):
+        assert getattr(B.lib, name)(B.shape(1, H, 1, 1, I, "bf16"), *[FAKE] * n, *tail) == code
+
+
 @pytest.mark.parametrize("name,n,optional,aligned", [
     ("moe_gemm_gate_up_ckpt8", 10, 1, (0, 3, 4, 5, 7, 9)), ("moe_gemm_down_dgrad_ckpt8", 14, None, (0, 5, 6, 8, 10, 11, 13)),
     ("moe_gemm_down_wgrad_dy", 5, None, (0, 2, 4))])

@@ -146,6 +146,21 @@ def test_down_dgrad(T, H, E, k, I, skew, empty):
     assert (got - want_dot).abs().le(mag * (H + I + 20) * f + 1e-30).all()
 
 
+# More tiles than workgroups, of all the numbers of steps that end a tile differently.
+SEVERAL = [(300, 64, 128, 4, 1088, 0.0, ()), (300, 128, 128, 4, 1088, 0.02, (3, 127)), (260, 192, 160, 3, 832, 0.0, (0,))]
+
+
+@pytest.mark.parametrize("gathered", [True, False])
+@pytest.mark.parametrize("T,H,E,k,I,skew,empty", SEVERAL)
+def test_gate_up_several_tiles_a_workgroup(T, H, E, k, I, skew, empty, gathered):
+    test_gate_up(T, H, E, k, I, skew, empty, gathered)
+
+
+@pytest.mark.parametrize("T,H,E,k,I,skew,empty", SEVERAL)
+def test_down_dgrad_several_tiles_a_workgroup(T, H, E, k, I, skew, empty):
+    test_down_dgrad(T, H, E, k, I, skew, empty)
+
+
 # ---- the training step -------------------------------------------------------------
 
 

@@ -120,6 +120,14 @@ def test_gemm(rows, N, K, weighted):
     assert (got[r] - want).abs().le(want.abs() * (U + 2.0**-21)).all()
 
 
+@pytest.mark.parametrize("K", [16, 144, 208, 592])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_gemm_several_short_tiles_a_workgroup(K, weighted, monkeypatch):
+    """More 128 x 256 tiles than workgroups, of all the numbers of steps that end a tile differently."""
+    monkeypatch.setitem(OFFSETS, "short", ([(7 * e) % 41 for e in range(96)], 1, 2))
+    test_gemm("short", 1552, K, weighted)
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 2048, 2048), (33, 136, 4096), (192, 264, 512), (300, 520, 640), (2000, 512, 256)])
 def test_gemm_dense(M, N, K):
     """One expert without offsets; the codes' extremes, whose sums are the largest."""
@@ -223,6 +231,11 @@ def test_experts(T, H, E, k, I, skew, empty):
     assert (got - y).abs().le(U * y.abs() + (U + 2.0**-20) * size + slack + 1e-30).all()
     rel = (got - y).norm() / y.norm()
     assert rel < 2.0**-8, rel
+
+
+@pytest.mark.parametrize("H", [64, 192, 256, 640])
+def test_experts_several_tiles_a_workgroup(H):
+    test_experts(300, H, 64, 4, 1088, 0.0, (5,))
 
 
 def test_experts_rows_without_numbers():
