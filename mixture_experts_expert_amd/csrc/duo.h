@@ -8,7 +8,7 @@
 // go out under the other's products, and what one waits for at its barrier the
 // other fills. 256 x 256 tiles of 8 wavefronts, one workgroup per CU, read each
 // operand half as often and are a tenth faster where the products are most of the
-// work (int8 8192 x 4096 x 4096 123 us against 135, bf16 8192 rows per expert 393
+// work (int8 8192 x 4096 x 4096 117 us against 134, bf16 8192 rows per expert 393
 // against 424), but stand still during their epilogue and half empty with few
 // rows; where the kernels are chosen both sides are given.
 //
@@ -65,6 +65,14 @@ struct Base {
   const int32_t* row_token;
   const uint8_t *a, *w0, *w1;
 };
+
+// Which 16-byte chunk of LDS rows a read takes, by four rows: what rows t * 4 .. + 3
+// XOR into the chunk's place. A ds_read_b128 goes through in four passes, the first
+// two of lanes {0-3, 12-15, 20-23, 24-27} and {4-7, 8-11, 16-19, 28-31}, the others
+// 32 on. With 16 rows in lanes 0-15 and the next chunk of the same rows in lanes
+// 16-31, the places 0, 2, 3, 1 keep each pass on different banks (t itself does
+// not: half of the LDS cycles were conflicts).
+__device__ __forceinline__ int place4(int t) { return 0x78 >> 2 * (t & 3) & 3; }
 
 __device__ __forceinline__ int kflip(int k) { return (k & 3) | (k >> 1 & 4); }
 
@@ -180,9 +188,8 @@ __device__ __forceinline__ void run(const typename OP::Params& P) {
     return t;
   };
   // LDS of a stage. a, and weights whose rows are the output's columns: row r is
-  // 64 bytes, chunk c of 16 at (c ^ (r >> 2 & 3)), so that 16 rows of one chunk
-  // touch every bank once; row r of the weights holds the column that makes a
-  // lane's results neighbours (Where). KROWS: reduction row k is 256 columns,
+  // 64 bytes, chunk c of 16 at c ^ place4(r / 4); row r of the weights holds the
+  // column that makes a lane's results neighbours (Where). KROWS: reduction row k is 256 columns,
   // chunk c at c ^ 2 kflip(k): a transposing read takes 32 bytes each of rows
   // 8 g .. 8 g + 3, which with those of two neighbouring g touch every bank once.
   rsrc_t ra, rb;
@@ -199,7 +206,7 @@ __device__ __forceinline__ void run(const typename OP::Params& P) {
 #pragma unroll
     for (int i = 0; i < LA; ++i) {
       const int r = (wave * LA + i) * 16 + (lane >> 2);
-      const int c = (lane & 3) ^ ((r >> 2) & 3);
+      const int c = (lane & 3) ^ place4(r >> 2);
       const int row = OP::GATHER ? (r < t.valid ? per_row[r] : 0) : r;
       aoff[i] = r < t.valid ? static_cast<uint32_t>(row) * K + c * 16 : kOutside;
     }
@@ -211,7 +218,7 @@ __device__ __forceinline__ void run(const typename OP::Params& P) {
         boff[i] = n < A->N ? (static_cast<uint32_t>(k) * A->N + n) * 2 : kOutside;
       } else {
         const int r = (wave * 4 + i) * 16 + (lane >> 2);
-        const int c = (lane & 3) ^ ((r >> 2) & 3);
+        const int c = (lane & 3) ^ place4(r >> 2);
         const int j = (r >> 4) & (OP::PAIRED ? 3 : 7), q = r & 15;
         const int n = t.n0 + (r >> 7) * (OP::PAIRED ? 64 : 128) + (j >> 1) * 32 + 8 * (q >> 2) + 4 * (j & 1) + (q & 3);
         boff[i] = n < A->N ? static_cast<uint32_t>(n) * K + c * 16 : kOutside;
@@ -224,7 +231,7 @@ __device__ __forceinline__ void run(const typename OP::Params& P) {
   auto load = [&](int v, uint8_t* S, int sa, int sb, int k) __attribute__((always_inline)) {
     const bool weights = v < 4;
     const int i = weights ? v : v - 4, blk = weights ? wave * 4 + i : wave * LA + i;
-    const int c = (lane_id & 3) ^ ((lane_id >> 4) & 3);  // of the lane's row: (r >> 2 & 3) = lane >> 4
+    const int c = (lane_id & 3) ^ place4(lane_id >> 4);  // of the lane's row: r >> 2 & 3 = lane >> 4
     const uint32_t to = weights ? boff[i & 3] : aoff[i % LA];
     const uint32_t off = (weights && OP::KROWS ? 0 : c * 16) < k ? to : kOutside;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(weights ? rb : ra, (lds_ptr)(S + (weights ? SA : 0) + blk * 1024), 16, off,
@@ -259,7 +266,7 @@ __device__ __forceinline__ void run(const typename OP::Params& P) {
   int fo, fk;  // the lane's byte in a 16-row tile, and in KROWS' weights
   {
     const int q = lane_id & 15, g = lane_id >> 4, k = 8 * g + (q >> 2);
-    fo = q * KB + ((g ^ ((q >> 2) & 3)) << 4);
+    fo = q * KB + ((g ^ place4(q >> 2)) << 4);
     fk = k * (BN * 2) + ((wn * 16 + ((q & 3) >> 1)) ^ (kflip(k) << 1)) * 16 + (q & 1) * 8;
   }
   // The wavefront's 16-row tile i is the tile's 2 i + wm: both halves of a short tile have rows.

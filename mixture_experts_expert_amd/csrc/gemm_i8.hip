@@ -13,7 +13,7 @@
 // wavefronts per CU on 256 x 256 tiles, 2 x 4 wavefronts of 128 x 64. Operands go
 // from memory straight into LDS, two stages of one 128-wide k-step in halves that
 // are refilled as soon as they are read (see there). A row's 128 bytes are eight
-// 16-byte chunks, XOR-swizzled by row so that a 16-lane read touches every bank
+// 16-byte chunks, XOR-swizzled by row so that a pass of a read touches every bank
 // once. Which weight row sits at which LDS row is chosen so that a lane ends with
 // 8 consecutive output columns.
 //
@@ -66,6 +66,10 @@ struct Params {
   uint8_t* v8;
   float* amax;
 };
+
+// Rows of 128 bytes in LDS: chunk c of row r is at c ^ place8(r). A lane reads a row's
+// chunks 2 g and 2 g + 1 (lane / 16 = g), so that places go by pairs (place4).
+__device__ __forceinline__ int place8(int r) { return 2 * duo::place4(r >> 2) | (r >> 1 & 1); }
 
 __device__ __forceinline__ rsrc_t make_rsrc(const void* base, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), static_cast<short>(0), static_cast<int>(bytes),
@@ -232,13 +236,13 @@ __global__ __launch_bounds__(kThreads, 2) void i8_tile_kernel(const Params P) {
 #pragma unroll
     for (int i = 0; i < 2 * HA; ++i) {
       const int r = (i / HA) * (BM / 2) + (wave * HA + i % HA) * 8 + (lane >> 3);
-      const int c = (lane & 7) ^ ((r >> 1) & 7);
+      const int c = (lane & 7) ^ place8(r);
       aoff[i] = r < t.valid ? static_cast<uint32_t>(r) * K + c * 16 : kOutside;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int r = (wave * 4 + i) * 8 + (lane >> 3);
-      const int c = (lane & 7) ^ ((r >> 1) & 7);
+      const int c = (lane & 7) ^ place8(r);
       const int j = (r >> 4) & 3, q = r & 15;
       const int n = t.n0 + (r >> 6) * 64 + (j >> 1) * 32 + 8 * (q >> 2) + 4 * (j & 1) + (q & 3);
       boff[i] = n < A->N ? static_cast<uint32_t>(n) * K + c * 16 : kOutside;
@@ -254,7 +258,7 @@ __global__ __launch_bounds__(kThreads, 2) void i8_tile_kernel(const Params P) {
     const bool weights = !h && v < 4;
     const int i = weights ? v : h ? v : v - 4, blk = wave * (weights ? 4 : HA) + i;  // eight rows of its array
     const uint32_t to = weights ? boff[i & 3] : aoff[(h * HA + i) % (2 * HA)];
-    const int c = (lane_id & 7) ^ (lane_id >> 4) ^ ((blk & 1) * 4);
+    const int c = (lane_id & 7) ^ place8((blk & 1) * 8 + (lane_id >> 3));
     const uint32_t off = c * 16 < (!live ? 0 : s == steps - 1 ? tail : KS) ? to : kOutside;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(weights ? rb : ra, (lds_ptr)((weights ? W : S) + blk * 1024), 16, off,
                                              min(s, steps - 1) * KS, 0, 0);
@@ -307,7 +311,7 @@ __global__ __launch_bounds__(kThreads, 2) void i8_tile_kernel(const Params P) {
     if constexpr (h * HM < NI) {
       int lane = lane_id;
       asm volatile("" : "+v"(lane));
-      const int q = lane & 15, o = ((2 * (lane >> 4)) ^ ((q >> 1) & 7)) << 4;  // rows 16 apart: the same swizzle
+      const int q = lane & 15, o = ((2 * (lane >> 4)) ^ place8(q)) << 4;  // rows 16 apart: the same swizzle
       auto chunk = [&](u32x4(&to)[2], const uint8_t* p) __attribute__((always_inline)) {
         to[0] = *reinterpret_cast<const u32x4*>(p + o);
         to[1] = *reinterpret_cast<const u32x4*>(p + (o ^ 16));
@@ -617,12 +621,12 @@ __global__ __launch_bounds__(kThreads, 2) void i8_stream_kernel(const Params P, 
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = lr + 8 * i;
-      *reinterpret_cast<u32x4*>(to + r * KS + ((lc ^ ((r >> 1) & 7)) << 4)) = v[i];
+      *reinterpret_cast<u32x4*>(to + r * KS + ((lc ^ place8(r)) << 4)) = v[i];
     }
   };
   auto fragment = [&](u32x4(&to)[2], const uint8_t* from) __attribute__((always_inline)) {
     const uint8_t* p = from + q * KS;
-    const int o = ((2 * g) ^ ((q >> 1) & 7)) << 4;
+    const int o = ((2 * g) ^ place8(q)) << 4;
     to[0] = *reinterpret_cast<const u32x4*>(p + o);
     to[1] = *reinterpret_cast<const u32x4*>(p + (o ^ 16));
   };
@@ -766,7 +770,7 @@ __global__ __launch_bounds__(kThreads, 2) void i8_stream_kernel(const Params P, 
 //   expert is where the loss from skew passes the gain.
 //   Many rows: 256-row tiles need full ones and enough of them for every CU.
 //   tile | duo, one expert with N = K = 4096: 1024 rows 55 | 36, 4096 64 | 71, 8192
-//   123 | 135; 128 experts of 512 rows, 2048 x 768, 171 | 181. Gate/up and the
+//   117 | 134; 128 experts of 512 rows, 2048 x 768, 162 | 181. Gate/up and the
 //   shared8 form have longer epilogues, which the second workgroup hides: 8192
 //   tokens of the stage above gate/up 299 | 295, down 204 | 196, 4096 skewed ones
 //   207 | 177 and 136 | 118.
