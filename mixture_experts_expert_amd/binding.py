@@ -836,14 +836,21 @@ class Ckpt8Stage:
         """Bytes held between forward and backward (x itself not among them)."""
         return sum(t.numel() * t.element_size() for t in self.kept.values())
 
-    def _activations(self, t, name):
-        if tuple(t.shape) != (self.T, self.H) or t.dtype != torch.bfloat16 or not t.is_contiguous():
-            raise ValueError(f"{name} has to be [{self.T}, {self.H}] in bf16, contiguous")
-        if t.device != self.buf["y"].device or t.device.type != "cuda":
-            raise ValueError(f"{name} is on {t.device}, the stage on {self.buf['y'].device}; both have to be on one GPU")
+    def _check_tensors(self, *named):
+        """(name, tensor, sizes[, dtype]): what the kernels would read wrongly is refused."""
+        for name, t, sizes, *dt in named:
+            dt = dt[0] if dt else torch.bfloat16
+            if tuple(t.shape) != sizes or t.dtype != dt or not t.is_contiguous():
+                raise ValueError(f"{name} has to be {list(sizes)} in {dt}, contiguous")
+        for name, t, *_ in named:
+            if t.device != self.buf["y"].device or t.device.type != "cuda":
+                raise ValueError(f"{name} is on {t.device}, the stage on {self.buf['y'].device}; both have to be on one GPU")
 
     def forward(self, x, w_router, w_gate, w_up, w_down, logit_bias=None, stream=None):
-        self._activations(x, "x")
+        T, H, E, I = self.T, self.H, self.E, self.I
+        bias = () if logit_bias is None else (("logit_bias", logit_bias, (E,), torch.float32),)
+        self._check_tensors(("x", x, (T, H)), ("w_router", w_router, (E, H)), ("w_gate", w_gate, (E, I, H)),
+                            ("w_up", w_up, (E, I, H)), ("w_down", w_down, (E, H, I)), *bias)
         b, c, s = self.buf, self.scratch, self.s
         with torch.cuda.device(x.device):
             moe_route(s, x, w_router, logit_bias, b["logits"], b["topk_idx"], b["topk_w"], stream)
@@ -863,7 +870,7 @@ class Ckpt8Stage:
     def backward(self, dy, accumulate_dw: bool = False, stream=None):
         """Of the last forward: returns dx; dw_gate, dw_up, dw_down (float32, added to with
         ``accumulate_dw``), d_topk_w and d_logits are in ``buf``."""
-        self._activations(dy, "dy")
+        self._check_tensors(("dy", dy, (self.T, self.H)))
         if not hasattr(self, "w"):
             raise ValueError("backward before forward")
         b, c, s, acc = self.buf, self.scratch, self.s, int(accumulate_dw)

@@ -111,6 +111,20 @@ def test_stage_refusals(B):
     assert big.kept_bytes() < M * (6 * 768 + 2 * 2048) / 5
 
 
+def test_stage_refuses_weights_of_other_sizes_and_types(B):
+    st = B.Ckpt8Stage(8, 128, 4, 2, 64, device="cpu")
+    z = lambda *d, dt=torch.bfloat16: torch.zeros(*d, dtype=dt)
+    good = {"x": z(8, 128), "w_router": z(4, 128), "w_gate": z(4, 64, 128), "w_up": z(4, 64, 128), "w_down": z(4, 128, 64),
+            "logit_bias": z(4, dt=torch.float32)}
+    for name, t in good.items():
+        other = torch.bfloat16 if name == "logit_bias" else torch.float32
+        for bad in (t.to(other), t[:-1], t.unsqueeze(0), torch.stack((t, t), -1)[..., 0]):
+            with pytest.raises(ValueError, match=name + " has to be"):
+                st.forward(**{**good, name: bad})
+    with pytest.raises(ValueError, match="on one GPU"):
+        st.forward(**good)
+
+
 def test_backward_is_the_derivative():
     """Central differences of f = sum over rows of w <dy[t], a W_down^T> in g, u and w."""
     g = torch.Generator().manual_seed(1)
