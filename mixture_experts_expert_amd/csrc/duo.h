@@ -8,7 +8,7 @@
 // go out under the other's products, and what one waits for at its barrier the
 // other fills. 256 x 256 tiles of 8 wavefronts, one workgroup per CU, read each
 // operand half as often and are a tenth faster where the products are most of the
-// work (int8 8192 x 4096 x 4096 117 us against 134, bf16 8192 rows per expert 393
+// work (int8 8192 x 4096 x 4096 122 us against 142, bf16 8192 rows per expert 393
 // against 424), but stand still during their epilogue and half empty with few
 // rows; where the kernels are chosen both sides are given.
 //

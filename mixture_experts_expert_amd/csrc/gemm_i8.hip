@@ -769,11 +769,12 @@ __global__ __launch_bounds__(kThreads, 2) void i8_stream_kernel(const Params P, 
 //   their ranks' 1.2th powers, of 128 tokens 129 | 139 and 148 | 98. Four rows per
 //   expert is where the loss from skew passes the gain.
 //   Many rows: 256-row tiles need full ones and enough of them for every CU.
-//   tile | duo, one expert with N = K = 4096: 1024 rows 55 | 36, 4096 64 | 71, 8192
-//   117 | 134; 128 experts of 512 rows, 2048 x 768, 162 | 181. Gate/up and the
-//   shared8 form have longer epilogues, which the second workgroup hides: 8192
-//   tokens of the stage above gate/up 299 | 295, down 204 | 196, 4096 skewed ones
-//   207 | 177 and 136 | 118.
+//   tile | duo, one expert with N = K = 4096: 1024 rows 52 | 34, 2048 54 | 40, 4096
+//   63 | 72, 8192 122 | 142; 128 experts, 2048 x 768, of 256 rows each 101 | 106, of
+//   512 160 | 183; 32 experts of 512 rows 53 | 52, of 1024 82 | 90. Gate/up and the
+//   shared8 form have longer epilogues, which the second workgroup hides: 4096
+//   skewed tokens of the stage above 207 | 177 and 136 | 118 with the same LDS
+//   places in both.
 template <bool GU>
 hipError_t launch(const I8GemmArgs& a, hipStream_t st) {
   Params P{};
@@ -809,7 +810,7 @@ hipError_t launch(const I8GemmArgs& a, hipStream_t st) {
       while (ks < kWaves && static_cast<int64_t>(a.E) * ceil_div(a.N, 16 * kWaves / ks) < 2 * grid && ks < KB) ks *= 2;
     const int groups = ceil_div(a.N, 16 * kWaves / ks);
     i8_stream_kernel<GU><<<static_cast<unsigned>(a.E) * groups, kThreads, 0, st>>>(P, ks, groups);
-  } else if (!GU && !a.shared8 && avg >= 512 && (a.M / 256) * static_cast<int64_t>(ceil_div(a.N, BN)) >= grid) {
+  } else if (!GU && !a.shared8 && avg >= 256 && (a.M / 256) * static_cast<int64_t>(ceil_div(a.N, BN)) >= grid) {
     i8_tile_kernel<<<grid, kThreads, 0, st>>>(P);
   } else {
     DuoParams D{};
