@@ -24,13 +24,15 @@
 //   GATHER    rows of a through row_token
 //   KROWS     the weights' reduction index is their strided one ([K][N], bf16);
 //             then acc[i][j][x] is column 16 j + 4 g + x
-//   STORES    store instructions of finish() per wavefront, a fixed number
 //   EXTRA     bytes of LDS for what begin() fetches
 //   Acc, product(w, a, acc)
 //   begin     sends for the tile's extras, into LDS; per_row: its tokens (GATHER)
-//   finish    the epilogue; rows and columns that are not there go out of range,
-//             so that the number of stores is fixed and they run on under the
-//             next tile's first steps
+//   finish    the epilogue; calls loads_landed() before its first store
+//
+// The counter of memory instructions says how many are left, not which. A tile's
+// stores run on under the next one's first two steps, so those steps' loads have
+// to be done before the first store goes out (loads_landed): no wait then counts
+// stores, whose number is the compiler's affair (it joins equal neighbours).
 #pragma once
 #include <type_traits>
 
@@ -98,6 +100,13 @@ __device__ __forceinline__ void words_to_lds(const rsrc_t& r, char* to, uint32_t
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr)to, 4, off, 0, 0, 0);
 }
 
+// Every load of this wavefront has landed.
+__device__ __forceinline__ void loads_landed() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+  asm volatile("" ::: "memory");
+}
+
 __device__ __forceinline__ float across_groups_max(float m) {  // lanes 16, 32 and 48 apart; NaN if one is
   m = __builtin_elementwise_maximum(m, __shfl_xor(m, 16, kWave));
   return __builtin_elementwise_maximum(m, __shfl_xor(m, 32, kWave));
@@ -108,8 +117,6 @@ __device__ __forceinline__ void run(const typename OP::Params& P) {
   typedef typename OP::Acc Acc;
   typedef const __attribute__((address_space(4))) typename OP::Params* args_t;
   constexpr int TN = OP::PAIRED ? BN / 2 : BN;
-  constexpr int STORES = OP::STORES;
-  static_assert(LOADS + STORES < 64, "the counter of memory instructions has six bits");
   __shared__ __attribute__((aligned(1024))) uint8_t lds0[STAGE];
   __shared__ __attribute__((aligned(1024))) uint8_t lds1[STAGE];
   __shared__ __attribute__((aligned(1024))) uint8_t lds2[STAGE];
@@ -286,13 +293,14 @@ __device__ __forceinline__ void run(const typename OP::Params& P) {
       to = *reinterpret_cast<const u32x4*>(S + SA + (wn * 8 + j) * (16 * KB) + fo);
     }
   };
-  // Step s on stage C, while the loads of step sn go out into stage D.
-  auto kstep = [&](auto nic, auto firstc, bool stores, const uint8_t* C, uint8_t* D, int sn, bool live,
+  // Step s on stage C, while the loads of step sn go out into stage D. `there`: the
+  // step's loads were done before the last tile's stores, which are still under way.
+  auto kstep = [&](auto nic, auto firstc, bool there, const uint8_t* C, uint8_t* D, int sn, bool live,
                    auto&& after) __attribute__((always_inline)) {
     constexpr int NI = decltype(nic)::value;
     constexpr bool first = decltype(firstc)::value != 0;
     asm volatile("" ::: "memory");
-    if (stores) __builtin_amdgcn_s_waitcnt(0x0070 | ((LOADS + STORES) & 15) | ((LOADS + STORES) >> 4) << 14);
+    if (there) __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
     else __builtin_amdgcn_s_waitcnt(0x0070 | (LOADS & 15) | (LOADS >> 4) << 14);
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
@@ -330,7 +338,7 @@ __device__ __forceinline__ void run(const typename OP::Params& P) {
     const bool more = next < hi;
     auto nothing = [] {};
     // Step s is read after its own barrier, at which all but step s + 1's loads
-    // (and the stores, if they are newer) have landed; step s + 2's go out then.
+    // have landed (steps 0 and 1: all); step s + 2's go out then.
     auto send_tokens = [&]() __attribute__((always_inline)) {  // every wavefront has left begin()
       if (!more) return;
       nx = find(next);

@@ -57,7 +57,6 @@ struct GateUpOp : Bf16Product {
   typedef CkptParams Params;
   typedef const __attribute__((address_space(4))) Params* args_t;
   static constexpr bool PAIRED = true, GATHER = ROWS, KROWS = false;
-  static constexpr int STORES = 8 * duo::FM;
   static constexpr int EXTRA = 4;
 
   static __device__ __forceinline__ void begin(args_t, const duo::Tile&, const int*, char*, int, int) {}
@@ -90,26 +89,25 @@ struct GateUpOp : Bf16Product {
     const rsrc_t rgs = make_rsrc(A->gs + sbase, sbytes), rus = make_rsrc(A->us + sbase, sbytes);
     const rsrc_t ra = make_rsrc(A->a_out + base, 2 * bytes);
 #pragma unroll
-    for (int i = 0; i < duo::FM; ++i) {
+    for (int i = 0; i < NI; ++i) {
       const int r = w.row(i);
-      const bool there = i < NI && r < t.valid && blk < nblk;
-      u32x2 gc[2]{}, uc[2]{};
-      u32x4 av[2]{};
-      float sg = 0.0f, su = 0.0f;
-      if (i < NI) {
-        block(&acc[i][0], gc, sg);
-        block(&acc[i][4], uc, su);
+      const bool there = r < t.valid && blk < nblk;
+      u32x2 gc[2], uc[2];
+      u32x4 av[2];
+      float sg, su;
+      block(&acc[i][0], gc, sg);
+      block(&acc[i][4], uc, su);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          float a[8];
+      for (int h = 0; h < 2; ++h) {
+        float a[8];
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const float g = acc[i][2 * h + x / 4][x % 4];
-            a[x] = g * sigmoid(g) * acc[i][4 + 2 * h + x / 4][x % 4];
-          }
-          av[h] = pack8(a);
+        for (int x = 0; x < 8; ++x) {
+          const float g = acc[i][2 * h + x / 4][x % 4];
+          a[x] = g * sigmoid(g) * acc[i][4 + 2 * h + x / 4][x % 4];
         }
+        av[h] = pack8(a);
       }
+      if (i == 0) duo::loads_landed();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const uint32_t to = there ? static_cast<uint32_t>(r) * N + blk * kCkptBlock + 32 * h + 8 * w.g : kOutside;
@@ -128,7 +126,6 @@ struct DownGradOp : Bf16Product {
   typedef CkptParams Params;
   typedef const __attribute__((address_space(4))) Params* args_t;
   static constexpr bool PAIRED = false, GATHER = true, KROWS = true;
-  static constexpr int STORES = 13 * duo::FM;
   static constexpr int EXTRA = 4 * duo::BM;  // the rows' weights
 
   static __device__ __forceinline__ void begin(args_t A, const duo::Tile& t, const int*, char* extra, int wave, int lane) {
@@ -172,42 +169,41 @@ struct DownGradOp : Bf16Product {
     };
     Kept kept[2];  // a 16-row tile's are read during the arithmetic of the one before
     fetch(0, kept[0]);
+    duo::loads_landed();
 #pragma unroll
-    for (int i = 0; i < duo::FM; ++i) {
+    for (int i = 0; i < NI; ++i) {
       if (i + 1 < NI) fetch(i + 1, kept[(i + 1) & 1]);
       const Kept& k = kept[i & 1];
       const int r = w.row(i);
-      const bool row = i < NI && r < t.valid;
+      const bool row = r < t.valid;
       const float rw = reinterpret_cast<const float*>(extra)[r];
       float sum = 0.0f;
 #pragma unroll
       for (int h = 0; h < 4; ++h) {
         const int n = c0 + 32 * h + col;
-        u32x4 dg{}, du{}, aw{};
-        if (i < NI) {
-          float d8[8], g8[8], u8[8], a8[8];
+        u32x4 dg, du, aw;
+        float d8[8], g8[8], u8[8], a8[8];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i][2 * h][x]),
-                                                            __float_as_uint(acc[i][2 * h + 1][x]), false, false);
-            d8[x] = __uint_as_float(p[0]);
-            d8[4 + x] = __uint_as_float(p[1]);
-          }
-          float part = 0.0f;
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            const float g = code_value(k.g[h][x / 4], x & 3) * k.gs[h / 2], u = code_value(k.u[h][x / 4], x & 3) * k.us[h / 2];
-            const float s = sigmoid(g), silu = g * s, a = silu * u, d = rw * d8[x];
-            part = fmaf(d8[x], a, part);
-            a8[x] = rw * a;
-            g8[x] = d * u * s * (1.0f + g * (1.0f - s));
-            u8[x] = d * silu;
-          }
-          sum += n < N ? part : 0.0f;
-          dg = pack8(g8);
-          du = pack8(u8);
-          aw = pack8(a8);
+        for (int x = 0; x < 4; ++x) {
+          const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i][2 * h][x]),
+                                                          __float_as_uint(acc[i][2 * h + 1][x]), false, false);
+          d8[x] = __uint_as_float(p[0]);
+          d8[4 + x] = __uint_as_float(p[1]);
         }
+        float part = 0.0f;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const float g = code_value(k.g[h][x / 4], x & 3) * k.gs[h / 2], u = code_value(k.u[h][x / 4], x & 3) * k.us[h / 2];
+          const float s = sigmoid(g), silu = g * s, a = silu * u, d = rw * d8[x];
+          part = fmaf(d8[x], a, part);
+          a8[x] = rw * a;
+          g8[x] = d * u * s * (1.0f + g * (1.0f - s));
+          u8[x] = d * silu;
+        }
+        sum += n < N ? part : 0.0f;
+        dg = pack8(g8);
+        du = pack8(u8);
+        aw = pack8(a8);
         const bool there = row && n < N;
         const uint32_t to = (static_cast<uint32_t>(r) * 2 * N + n) * 2;
         __builtin_amdgcn_raw_buffer_store_b128(dg, ro, there ? to : kOutside, 0, 0);

@@ -131,13 +131,16 @@ constexpr int kBand = 8;  // row tiles that run side by side over all columns: w
 // half's rows once step s - 2 has ended. In order of issue:
 //   .. | W, A0 of s+1 | A1 of s+1 | W, A0 of s+2 | A1 of s+2 | ..
 //         step s-1, 2nd  step s, 1st   step s, 2nd  step s+1, 1st half
-// so at each barrier all but the last two groups have landed.
+// so at each barrier all but the last two groups have landed. A tile's stores run
+// on under the next one's first step; the three groups that are on their way by
+// then land before the first store (duo.h says why), so that its first two
+// barriers wait for none.
 __global__ __launch_bounds__(kThreads, 2) void i8_tile_kernel(const Params P) {
   constexpr int BM = 256;
   constexpr int FM = BM / 32, HM = FM / 2;  // 16-row tiles of a per wavefront, and of those per half
   constexpr int HA = BM / 128;              // load instructions of half a's rows per wavefront
   constexpr int OS = BM / 2 * KS;
-  constexpr int G1 = HA, G2 = 4 + HA, STORES = 2 * FM;
+  constexpr int G1 = HA, G2 = 4 + HA;
   // A stage, in three arrays, so that the compiler sees which reads follow
   // which loads: the weights' rows, the first and the second half's rows of a.
   __shared__ __attribute__((aligned(1024))) uint8_t w0[BN * KS];
@@ -263,7 +266,8 @@ __global__ __launch_bounds__(kThreads, 2) void i8_tile_kernel(const Params P) {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(weights ? rb : ra, (lds_ptr)((weights ? W : S) + blk * 1024), 16, off,
                                              min(s, steps - 1) * KS, 0, 0);
   };
-  // All but the last PENDING memory instructions are done, and every wavefront is here.
+  // All but the last PENDING memory instructions are done (kAny: as many as there are), and every wavefront is here.
+  constexpr int kAny = 63;
   auto landed = [&](auto pending) __attribute__((always_inline)) {
     constexpr int n = decltype(pending)::value;
     asm volatile("" ::: "memory");
@@ -356,7 +360,7 @@ __global__ __launch_bounds__(kThreads, 2) void i8_tile_kernel(const Params P) {
     // pair on the loads are the next tile's.
     auto pair = [&](auto firstc, int s) __attribute__((always_inline)) {
       constexpr bool first = decltype(firstc)::value != 0;
-      using pending = std::integral_constant<int, G1 + G2 + (first ? STORES : 0)>;
+      using pending = std::integral_constant<int, first ? kAny : G1 + G2>;
       const bool last = s + 2 == padded;
       half(nic, none{}, x0, w0, y1, nullptr, s + 1, s + 1 < steps);  // an odd count's last step: zeros
       landed(pending{});
@@ -377,8 +381,7 @@ __global__ __launch_bounds__(kThreads, 2) void i8_tile_kernel(const Params P) {
     };
     pair(one{}, 0);
     for (int s = 2; s < padded; s += 2) pair(none{}, s);
-    // ---- epilogue; stores of rows and columns outside go out of range, so
-    // that their count is fixed: they run on under the next tile's first step.
+    // ---- epilogue
     const auto* A = args();
     const int lane = lane_id, g = lane >> 4, q = lane & 15;
     const int row0 = now.row0, valid = now.valid, n0 = now.n0;
@@ -388,23 +391,22 @@ __global__ __launch_bounds__(kThreads, 2) void i8_tile_kernel(const Params P) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) cs[j] = columns(wn * 64 + (j >> 1) * 32 + 8 * g + 4 * (j & 1));
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
+    for (int i = 0; i < NI; ++i) {
       const int r = row_of(i, q);
       const float rs = scale[r] * (A->row_weight != nullptr ? __int_as_float(per_row[r]) : 1.0f);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int n = n0 + wn * 64 + 32 * h + 8 * g;
-        u32x4 o{};
-        if (i < NI && row_of(i, 0) < valid) {  // 16 rows past the end are not packed
-          float v[8];
+        u32x4 o;
+        float v[8];
 #pragma unroll
-          for (int c = 0; c < 8; ++c)
-            v[c] = static_cast<float>(acc[i][2 * h + c / 4][c % 4]) * cs[2 * h + c / 4][c % 4] * rs;
+        for (int c = 0; c < 8; ++c)
+          v[c] = static_cast<float>(acc[i][2 * h + c / 4][c % 4]) * cs[2 * h + c / 4][c % 4] * rs;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) o[c] = pack_bf16x2(v[2 * c], v[2 * c + 1]);
-        }
+        for (int c = 0; c < 4; ++c) o[c] = pack_bf16x2(v[2 * c], v[2 * c + 1]);
+        if (i == 0 && h == 0) duo::loads_landed();
         __builtin_amdgcn_raw_buffer_store_b128(
-            o, ro, i < NI && r < valid && n < A->N ? (static_cast<uint32_t>(r) * A->N + n) * 2 : kOutside, 0, 0);
+            o, ro, r < valid && n < A->N ? (static_cast<uint32_t>(r) * A->N + n) * 2 : kOutside, 0, 0);
       }
     }
     now = nx;
@@ -446,7 +448,6 @@ struct I8Op {
   typedef const __attribute__((address_space(4))) Params* args_t;
   typedef i32x4 Acc;
   static constexpr bool PAIRED = GU, GATHER = GU, KROWS = false;
-  static constexpr int STORES = (GU ? 5 : 4) * duo::FM;
   static constexpr int EXTRA = 4 * (2 * duo::BN + (GU ? 2 * duo::BM : duo::BM));
 
   static __device__ __forceinline__ Acc product(const u32x4& w, const u32x4& a, const Acc& c) { return product64(w, a, c); }
@@ -468,7 +469,6 @@ struct I8Op {
   template <int NI>
   static __device__ __forceinline__ void finish(args_t A, Acc (&acc)[duo::FM][duo::FN], const duo::Tile& t, char* extra,
                                                 const duo::Where& w) {
-    constexpr int FM = duo::FM;
     const int g = w.g, wn = w.wn, n0 = t.n0, valid = t.valid;
     const float* scale = reinterpret_cast<const float*>(extra);
     auto columns = [&](int at) __attribute__((always_inline)) {
@@ -505,22 +505,18 @@ struct I8Op {
       __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
+      duo::loads_landed();
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
+      for (int i = 0; i < NI; ++i) {
         const int r = w.row(i);
-        const bool row = i < NI && r < valid;
-        float m = 0.0f;
-        if (i < NI) m = __builtin_elementwise_maximum(amax[r][0], amax[r][1]);
+        const bool row = r < valid;
+        const float m = __builtin_elementwise_maximum(amax[r][0], amax[r][1]);
         const Factor24 f(m);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          u32x4 o{};
-          u32x2 low{};
-          if (i < NI) {
-            const Packed24 p0(__builtin_bit_cast(f32x4, acc[i][2 * h]), f), p1(__builtin_bit_cast(f32x4, acc[i][2 * h + 1]), f);
-            o = u32x4{p0.hi[0], p0.hi[1], p1.hi[0], p1.hi[1]};
-            low = u32x2{p0.lo, p1.lo};
-          }
+          const Packed24 p0(__builtin_bit_cast(f32x4, acc[i][2 * h]), f), p1(__builtin_bit_cast(f32x4, acc[i][2 * h + 1]), f);
+          const u32x4 o{p0.hi[0], p0.hi[1], p1.hi[0], p1.hi[1]};
+          const u32x2 low{p0.lo, p1.lo};
           const int n = n0 + wn * 64 + 32 * h + 8 * g;
           const uint32_t to = row && n < A->N ? static_cast<uint32_t>(r) * A->N + n : kOutside;
           __builtin_amdgcn_raw_buffer_store_b128(o, rv, to == kOutside ? to : 2 * to, 0, 0);
@@ -535,31 +531,30 @@ struct I8Op {
 #pragma unroll
       for (int j = 0; j < 8; ++j) cs[j] = columns(wn * 128 + (j >> 1) * 32 + 8 * g + 4 * (j & 1));
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
+      for (int i = 0; i < NI; ++i) {
         const int r = w.row(i);
-        const float rs = i < NI ? scale[r] * (A->row_weight != nullptr ? scale[2 * duo::BN + r] : 1.0f) : 0.0f;
+        const float rs = scale[r] * (A->row_weight != nullptr ? scale[2 * duo::BN + r] : 1.0f);
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           const int n = n0 + wn * 128 + 32 * h + 8 * g;
-          u32x4 o{};
-          if (i < NI) {
-            float v[8], m = 0.0f;
+          u32x4 o;
+          float v[8], m = 0.0f;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              v[c] = static_cast<float>(acc[i][2 * h + c / 4][c % 4]) * cs[2 * h + c / 4][c % 4] * rs;
-              if constexpr (S8) m = __builtin_elementwise_maximum(m, fabsf(v[c]));  // NaN if one is
-            }
-            float f = 0.0f;
-            uint32_t s = 0;
-            if constexpr (S8) s = shared8_exponent(m, f);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              if constexpr (S8) o[c] = shared8_word(v[2 * c], v[2 * c + 1], s, f, c);
-              else o[c] = pack_bf16x2(v[2 * c], v[2 * c + 1]);
-            }
+          for (int c = 0; c < 8; ++c) {
+            v[c] = static_cast<float>(acc[i][2 * h + c / 4][c % 4]) * cs[2 * h + c / 4][c % 4] * rs;
+            if constexpr (S8) m = __builtin_elementwise_maximum(m, fabsf(v[c]));  // NaN if one is
           }
+          float f = 0.0f;
+          uint32_t s = 0;
+          if constexpr (S8) s = shared8_exponent(m, f);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if constexpr (S8) o[c] = shared8_word(v[2 * c], v[2 * c + 1], s, f, c);
+            else o[c] = pack_bf16x2(v[2 * c], v[2 * c + 1]);
+          }
+          if (i == 0 && h == 0) duo::loads_landed();
           __builtin_amdgcn_raw_buffer_store_b128(
-              o, ro, i < NI && r < valid && n < A->N ? (static_cast<uint32_t>(r) * A->N + n) * 2 : kOutside, 0, 0);
+              o, ro, r < valid && n < A->N ? (static_cast<uint32_t>(r) * A->N + n) * 2 : kOutside, 0, 0);
         }
       }
     }
