@@ -40,6 +40,7 @@
 // 1 x 128 blocks of a, whose maxima meet in LDS.
 #include <type_traits>
 
+#include "duo.h"
 #include "shared8.h"
 
 namespace moe {
@@ -129,14 +130,17 @@ constexpr int kBand = 8;  // row tiles that run side by side over all columns: w
 // half's rows once step s - 2 has ended. In order of issue:
 //   .. | W, A0 of s+1 | A1 of s+1 | W, A0 of s+2 | A1 of s+2 | ..
 //         step s-1, 2nd  step s, 1st   step s, 2nd  step s+1, 1st half
-// so at each barrier all but the last two groups have landed.
+// so at each barrier all but the last two groups have landed. A tile's stores run
+// on under the next one's first step; the three groups that are on their way by
+// then land before the first store (duo.h says why), so that its first two
+// barriers wait for none.
 template <bool GU, int BM>
 __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P) {
   constexpr int FM = BM / 32, HM = FM / 2;  // 16-row tiles of a per wavefront, and of those per half
   constexpr int HA = BM / 128;              // load instructions of half a's rows per wavefront
   constexpr int OS = BM / 2 * KS;
   constexpr int TN = GU ? BN / 2 : BN;
-  constexpr int G1 = HA + 1, G2 = 4 + HA + 1, STORES = 2 * FM;
+  constexpr int G1 = HA + 1, G2 = 4 + HA + 1;
   // A stage, in three arrays, so that the compiler sees which reads follow
   // which loads: the weights' rows; the first half's rows of a and 8 x 64 scales
   // (waves 0 ..: rows; 6 and 7: the weights'); the second half's rows and scales.
@@ -286,7 +290,8 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
     __builtin_amdgcn_raw_ptr_buffer_load_lds(weights ? rb : ra, (lds_ptr)((weights ? W : S) + blk * 1024), 16, off, s * KS,
                                              0, 0);
   };
-  // All but the last PENDING memory instructions are done, and every wavefront is here.
+  // All but the last PENDING memory instructions are done (kAny: as many as there are), and every wavefront is here.
+  constexpr int kAny = 63;
   auto landed = [&](auto pending) __attribute__((always_inline)) {
     constexpr int n = decltype(pending)::value;
     asm volatile("" ::: "memory");
@@ -387,7 +392,7 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
     // pair on the loads are the next tile's.
     auto pair = [&](auto firstc, int s) __attribute__((always_inline)) {
       constexpr bool first = decltype(firstc)::value != 0;
-      using pending = std::integral_constant<int, G1 + G2 + (first ? STORES : 0)>;
+      using pending = std::integral_constant<int, first ? kAny : G1 + G2>;
       const bool last = s + 2 == padded;
       half(nic, none{}, x0, w0, y1, nullptr, s + 1, s + 1 < steps);  // an odd count's last step: zeros
       landed(pending{});
@@ -415,8 +420,7 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
     };
     pair(one{}, 0);
     for (int s = 2; s < padded; s += 2) pair(none{}, s);
-    // ---- epilogue; stores of rows and columns outside go out of range, so
-    // that their count is fixed: they run on under the next tile's first step.
+    // ---- epilogue
     const auto* A = args();
     const int lane = lane_id, g = lane >> 4, q = lane & 15;
     const int row0 = now.row0, valid = now.valid, n0 = now.n0;
@@ -443,21 +447,18 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
       __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
       __builtin_amdgcn_s_barrier();
       asm volatile("" ::: "memory");
+      duo::loads_landed();
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
+      for (int i = 0; i < NI; ++i) {
         const int r = row_of(i, q);
-        uint2 codes = make_uint2(0, 0);
-        float m = 0.0f;
-        if (i < NI) {
-          m = fmaxf(fmaxf(amax[r][0], amax[r][1]), fmaxf(amax[r][2], amax[r][3]));
-          float up;
-          const float f = code_factor(m, up);
-          const float v0[4] = {acc[i][0][0], acc[i][0][1], acc[i][0][2], acc[i][0][3]};
-          const float v1[4] = {acc[i][1][0], acc[i][1][1], acc[i][1][2], acc[i][1][3]};
-          codes = make_uint2(codes4(v0, up, f), codes4(v1, up, f));
-        }
+        const float m = fmaxf(fmaxf(amax[r][0], amax[r][1]), fmaxf(amax[r][2], amax[r][3]));
+        float up;
+        const float f = code_factor(m, up);
+        const float v0[4] = {acc[i][0][0], acc[i][0][1], acc[i][0][2], acc[i][0][3]};
+        const float v1[4] = {acc[i][1][0], acc[i][1][1], acc[i][1][2], acc[i][1][3]};
+        const uint2 codes = make_uint2(codes4(v0, up, f), codes4(v1, up, f));
         const int n = n0 + wn * 32 + 8 * g;
-        const bool row = i < NI && r < valid;
+        const bool row = r < valid;
         __builtin_amdgcn_raw_buffer_store_b64(u32x2{codes.x, codes.y}, rq,
                                               row && n < A->N ? static_cast<uint32_t>(r) * A->N + n : kOutside, 0, 0);
         __builtin_amdgcn_raw_buffer_store_b32(
@@ -467,28 +468,27 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
     } else {
       const rsrc_t ro = make_rsrc(A->out + static_cast<int64_t>(row0) * A->N, static_cast<int64_t>(valid) * A->N * 2);
 #pragma unroll
-      for (int i = 0; i < FM; ++i) {
+      for (int i = 0; i < NI; ++i) {
         const int r = row_of(i, q);
         const float x = A->row_weight != nullptr ? __int_as_float(per_row[r]) : 1.0f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int n = n0 + wn * 64 + 32 * h + 8 * g;
-          u32x4 o{};
-          if (i < NI && row_of(i, 0) < valid) {  // 16 rows past the end are not packed
-            float v[8], m = 0.0f;
+          u32x4 o;
+          float v[8], m = 0.0f;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-              v[c] = x * acc[i][2 * h + c / 4][c % 4];
-              m = __builtin_elementwise_maximum(m, fabsf(v[c]));  // NaN if one is
-            }
-            float f = 0.0f;
-            const uint32_t s = A->shared8 ? shared8_exponent(m, f) : 0;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              o[c] = A->shared8 ? shared8_word(v[2 * c], v[2 * c + 1], s, f, c) : pack_bf16x2(v[2 * c], v[2 * c + 1]);
+          for (int c = 0; c < 8; ++c) {
+            v[c] = x * acc[i][2 * h + c / 4][c % 4];
+            m = __builtin_elementwise_maximum(m, fabsf(v[c]));  // NaN if one is
           }
+          float f = 0.0f;
+          const uint32_t s = A->shared8 ? shared8_exponent(m, f) : 0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            o[c] = A->shared8 ? shared8_word(v[2 * c], v[2 * c + 1], s, f, c) : pack_bf16x2(v[2 * c], v[2 * c + 1]);
+          if (i == 0 && h == 0) duo::loads_landed();
           __builtin_amdgcn_raw_buffer_store_b128(
-              o, ro, i < NI && r < valid && n < A->N ? (static_cast<uint32_t>(r) * A->N + n) * 2 : kOutside, 0, 0);
+              o, ro, r < valid && n < A->N ? (static_cast<uint32_t>(r) * A->N + n) * 2 : kOutside, 0, 0);
         }
       }
     }

@@ -5,11 +5,13 @@ shorter or a longer one's first steps.
 
 Operands are small whole numbers with powers of two as scales: sums and scaled sums
 are exact in fp32 and the one rounding to bf16 is compared exactly. The kept codes
-and gradients go by the tolerances of test_gpu_ckpt8.py."""
+and gradients go by the tolerances of test_gpu_ckpt8.py, the E4M3 codes by those of
+test_gpu_serve_tiles.py."""
 import pytest
 import torch
 
 import test_gpu_ckpt8 as C
+import test_gpu_serve_tiles as V
 from mixture_experts_expert_amd import binding as B
 
 pytestmark = pytest.mark.gpu
@@ -115,3 +117,19 @@ def test_gate_up_ckpt8(counts, H, gathered, monkeypatch):
 def test_down_dgrad_ckpt8(counts, H, monkeypatch):
     monkeypatch.setattr(C, "routing", experts_of(counts))
     C.test_down_dgrad(sum(counts), H, len(counts), 1, 3008 if counts is SHORT else 4160, 0.0, ())
+
+
+@pytest.mark.parametrize("K", [16, 240, 272, 400])
+@pytest.mark.parametrize("weighted", [False, True])
+@pytest.mark.parametrize("counts", [SHORT, MIXED], ids=["short", "mixed"])
+def test_gemm_fp8_block(counts, weighted, K, monkeypatch):
+    """short: 128-row tiles; mixed: 256-row tiles (more than 96 rows per expert on average)."""
+    monkeypatch.setitem(V.ROWS, "mix", counts)
+    V.test_gemm_many_tiles("mix", weighted, K)
+
+
+@pytest.mark.parametrize("H", [64, 192, 320, 448])
+@pytest.mark.parametrize("counts", [SHORT, MIXED], ids=["short", "mixed"])
+def test_gate_up_fp8_block(counts, H, monkeypatch):
+    monkeypatch.setitem(V.ROWS, "mix", counts)
+    V.test_gate_up_many_tiles("mix", H)

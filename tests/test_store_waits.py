@@ -58,7 +58,7 @@ def unwaited(lines):
 
 
 @pytest.mark.parametrize("name, n", [("i8_duo_kernel", 3), ("i8_tile_kernel", 1), ("gate_up_ckpt8_kernel", 2),
-                                     ("down_dgrad_ckpt8_kernel", 1)])
+                                     ("down_dgrad_ckpt8_kernel", 1), ("block_tile_kernel", 4)])
 def test_no_store_behind_loads_into_lds(code, name, n):
     found = kernels(code, name)
     assert len(found) == n, list(found)
