@@ -274,11 +274,13 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
   // second half's group (rows, scales). Every wavefront issues every one in
   // every step (a branch in the loop costs more than the instruction): chunks
   // past a row's end, and all of a step that is not there, lie outside and
-  // read zeros.
+  // read zeros; the part of the address that the hardware adds after its range
+  // check stays inside the rows then too.
   typedef __attribute__((address_space(3))) void* lds_ptr;
   auto load = [&](int h, int v, uint8_t* S, uint8_t* W, int s, bool live) __attribute__((always_inline)) {
+    const int at = min(s, steps - 1);
     if (v == (h ? G1 : G2) - 1) {
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)(S + OS + wave * 256), 4, live ? soff[h] : kOutside, s * 4, 0,
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)(S + OS + wave * 256), 4, live ? soff[h] : kOutside, at * 4, 0,
                                                0);
       return;
     }
@@ -287,7 +289,7 @@ __global__ __launch_bounds__(kThreads, 2) void block_tile_kernel(const Params P)
     const uint32_t to = weights ? boff[i & 3] : aoff[(h * HA + i) % (2 * HA)];
     const int c = (lane_id & 7) ^ (lane_id >> 4) ^ ((blk & 1) * 4);
     const uint32_t off = c * 16 < (!live ? 0 : s == steps - 1 ? tail : KS) ? to : kOutside;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(weights ? rb : ra, (lds_ptr)((weights ? W : S) + blk * 1024), 16, off, s * KS,
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(weights ? rb : ra, (lds_ptr)((weights ? W : S) + blk * 1024), 16, off, at * KS,
                                              0, 0);
   };
   // All but the last PENDING memory instructions are done (kAny: as many as there are), and every wavefront is here.
