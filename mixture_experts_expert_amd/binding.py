@@ -797,6 +797,11 @@ class Ckpt8Stage:
     given the same dict share it; their calls then have to be on one stream, or
     ordered. ``forward`` and ``backward`` return views of held buffers (y and dx,
     overwritten by the stage's next call).
+
+    Inputs of a call on ``stream`` may be dropped after it: their memory is kept until
+    the stream has read them. The gradients are tensors of the first backward's
+    stream, the other buffers of the one current at construction: wait for that one
+    before a first call on another, and for the last call's before the stage goes.
     """
 
     def __init__(self, T: int, H: int, E: int, k: int, I: int, device="cuda", x8: bool = False,
@@ -846,12 +851,20 @@ class Ckpt8Stage:
             if t.device != self.buf["y"].device or t.device.type != "cuda":
                 raise ValueError(f"{name} is on {t.device}, the stage on {self.buf['y'].device}; both have to be on one GPU")
 
+    @staticmethod
+    def _read_on(stream, *tensors):
+        """The caller may drop them, and the stage does at its next forward."""
+        for t in tensors:
+            if stream is not None and t is not None:
+                t.record_stream(stream)
+
     def forward(self, x, w_router, w_gate, w_up, w_down, logit_bias=None, stream=None):
         T, H, E, I = self.T, self.H, self.E, self.I
         bias = () if logit_bias is None else (("logit_bias", logit_bias, (E,), torch.float32),)
         self._check_tensors(("x", x, (T, H)), ("w_router", w_router, (E, H)), ("w_gate", w_gate, (E, I, H)),
                             ("w_up", w_up, (E, I, H)), ("w_down", w_down, (E, H, I)), *bias)
         b, c, s = self.buf, self.scratch, self.s
+        self._read_on(stream, x, w_router, w_gate, w_up, w_down, logit_bias)
         with torch.cuda.device(x.device):
             moe_route(s, x, w_router, logit_bias, b["logits"], b["topk_idx"], b["topk_w"], stream)
             moe_permute_fused(s, b["topk_idx"], b["topk_w"], b["counts"], b["offsets"], b["sorted_to_flat"],
@@ -862,8 +875,6 @@ class Ckpt8Stage:
             moe_combine(s, c["o_perm"], b["topk_w"], b["flat_to_sorted"], b["y"], stream)
             if self.x8:
                 moe_quantize_ckpt8(self.T, self.H, x, b["xq"], b["x_scale"], stream)
-        if self.x8 and stream is not None:
-            x.record_stream(stream)  # the caller may drop it
         self.x, self.w = (None if self.x8 else x), (w_gate, w_up, w_down)
         return b["y"]
 
@@ -875,14 +886,16 @@ class Ckpt8Stage:
             raise ValueError("backward before forward")
         b, c, s, acc = self.buf, self.scratch, self.s, int(accumulate_dw)
         w_gate, w_up, w_down = self.w
-        if "dx" not in b:
-            if acc:
-                raise ValueError("accumulate_dw before a first backward: there is nothing to add to")
-            z = lambda *sz, dt=torch.float32: torch.empty(*sz, dtype=dt, device=dy.device)  # noqa: E731
-            T, H, E, k, I = self.T, self.H, self.E, self.k, self.I
-            b.update({"dx": z(T, H, dt=torch.bfloat16), "d_topk_w": z(T, k), "d_logits": z(T, E), "dw_gate": z(E, I, H),
-                      "dw_up": z(E, I, H), "dw_down": z(E, H, I)})
+        if "dx" not in b and acc:
+            raise ValueError("accumulate_dw before a first backward: there is nothing to add to")
+        self._read_on(stream, dy, self.x, *self.w)
         with torch.cuda.device(dy.device):
+            if "dx" not in b:
+                z = lambda *sz, dt=torch.float32: torch.empty(*sz, dtype=dt, device=dy.device)  # noqa: E731
+                T, H, E, k, I = self.T, self.H, self.E, self.k, self.I
+                with torch.cuda.stream(stream):
+                    b.update({"dx": z(T, H, dt=torch.bfloat16), "d_topk_w": z(T, k), "d_logits": z(T, E),
+                              "dw_gate": z(E, I, H), "dw_up": z(E, I, H), "dw_down": z(E, H, I)})
             moe_gemm_down_dgrad_ckpt8(s, dy, b["row_token"], b["row_weight"], b["sorted_to_flat"], b["offsets"], w_down,
                                       b["gq"], b["g_scale"], b["uq"], b["u_scale"], c["dgu"], c["a_w"], b["d_topk_w"],
                                       c["ws"], stream=stream)
