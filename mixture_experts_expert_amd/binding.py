@@ -828,13 +828,16 @@ class Ckpt8Stage:
         for n, sz in sizes.items():
             if n not in self.scratch:
                 self.scratch[n] = e(*sz, dt=bf16)
-            elif tuple(self.scratch[n].shape) != sz or self.scratch[n].device != self.buf["y"].device:
-                raise ValueError(f"scratch {n} is {tuple(self.scratch[n].shape)} on {self.scratch[n].device}: "
-                                 f"stages that share it have the same sizes, here {sz}, and device")
+                continue
+            t = self.scratch[n]
+            if tuple(t.shape) != sz or t.dtype != bf16 or not t.is_contiguous() or t.device != self.buf["y"].device:
+                raise ValueError(f"scratch {n} is {tuple(t.shape)} in {t.dtype} on {t.device}: stages that share it have "
+                                 f"the same sizes, here {sz}, contiguous in {bf16}, and device")
         if "ws" not in self.scratch:
             self.scratch["ws"] = e(ws_bytes, dt=torch.uint8)
-        elif self.scratch["ws"].numel() < ws_bytes or self.scratch["ws"].device != self.buf["y"].device:
-            raise ValueError("scratch ws is of another shape's size or on another device")
+        ws = self.scratch["ws"]
+        if ws.numel() < ws_bytes or ws.dtype != torch.uint8 or not ws.is_contiguous() or ws.device != self.buf["y"].device:
+            raise ValueError("scratch ws is not bytes, contiguous, of this shape's size, or on another device")
         self.x = None
 
     def kept_bytes(self) -> int:
@@ -847,6 +850,8 @@ class Ckpt8Stage:
             dt = dt[0] if dt else torch.bfloat16
             if tuple(t.shape) != sizes or t.dtype != dt or not t.is_contiguous():
                 raise ValueError(f"{name} has to be {list(sizes)} in {dt}, contiguous")
+            if t.data_ptr() % 16 != 0:
+                raise ValueError(f"{name} has to start at a multiple of 16 bytes")
         for name, t, *_ in named:
             if t.device != self.buf["y"].device or t.device.type != "cuda":
                 raise ValueError(f"{name} is on {t.device}, the stage on {self.buf['y'].device}; both have to be on one GPU")

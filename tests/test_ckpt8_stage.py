@@ -62,3 +62,28 @@ def test_nothing_is_recorded_on_the_current_stream(calls):
     st.forward(x, *w)
     st.backward(dy)
     assert recorded == []
+
+
+def test_scratch_of_other_types_is_refused():
+    """A shared buffer of fewer bytes would be written past its end."""
+    from mixture_experts_expert_amd import binding as B
+    dims, scratch = (8, 128, 4, 2, 64), {}
+    B.Ckpt8Stage(*dims, device="cpu", x8=True, scratch=scratch)
+    B.Ckpt8Stage(*dims, device="cpu", x8=True, scratch=scratch)
+    for n, t in scratch.items():
+        for bad in (t.to(torch.int8 if t.dtype == BF else BF), torch.stack((t, t), -1)[..., 0]):
+            with pytest.raises(ValueError, match=f"scratch {n}"):
+                B.Ckpt8Stage(*dims, device="cpu", x8=True, scratch={**scratch, n: bad})
+
+
+def test_tensors_off_a_16_byte_boundary_are_refused_before_any_launch():
+    from mixture_experts_expert_amd import binding as B
+    st = B.Ckpt8Stage(8, 128, 4, 2, 64, device="cpu")
+    x, w, dy = _inputs()
+    good = dict(zip(("x", "w_router", "w_gate", "w_up", "w_down", "logit_bias"), (x, *w)))
+    for name, t in good.items():
+        off = torch.cat((t.flatten()[:1], t.flatten()))[1:].view(t.shape)
+        with pytest.raises(ValueError, match=f"{name} has to start"):
+            st.forward(**{**good, name: off})
+    with pytest.raises(ValueError, match="dy has to start"):
+        st.backward(torch.cat((dy.flatten()[:1], dy.flatten()))[1:].view(dy.shape))
