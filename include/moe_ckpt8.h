@@ -74,7 +74,8 @@ moe_status moe_gemm_down_dgrad_ckpt8(moe_shape s, const void* dy, const int32_t*
 
 /* The weight-gradient half of moe_gemm_down_bwd_dy on its own:
  *   dW_down[e] = sum over p of dy[row_token[p]]^T a_w[p]   (f32 [E,H,I]; += if accumulate_dw)
- * The same limits and workspace (moe_workspace_bytes). */
+ * bf16 only, T*H*2 and 4*(T*k+256) below 2^31 (MOE_EUNSUPPORTED otherwise); ws of
+ * ws_bytes >= moe_workspace_bytes(s). */
 moe_status moe_gemm_down_wgrad_dy(moe_shape s, const void* dy, const int32_t* row_token, const void* a_w,
                                   const int32_t* offsets, float* dw_down, int accumulate_dw, void* ws, size_t ws_bytes,
                                   hipStream_t stream);

@@ -613,7 +613,9 @@ moe_status moe_gemm_gate_up_ckpt8(moe_shape s, const void* x_rows, const int32_t
   return from_hip(moe::launch_gate_up_ckpt8(s, g, stream));
 }
 
-size_t moe_ckpt8_workspace_bytes(moe_shape s) { return check_ckpt8_shape(s) != MOE_OK ? 0 : ckpt8_dots_bytes(s); }
+size_t moe_ckpt8_workspace_bytes(moe_shape s) {
+  return check_ckpt8_shape(s) != MOE_OK || !ckpt8_tile_fits(s) ? 0 : ckpt8_dots_bytes(s);
+}
 
 moe_status moe_gemm_down_dgrad_ckpt8(moe_shape s, const void* dy, const int32_t* row_token, const float* row_weight,
                                      const int32_t* sorted_to_flat, const int32_t* offsets, const void* w_down,

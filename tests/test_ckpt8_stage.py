@@ -87,3 +87,13 @@ def test_tensors_off_a_16_byte_boundary_are_refused_before_any_launch():
             st.forward(**{**good, name: off})
     with pytest.raises(ValueError, match="dy has to start"):
         st.backward(torch.cat((dy.flatten()[:1], dy.flatten()))[1:].view(dy.shape))
+
+
+@pytest.mark.parametrize("H, I", [(1 << 15, 1 << 15), (64, 1 << 22), (1 << 22, 64)])
+def test_no_workspace_for_a_shape_that_the_call_rejects(H, I):
+    """One expert's weight, or 256 rows of g, past 2 GiB."""
+    from mixture_experts_expert_amd import binding as B
+    s = B.shape(1, H, 1, 1, I, BF)
+    assert B.moe_workspace_bytes(s) > 0 and B.moe_ckpt8_workspace_bytes(s) == 0
+    with pytest.raises(B.MoEError):
+        B.Ckpt8Stage(1, H, 1, 1, I, device="meta")
