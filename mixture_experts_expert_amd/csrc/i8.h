@@ -64,11 +64,13 @@ __device__ __forceinline__ uint2 codes8(const uint4& v, const CodeFactor& f) {
 // The same for a block of fp32 sums whose largest magnitude is m (NaN if one is).
 // The hardware's reciprocal is off by about 1 ulp, which moves a value's code only
 // if it is that close to a border: the code is off by less than 0.5 + 2^-15 still.
+// It does not return subnormal numbers, which from 2^126 on its result would be:
+// blocks above 2^64 are brought down by 2^64, as those below 2^-64 are lifted.
 struct SumFactor {
   float up, r, scale;
   __device__ __forceinline__ explicit SumFactor(float m) {
     const bool finite = m < __builtin_inff();
-    up = m < 0x1p-64f ? 0x1p64f : 1.0f;
+    up = m < 0x1p-64f ? 0x1p64f : m > 0x1p64f ? 0x1p-64f : 1.0f;
     r = finite && m > 0.0f ? 127.0f * __builtin_amdgcn_rcpf(m * up) : 0.0f;
     scale = finite ? m * (1.0f / 127.0f) : __builtin_nanf("");
   }
