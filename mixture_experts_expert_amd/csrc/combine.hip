@@ -73,22 +73,22 @@ __device__ __forceinline__ float slot_bcast(float v, int jj) {
 
 // y[t] = sum_j w[t,j] * o_perm[f2s[t*k+j]]   (WEIGHTED)   or   sum_j src[f2s[t*k+j]]
 // fp32 sums in ascending j, one rounding to T at the end.
-// SPLIT: a token's columns in runs of `band` chunks, one per workgroup along y (few tokens).
+// SPLIT: a token's columns one band of 64 chunks per workgroup along y (few tokens).
 template <class T, bool WEIGHTED, bool SPLIT = false>
 __global__ __launch_bounds__(kThreads) void gather_sum_kernel(int Tn, int k, int chunks,
                                                               const uint4* __restrict__ src,
                                                               const float* __restrict__ w,
                                                               const int32_t* __restrict__ f2s,
-                                                              uint4* __restrict__ out, int band = 0) {
-  constexpr int N = Vec<T>::N;
-  const int c0 = SPLIT ? static_cast<int>(blockIdx.y) * band : 0, c1 = SPLIT ? min(chunks, c0 + band) : chunks;
+                                                              uint4* __restrict__ out) {
+  constexpr int N = Vec<T>::N, BANDS = SPLIT ? 1 : 2;
+  const int c0 = SPLIT ? static_cast<int>(blockIdx.y) * kWave : 0, c1 = SPLIT ? min(chunks, c0 + kWave) : chunks;
   const int lane = threadIdx.x % kWave;
   const int t = __builtin_amdgcn_readfirstlane(blockIdx.x * kWavesPerBlock + static_cast<int>(threadIdx.x) / kWave);
   if (t >= Tn) return;
   const int64_t tk = static_cast<int64_t>(t) * k;
   if (k <= kBatch) {
     // One batch of slots: the row indices once, then two bands of 64 chunks
-    // (16 row chunks) in flight together. A second band past the row repeats
+    // (16 row chunks; one if there is no more) in flight together. A second band past the row repeats
     // the first band's chunk and stores the same bytes there again (no branch
     // for the loads to sink into).
     int idx;
@@ -101,17 +101,17 @@ __global__ __launch_bounds__(kThreads) void gather_sum_kernel(int Tn, int k, int
       row[jj] = static_cast<int64_t>(slot_bcast(idx, jj)) * chunks;
       wj[jj] = slot_bcast(wt, jj);
     }
-    for (int c = c0 + lane; c < c1; c += 2 * kWave) {
+    for (int c = c0 + lane; c < c1; c += BANDS * kWave) {
       const bool second = c + kWave < c1;
       const int c2 = second ? c + kWave : c;
-      uint4 v[2][kBatch];
+      uint4 v[BANDS][kBatch];
 #pragma unroll
       for (int jj = 0; jj < kBatch; ++jj) {
         v[0][jj] = src[row[jj] + c];
-        v[1][jj] = src[row[jj] + c2];
+        if constexpr (BANDS > 1) v[1][jj] = src[row[jj] + c2];
       }
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < BANDS; ++b) {
         float acc[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) acc[i] = 0.0f;
@@ -243,12 +243,14 @@ hipError_t launch_unpermute_sum(const moe_shape& s, const void* dx_perm, const i
 }
 
 hipError_t launch_sum_shared8(const moe_shape& s, const void* o_perm, const int32_t* f2s, void* y, hipStream_t st) {
-  // Few tokens: their columns over several workgroups, 64 chunks each, until
-  // there are two workgroups per CU (192 tokens of 2048: 10.7 -> 7.0 us).
+  // Up to 2044 tokens (two workgroups per CU): their columns over several
+  // workgroups, 64 chunks each. us, k = 8, rows whole | split: 2048 columns of 192
+  // tokens 9.8 | 4.0, 800 11.9 | 9.2, 2040 17.6 | 15.5; 4096 columns 18.3 | 5.9,
+  // 19.8 | 13.4, 37.4 | 34.4.
   const int chunks = s.H / 8, blocks = ceil_div(s.T, kWavesPerBlock);
   if (blocks < 512 && chunks > kWave) {
     gather_sum_kernel<shared8_t, false, true><<<dim3(blocks, ceil_div(chunks, kWave)), kThreads, 0, st>>>(
-        s.T, s.k, chunks, static_cast<const uint4*>(o_perm), nullptr, f2s, static_cast<uint4*>(y), kWave);
+        s.T, s.k, chunks, static_cast<const uint4*>(o_perm), nullptr, f2s, static_cast<uint4*>(y));
     return hipGetLastError();
   }
   return gather_sum<shared8_t, false>(s, o_perm, nullptr, f2s, y, st);

@@ -73,3 +73,11 @@ def test_the_reading_itself():
     assert unwaited([load, "  s_waitcnt vmcnt(0)", store, store]) == []
     assert unwaited([load, "  s_waitcnt vmcnt(0)", store, load, store]) == [store.strip()]
     assert unwaited(["  buffer_load_dwordx4 v[0:3], v1, s[0:3], 0 offen", store]) == []
+
+
+def test_sum_over_split_columns_loads_each_chunk_once(code):
+    """Its instance for few tokens has one band of chunks a workgroup: eight loads where the slots fit one batch, eight
+    in the loop over batches. (Not about waits; it is read from the same listing.)"""
+    (name, lines), = [(k, v) for k, v in kernels(code, "gather_sum_kernel").items() if "shared8" in k and "Lb1E" in k]
+    assert sum("global_load_dwordx4" in l for l in lines) == 16, name
+    assert sum("global_store_dwordx4" in l for l in lines) == 2, name
