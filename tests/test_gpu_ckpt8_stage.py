@@ -72,3 +72,19 @@ def test_first_gradients_keep_off_freed_memory():
     assert all(t.eq(8).all() for t in kept)
     for n in GRADS:
         assert torch.equal(st.buf[n], ref.buf[n]), n
+
+
+@pytest.mark.parametrize("T, E, I", [(500, 16, 320), (700, 4, 320), (4096, 16, 768)])
+def test_activations_are_the_plain_steps_at_full_depth(T, E, I):
+    """a, before anything rounds it away further, beside MoEStage's at H = 2048: by 128-row tiles (62 rows per expert on
+    average) and by 256-row ones."""
+    H, k = 2048, 2
+    g = torch.Generator("cuda").manual_seed(T)
+    r = lambda *d: torch.randn(*d, generator=g, device="cuda")
+    x, wr = r(T, H).to(BF), (0.1 * r(E, H)).to(BF)
+    w = [(r(E, n, m) * m**-0.5).to(BF) for n, m in ((I, H), (I, H), (H, I))]
+    st = B.Ckpt8Stage(T, H, E, k, I)
+    plain = B.MoEStage(T, H, E, k, I, BF, gather_fused=True, dy_fused=True)
+    y, want = st.forward(x, wr, *w), plain.forward(x, wr, *w)
+    assert torch.equal(st.scratch["a"], plain.buf["a"])
+    assert torch.equal(y, want)
