@@ -57,6 +57,7 @@ size_t moe_i8_workspace_bytes(moe_shape s);
  *   v = silu(g) * u,  g = deq(xq[row_token[p]]) deq(Wg[e])^T, u likewise,
  *   aq [T*k,I], a_scale [T*k]: v's codes. In between v is held in 24 bits of its
  *   largest magnitude in 128 columns.
+ * offsets and rows outside the experts' as moe_gemm_fp8_block.
  * xq [T,H], x_scale [T]; wq_gate, wq_up [E,I,H] with scales [E,I]. The shape
  * limits of moe_gemm_gate_up_fp8_block, and H and I below 2^17, T k I below 2^35
  * - 2048 (MOE_EUNSUPPORTED otherwise). ws of ws_bytes >= moe_i8_workspace_bytes(s),

@@ -276,7 +276,7 @@ moe_status moe_gemm_gate_up_i8(moe_shape s, const int8_t* xq, const float* x_sca
   g.amax = reinterpret_cast<float*>(static_cast<char*>(ws) + l.amax);
   const moe_status done = from_hip(moe::launch_gemm_i8(g, stream));
   if (done != MOE_OK) return done;
-  return from_hip(moe::launch_requantize_i8_rows(g.M, s.I, g.v16, g.v8, g.amax, aq, a_scale, stream));
+  return from_hip(moe::launch_requantize_i8_rows(g.M, s.I, s.E, offsets, g.v16, g.v8, g.amax, aq, a_scale, stream));
 }
 
 moe_status moe_experts_i8(moe_shape s, const void* x, const int32_t* topk_idx, const float* topk_w,

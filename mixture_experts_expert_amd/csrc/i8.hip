@@ -99,8 +99,9 @@ __global__ __launch_bounds__(kThreads) void dequantize_ckpt8_kernel(uint32_t blo
 }
 
 // Rows of 24-bit codes with a maximum per 128 columns (amax, NT per row) -> 8-bit
-// codes with a scale per row.
-__global__ __launch_bounds__(kThreads) void requantize_rows_kernel(uint32_t total, uint32_t chunks, int NT,
+// codes with a scale per row, for the rows that some expert has.
+__global__ __launch_bounds__(kThreads) void requantize_rows_kernel(uint32_t total, uint32_t chunks, int NT, int E,
+                                                                   const int32_t* __restrict__ offsets,
                                                                    const uint4* __restrict__ v16,
                                                                    const uint2* __restrict__ v8,
                                                                    const float* __restrict__ amax,
@@ -108,6 +109,7 @@ __global__ __launch_bounds__(kThreads) void requantize_rows_kernel(uint32_t tota
   const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
   if (i >= total) return;
   const uint32_t row = i / chunks, c = i - row * chunks;
+  if (row < static_cast<uint32_t>(offsets[0]) || row >= static_cast<uint32_t>(offsets[E])) return;
   const float* a = amax + static_cast<int64_t>(row) * NT;
   const uint4 v = v16[i];
   const uint2 lo = v8[i];
@@ -161,11 +163,12 @@ hipError_t launch_dequantize_ckpt8(int rows, int K, const int8_t* q, const float
   return hipGetLastError();
 }
 
-hipError_t launch_requantize_i8_rows(int rows, int K, const void* v16, const void* v8, const float* amax, int8_t* q,
-                                     float* scale, hipStream_t st) {
+hipError_t launch_requantize_i8_rows(int rows, int K, int E, const int32_t* offsets, const void* v16, const void* v8,
+                                     const float* amax, int8_t* q, float* scale, hipStream_t st) {
   const uint32_t chunks = static_cast<uint32_t>(K / 8), total = static_cast<uint32_t>(rows) * chunks;
   requantize_rows_kernel<<<(total + kThreads - 1) / kThreads, kThreads, 0, st>>>(
-      total, chunks, ceil_div(K, 128), static_cast<const uint4*>(v16), static_cast<const uint2*>(v8), amax, reinterpret_cast<uint2*>(q), scale);
+      total, chunks, ceil_div(K, 128), E, offsets, static_cast<const uint4*>(v16), static_cast<const uint2*>(v8), amax,
+      reinterpret_cast<uint2*>(q), scale);
   return hipGetLastError();
 }
 

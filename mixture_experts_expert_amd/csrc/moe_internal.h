@@ -295,15 +295,15 @@ struct BlockGemmArgs {
 hipError_t launch_gemm_fp8_block(const BlockGemmArgs& a, hipStream_t st);
 
 // 8-bit integer codes (i8.hip): scale = amax / 127 per row, or per kCkptBlock
-// columns (and back); rows of 24-bit codes with a maximum per 128 columns to
-// 8-bit codes with a scale per row.
+// columns (and back); rows [offsets[0], offsets[E]) of 24-bit codes with a maximum
+// per 128 columns to 8-bit codes with a scale per row.
 constexpr int kCkptBlock = 64;
 constexpr float kFull24 = 8388600.0f;  // the largest 24-bit code; a few below 2^23, which its roundings may not reach
 hipError_t launch_quantize_i8_rows(int rows, int K, const void* in, int8_t* q, float* scale, hipStream_t st);
 hipError_t launch_quantize_ckpt8(int rows, int K, const void* in, int8_t* q, float* scale, hipStream_t st);
 hipError_t launch_dequantize_ckpt8(int rows, int K, const int8_t* q, const float* scale, void* out, hipStream_t st);
-hipError_t launch_requantize_i8_rows(int rows, int K, const void* v16, const void* v8, const float* amax, int8_t* q,
-                                     float* scale, hipStream_t st);
+hipError_t launch_requantize_i8_rows(int rows, int K, int E, const int32_t* offsets, const void* v16, const void* v8,
+                                     const float* amax, int8_t* q, float* scale, hipStream_t st);
 
 // Grouped products of 8-bit integer operands with a scale per row of each
 // (gemm_i8.hip). Plain: out [M][N] = bf16(row_weight (a w0^T)). Gate/up (w1 set):
