@@ -50,7 +50,8 @@ moe_status moe_dequantize_ckpt8(int32_t rows, int32_t K, const int8_t* q, const 
  * bits: gq, uq [T*k,I] and g_scale, u_scale [T*k,I/64], from the fp32 sums; a
  * [T*k,I] as there. bf16 only, I*H*2 < 2^31, H and I below 2^22
  * (MOE_EUNSUPPORTED otherwise); the limits of moe_gemm_gate_up_gathered with
- * row_token. */
+ * row_token. Results of rows outside [offsets[0], offsets[E]) are not written, here
+ * and below. */
 moe_status moe_gemm_gate_up_ckpt8(moe_shape s, const void* x_rows, const int32_t* row_token, const int32_t* offsets,
                                   const void* w_gate, const void* w_up, int8_t* gq, float* g_scale, int8_t* uq,
                                   float* u_scale, void* a, hipStream_t stream);

@@ -226,12 +226,13 @@ MOE_DUO_KERNEL void gate_up_ckpt8_kernel(const CkptParams P) {
 
 MOE_DUO_KERNEL void down_dgrad_ckpt8_kernel(const CkptParams P) { duo::run<DownGradOp>(P); }
 
-// d_topk_w of each (token, slot): its row's dots in column order.
-__global__ __launch_bounds__(256) void ckpt8_dots_kernel(int M, int n, const float* __restrict__ dot,
+// d_topk_w of each (token, slot) whose row some expert has: its row's dots in column order.
+__global__ __launch_bounds__(256) void ckpt8_dots_kernel(int M, int n, int E, const int32_t* __restrict__ offsets,
+                                                         const float* __restrict__ dot,
                                                          const int32_t* __restrict__ sorted_to_flat,
                                                          float* __restrict__ out) {
   const int p = blockIdx.x * 256 + threadIdx.x;
-  if (p >= M) return;
+  if (p >= M || p < offsets[0] || p >= offsets[E]) return;
   float v = 0.0f;
   for (int i = 0; i < n; ++i) v += dot[static_cast<int64_t>(p) * n + i];
   out[sorted_to_flat[p]] = v;
@@ -295,8 +296,8 @@ hipError_t launch_down_dgrad_ckpt8(const moe_shape& s, const Ckpt8Args& a, hipSt
   const hipError_t err = hipGetLastError();
   if (err != hipSuccess) return err;
   const int M = s.T * s.k;
-  ckpt8_dots_kernel<<<static_cast<unsigned>(ceil_div64(M, 256)), 256, 0, st>>>(M, ceil_div(s.I, 128), a.dot,
-                                                                               a.sorted_to_flat, a.d_topk_w);
+  ckpt8_dots_kernel<<<static_cast<unsigned>(ceil_div64(M, 256)), 256, 0, st>>>(
+      M, ceil_div(s.I, 128), s.E, a.offsets, a.dot, a.sorted_to_flat, a.d_topk_w);
   return hipGetLastError();
 }
 
