@@ -108,8 +108,8 @@ __global__ __launch_bounds__(kThreads) void requantize_rows_kernel(uint32_t tota
                                                                    uint2* __restrict__ q, float* __restrict__ scale) {
   const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
   if (i >= total) return;
+  const uint32_t first = static_cast<uint32_t>(offsets[0]), rows = static_cast<uint32_t>(offsets[E]) - first;
   const uint32_t row = i / chunks, c = i - row * chunks;
-  if (row < static_cast<uint32_t>(offsets[0]) || row >= static_cast<uint32_t>(offsets[E])) return;
   const float* a = amax + static_cast<int64_t>(row) * NT;
   const uint4 v = v16[i];
   const uint2 lo = v8[i];
@@ -127,6 +127,7 @@ __global__ __launch_bounds__(kThreads) void requantize_rows_kernel(uint32_t tota
     k[2 * j] = code_bits(static_cast<float>(even) * f);
     k[2 * j + 1] = code_bits(static_cast<float>(odd) * f);
   }
+  if (row - first >= rows) return;  // asked last: the loads do not wait for it
   q[i] = make_uint2(bytes4(k[0], k[1], k[2], k[3]), bytes4(k[4], k[5], k[6], k[7]));
   if (c == 0) scale[row] = finite ? m / 127.0f : __builtin_nanf("");
 }
