@@ -89,7 +89,10 @@ moe_status moe_forward_fused_i8(moe_shape s, const void* x, const void* w_router
 /* moe_forward_few on 8-bit integer weights (moe_quantize_i8_rows): codes convert
  * to bf16 exactly, the activations stay in bf16 (not quantised, unlike
  * moe_forward_fused_i8, to which it is close within their rounding), and a
- * channel's scale multiplies its finished fp32 sum. Limits, outputs and
+ * channel's scale multiplies its finished fp32 sum. a between gate/up and down is
+ * rounded to bf16, as there: y is off by 0.0024 in the norm, where moe_experts_i8,
+ * whose a is in 24 bits before its codes, is off by 0.0017 (bf16 y alone: 0.0016),
+ * each against its own definition. Limits, outputs and
  * workspace (moe_few_workspace_bytes) as there; scales [E,I], [E,I] and [E,H], at
  * multiples of 16 bytes. */
 moe_status moe_forward_few_i8(moe_shape s, const void* x, const void* w_router, const float* logit_bias,

@@ -265,9 +265,11 @@ CkptParams params(const moe_shape& s, const Ckpt8Args& a) {
 
 // From 256 rows per expert on 256-row tiles read the weights half as often and need
 // less LDS per product; below them they stand half empty. Gate/up of 128 experts,
-// 2048 x 768, top-8, us (256-row tiles | 128-row): 512 tokens 162 | 156, 2048 tokens
-// 226 | 194, 4096 tokens 260 | 286, 8192 tokens 472 | 494; 8 experts, 8192 rows each
-// 393 | 424. The data gradient has more to do in its epilogue, and the 128-row tiles'
+// 2048 x 768, top-8, us (256-row tiles | 128-row), the same rows for each: 512 tokens
+// 164 | 158, 2048 tokens 217 | 198, 4096 tokens 248 | 269, 8192 tokens 450 | 470; 8
+// experts, 8192 rows each 391 | 413. With rows spread as a random choice spreads
+// them, 128 on average pass 128 as often as not: 2048 tokens 232 | 249, 1024 tokens
+// 191 | 183. The data gradient has more to do in its epilogue, and the 128-row tiles'
 // runs under the other workgroup's products: 97 | 96, 145 | 139, 203 | 176,
 // 291 | 308 (343 | 337 where experts have 512 rows on average, not each), 249 | 269.
 hipError_t launch_gate_up_ckpt8(const moe_shape& s, const Ckpt8Args& a, hipStream_t st) {

@@ -32,7 +32,7 @@
 // codes once all maxima are there. With 16 bits one code in 500 falls on the
 // other side of its border, and since a code's step is large beside most of a
 // row's values (silu(g) u has long tails) that is y's error 0.0026 instead of
-// 0.0019 (192 tokens, 30B shape); bf16 in between would move a tenth of them.
+// 0.0017 (192 tokens, 30B shape; bf16 y alone is 0.0016); bf16 in between would move a tenth of them.
 #include <type_traits>
 
 #include "duo.h"
@@ -756,17 +756,17 @@ __global__ __launch_bounds__(kThreads, 2) void i8_stream_kernel(const Params P, 
 // Which kernel, in us:
 //   Few rows: the weights are read once whatever the tile, so what counts is how
 //   early their loads leave. stream | duo, one expert with N = K = 4096: 32 rows
-//   9.0 | 27.9, 64 12.7 | 28.7, 128 21.3 | 33.3, 192 29.7 | 33.0, 256 38.0 | 33.2.
+//   8.4 | 26.4, 64 12.3 | 27.8, 128 20.9 | 31.1, 192 29.4 | 30.6, 256 37.8 | 31.2.
 //   Several experts: the stream kernel takes an expert's rows 32 at a time and
 //   reads its weights for each again, so that the longest expert sets the time.
-//   16 of 2048 x 2048 with 4 rows each 14.0 | 17.3; a whole stage of 128 experts
-//   (2048 x 768, top-8) of 65 tokens 125 | 135 evenly spread and 102 | 87 with
-//   their ranks' 1.2th powers, of 128 tokens 129 | 139 and 148 | 98. Four rows per
+//   16 of 2048 x 2048 with 4 rows each 13.6 | 16.6; a whole stage of 128 experts
+//   (2048 x 768, top-8) of 65 tokens 123 | 133 evenly spread and 99 | 84 with
+//   their ranks' 1.2th powers, of 128 tokens 127 | 137 and 142 | 95. Four rows per
 //   expert is where the loss from skew passes the gain.
 //   Many rows: 256-row tiles need full ones and enough of them for every CU.
-//   tile | duo, one expert with N = K = 4096: 1024 rows 52 | 34, 2048 54 | 40, 4096
-//   63 | 72, 8192 122 | 142; 128 experts, 2048 x 768, of 256 rows each 101 | 106, of
-//   512 160 | 183; 32 experts of 512 rows 53 | 52, of 1024 82 | 90. Gate/up and the
+//   tile | duo, one expert with N = K = 4096: 1024 rows 52 | 33, 2048 53 | 40, 4096
+//   60 | 70, 8192 118 | 141; 128 experts, 2048 x 768, of 256 rows each 89 | 96, of
+//   512 144 | 169; 32 experts of 512 rows 42 | 48, of 1024 73 | 89. Gate/up and the
 //   shared8 form have longer epilogues, which the second workgroup hides: 4096
 //   skewed tokens of the stage above 207 | 177 and 136 | 118 with the same LDS
 //   places in both.

@@ -1,4 +1,4 @@
-"""The 8-bit integer operators (include/moe_serve.h, include/moe.h) in 64 bits, on
+"""The 8-bit integer operators (include/moe_i8.h, include/moe_ckpt8.h) in 64 bits, on
 the CPU: codes with one scale per row or per 64 columns, the grouped product, the
 expert stage, and the backward of the down projection from kept activations."""
 import torch
